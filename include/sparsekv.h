@@ -11,6 +11,11 @@
  *   kv_dropped_mass        diagnostic: dense attention mass of the pages not selected
  *   kv_decode_step         the four per-step calls above in one call, on a workspace
  *
+ * and, for the prompts (and later tokens) that fill the cache:
+ *
+ *   kv_append_rope         packed new tokens: rotary position, cache write, page statistics
+ *   kv_prefill_attn        causal attention of packed query rows over the cache
+ *
  * Sources, by page title and section:
  *   [ENTMAX]  "EntmaxKV: Support-Aware Decoding for Entmax Attention", abstract: pages are
  *             scored against the query from cheap per-page statistics before any page is
@@ -35,7 +40,7 @@
  *     KV_ERR_MISALIGNED and launch nothing. A failed launch returns KV_ERR_CUDA.
  *   - Device-detected faults in the DATA (a page-table entry outside [0, num_phys_pages),
  *     a sequence longer than its page-table row, a selected index outside the sequence,
- *     a keep count above k_max, an asynchronous copy that did not land in time) never
+ *     packed-row offsets out of order, a keep count above k_max, an asynchronous copy that did not land in time) never
  *     trap: the kernel skips the bad access, records a flag in a per-device error word
  *     and finishes. kv_check_device_errors() reports and clears that word.
  *   - Supported shapes: head_dim 64 or 128; page_size 16, 32 or 64; group size
@@ -93,7 +98,8 @@ typedef enum kv_dtype { KV_BF16 = 0, KV_FP32 = 1 } kv_dtype;
 /* Device-side error flags (bit mask) behind kv_check_device_errors(). */
 enum {
   KV_DEVERR_BAD_PAGE = 1,    /* page-table entry outside [0, num_phys_pages) */
-  KV_DEVERR_BAD_LEN = 2,     /* seq_len < 0 or above page_table_stride * page_size */
+  KV_DEVERR_BAD_LEN = 2,     /* seq_len < 0 or above page_table_stride * page_size; packed
+                                offsets out of order or longer than their sequence */
   KV_DEVERR_BAD_SEL = 4,     /* selected index outside [0, n_pages) or sel_cnt > stride */
   KV_DEVERR_KEEP = 8,        /* keep count above k_max (clamped to k_max) */
   KV_DEVERR_TIMEOUT = 16     /* bounded wait on an asynchronous copy ran out */
@@ -172,6 +178,84 @@ kv_status kv_build_page_stats_fp8(const kv_cache_desc* cache, void* stats_fp8,
  */
 kv_status kv_append_token(const kv_cache_desc* cache, const void* k_new, const void* v_new,
                           void* stats, cudaStream_t stream);
+
+/*
+ * kv_rope_turns -- host, launches nothing: the rotation frequencies kv_append_rope takes.
+ * inv_freq: host, n angles in radians per position (pair j turns by pos * inv_freq[j]);
+ * turns: host, n fractions of a full turn per position in units of 2^-64 (modulo one turn),
+ * which the caller copies to the device once per model. KV_ERR_INVALID_ARG for n <= 0 or a
+ * value that is not finite.
+ */
+kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/*
+ * kv_append_rope -- the new tokens of a whole batch: prompts, chunks of prompts, or one token
+ * per sequence. Rotates queries and keys by their positions, writes keys and values into the
+ * cache and keeps the page statistics current: kv_append_token for many tokens, with the
+ * rotary position applied on the way.
+ *
+ * Packed rows: sequence b's n_b = cu_tokens[b+1] - cu_tokens[b] new tokens are rows
+ * cu_tokens[b] .. cu_tokens[b+1]-1 of q, k_new and v_new (cu_tokens: device int32[batch+1],
+ * starting at 0, not falling, at most total_tokens) and its last n_b positions: row i of them
+ * is position seq_lens[b] - n_b + i (seq_lens already counts them), in a page that page_table
+ * must map. With cu_tokens = NULL (total_tokens = batch) row b is sequence b's one new token;
+ * a sequence of length 0 has none.
+ * Rotation: for pair j < rot_dim/2 of a row's first rot_dim columns, columns
+ * (j, j + rot_dim/2), or (2j, 2j+1) when interleaved is not 0:
+ *   (a, b) -> (a cos x - b sin x, a sin x + b cos x),  x = pos * inv_freq[j],
+ * with pos the token's cache position, or positions[row] if positions is not NULL (device
+ * int32[total_tokens], any values); the angle is exact to 2^-32 of a turn at every position.
+ * Computed in float32, rounded once to the cache dtype. Columns from rot_dim on, and values,
+ * are copied. rot_dim: a multiple of 16 up to head_dim (else KV_ERR_UNSUPPORTED), 0 for no
+ * rotation (turns may then be NULL). turns: device uint64[rot_dim/2] of kv_rope_turns.
+ * Rotated queries go to q_out (which may be q itself with q's stride; any other overlap is not
+ * allowed), keys to k_pool and values to v_pool (written through the descriptor's pointers).
+ * Statistics of every page written: the element-wise min/max of the old ones (when the page
+ * held tokens of the sequence before) and the new keys as stored, equal to
+ * kv_build_page_stats of the grown cache.
+ * q [total_tokens][num_q_heads][head_dim], k_new, v_new [total_tokens][num_kv_heads][head_dim]
+ * in the cache dtype, head_dim innermost and contiguous, heads side by side, and *_stride
+ * elements from one token to the next (so the three may be column ranges of one fused
+ * projection): at least heads * head_dim, a multiple of 16 bytes; all bases 16-byte aligned
+ * (KV_ERR_MISALIGNED). A page that two sequences of the batch share must not be written by
+ * both. Rows that belong to no sequence are left alone. Bad offsets, a sequence shorter than
+ * its new tokens (KV_DEVERR_BAD_LEN: the sequence is left out) and an unmapped page
+ * (KV_DEVERR_BAD_PAGE: its keys and values are left out) are flagged on the device.
+ */
+kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                         int32_t num_q_heads, const void* k_new, int64_t k_stride,
+                         const void* v_new, int64_t v_stride, const int32_t* cu_tokens,
+                         int32_t total_tokens, const int32_t* positions, const uint64_t* turns,
+                         int32_t rot_dim, int32_t interleaved, void* q_out, int64_t q_out_stride,
+                         void* stats, cudaStream_t stream);
+
+/*
+ * kv_prefill_attn -- causal attention of packed query rows over the paged cache: a prompt, a
+ * chunk of one after the tokens already cached, drafted tokens to verify, or single tokens,
+ * in any mixture. Run it after kv_append_rope (the rows' own keys must be in the cache).
+ * Rows are packed as in kv_append_rope (cu_tokens, total_tokens, q_stride). Row i of sequence
+ * b, at position pos = seq_lens[b] - n_b + i, sees tokens 0 .. pos of its sequence:
+ *   x_t = sm_scale * q . k_t,  lse = log sum_t exp(x_t),  out = sum_t exp(x_t - lse) v_t.
+ * out: device [total_tokens][num_q_heads][head_dim] of the CACHE dtype (a prompt's rows feed
+ * the next matrix product), 16-byte aligned; lse: device [total_tokens][num_q_heads] float32
+ * (natural log) or NULL. Scores, softmax and sums are float32; for bf16 caches the
+ * probabilities are rounded to bf16 before they meet the values. Rows that belong to no
+ * sequence are left as they were; with cu_tokens = NULL the row of an empty sequence gets
+ * out = 0 and lse = -inf. Cached tokens must be finite; what lies in a page past its
+ * sequence's end has no influence. Results do not depend on timing (no atomics).
+ * num_splits: 0 chooses how many ways the keys of a row are split (1 when the rows alone fill
+ * the GPU); 1 .. 64 asks for that many. workspace: device, 256-byte aligned,
+ * kv_prefill_attn_workspace_size() bytes for the same arguments (0 when the keys are not
+ * split: workspace may then be NULL); it holds nothing between calls, and calls that overlap
+ * on the GPU need one each. Bad offsets and lengths are flagged on the device and the sequence
+ * left out; an unmapped page is flagged and not read, and its sequence's rows are unspecified.
+ */
+size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_heads,
+                                      int32_t total_tokens, int32_t num_splits);
+kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                          int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
+                          float sm_scale, int32_t num_splits, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * kv_score_pages -- [ENTMAX] query-aware page score, [SPARDA] summed over a GQA group.
@@ -564,14 +648,16 @@ kv_status kv_entmax_decode_step(const kv_cache_desc* cache, const void* q, int32
  * kv_dropped_mass_workspace_size(cache, num_q_heads); KV_OP_ENTMAX_DECODE_ATTN:
  * kv_entmax_attn_workspace_size(cache, num_q_heads, k_max as sel_stride, 0 = every page);
  * KV_OP_ENTMAX_DECODE_STEP: kv_entmax_decode_step_workspace_size(cache, num_q_heads,
- * k_max)). Arguments a given op does not use are ignored. Every other call of this library
+ * k_max); KV_OP_PREFILL_ATTN: kv_prefill_attn_workspace_size(cache, num_q_heads, k_max as
+ * total_tokens, num_splits)). Arguments a given op does not use are ignored. Every other call of this library
  * takes no workspace. Returns 0 for an unknown op or a bad argument.
  */
 typedef enum {
   KV_OP_DECODE_STEP = 0,
   KV_OP_DROPPED_MASS = 1,
   KV_OP_ENTMAX_DECODE_ATTN = 2,
-  KV_OP_ENTMAX_DECODE_STEP = 3
+  KV_OP_ENTMAX_DECODE_STEP = 3,
+  KV_OP_PREFILL_ATTN = 4
 } kv_op;
 size_t kv_workspace_size(int32_t op, const kv_cache_desc* cache, int32_t num_q_heads,
                          int32_t k_max, int32_t num_splits);

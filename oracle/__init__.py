@@ -76,7 +76,7 @@ from .kvattn import (
     dropped_mass,
 )
 from .parity import check_selection
-from . import entmax, fp8stats  # noqa: F401
+from . import entmax, fp8stats, prompt  # noqa: F401
 
 __all__ = [
     "num_pages",

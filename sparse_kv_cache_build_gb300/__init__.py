@@ -11,6 +11,7 @@ from .binding import (  # noqa: F401
     PLANS,
     DecodeStepGraph,
     PagedKV,
+    kv_append_rope,
     kv_append_token,
     kv_auto_num_splits,
     kv_build_page_stats,
@@ -29,6 +30,9 @@ from .binding import (  # noqa: F401
     kv_entmax_select,
     kv_dropped_mass_workspace_size,
     kv_merge_splits,
+    kv_prefill_attn,
+    kv_prefill_attn_workspace_size,
+    kv_rope_turns,
     kv_score_pages,
     kv_score_pages_fp8,
     kv_score_select,

@@ -45,6 +45,7 @@ EXPORTS = (
     "kv_entmax_attn_workspace_size", "kv_entmax_decode_attn",
     "kv_entmax_decode_step_workspace_size", "kv_entmax_decode_step", "kv_workspace_size",
     "kv_decode_step_graph_create", "kv_decode_step_graph_launch", "kv_decode_step_graph_destroy",
+    "kv_rope_turns", "kv_append_rope", "kv_prefill_attn_workspace_size", "kv_prefill_attn",
 )
 
 
@@ -77,6 +78,7 @@ _lib = None
 def _declare(lib):
     P, I32, F32, F64, SZ, U64 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_float,
                                  ctypes.c_double, ctypes.c_size_t, ctypes.c_uint64)
+    I64 = ctypes.c_int64
     D = ctypes.POINTER(KVCacheDesc)
     sig = {
         "kv_status_string": (ctypes.c_char_p, [I32]),
@@ -117,6 +119,11 @@ def _declare(lib):
         "kv_entmax_decode_attn": (I32, [D, P, I32, F32, P, P, I32, P, P, P, SZ, P]),
         "kv_entmax_decode_step_workspace_size": (SZ, [D, I32, I32]),
         "kv_entmax_decode_step": (I32, [D, P, I32, F32, P, I32, P, P, P, SZ, P]),
+        "kv_rope_turns": (I32, [P, I32, P]),
+        "kv_append_rope": (I32, [D, P, I64, I32, P, I64, P, I64, P, I32, P, P, I32, I32, P, I64,
+                                 P, P]),
+        "kv_prefill_attn_workspace_size": (SZ, [D, I32, I32, I32]),
+        "kv_prefill_attn": (I32, [D, P, I64, I32, P, I32, F32, I32, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -294,6 +301,110 @@ def kv_append_token(kv: PagedKV, k_new, v_new, stats, stream=None):
     _check("kv_append_token", lib().kv_append_token(kv.ref(), _ptr(k_new), _ptr(v_new),
                                                     _ptr(stats), _stream(stream)))
     return stats
+
+
+def _rows(kv: PagedKV, t, name, heads=None):
+    """Checks packed rows [T][heads][D] and returns their stride between tokens: the last two
+    dimensions are contiguous, tokens may lie apart (a column range of a fused projection)."""
+    if t.device != kv.k_pool.device:
+        raise ValueError(f"{name} must be on the cache's device {kv.k_pool.device}")
+    if t.dtype != kv.dtype:
+        raise ValueError(f"{name} must be {kv.dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != kv.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape [tokens][{heads or 'heads'}][{kv.head_dim}], "
+                         f"got {tuple(t.shape)}")
+    T, H, D = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must be contiguous within a token")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _on_device(kv: PagedKV, t, name, dtype, shape):
+    _need(t, name, dtype, shape)
+    if t.device != kv.k_pool.device:
+        raise ValueError(f"{name} must be on the cache's device {kv.k_pool.device}")
+
+
+def _packed(kv: PagedKV, q, cu_tokens):
+    if kv.k_pool.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {kv.k_pool.device}, which is not the current device")
+    if cu_tokens is not None:
+        _on_device(kv, cu_tokens, "cu_tokens", torch.int32, (kv.batch + 1,))
+    elif q.shape[0] != kv.batch:
+        raise ValueError("without cu_tokens there is one row per sequence")
+
+
+def kv_rope_turns(inv_freq, device=None):
+    """The rotation frequencies of kv_append_rope, laid out once per model: inv_freq (radians per
+    position and pair, any sequence of numbers) as int64 fractions of a turn on `device`."""
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if freq.dim() != 1:
+        raise ValueError("inv_freq must have one dimension")
+    turns = torch.empty(freq.shape, dtype=torch.int64)
+    _check("kv_rope_turns", lib().kv_rope_turns(_ptr(freq), freq.numel(), _ptr(turns)))
+    return turns.to(device) if device is not None else turns
+
+
+def kv_append_rope(kv: PagedKV, q, k_new, v_new, stats, turns=None, cu_tokens=None,
+                   positions=None, interleaved: bool = False, q_out=None, stream=None):
+    """Append packed new tokens [T][heads][D] (cu_tokens: int32 [B+1], or None for one token per
+    sequence), rotating queries and keys over the first 2 * len(turns) columns (turns=None: no
+    rotation); pools and stats are updated in place. Returns the rotated queries (q_out, which
+    may be q)."""
+    _packed(kv, q, cu_tokens)
+    T, Hq, D = q.shape
+    qs = _rows(kv, q, "q")
+    ks, vs = (_rows(kv, t, n, kv.num_kv_heads) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    if k_new.shape[0] != T or v_new.shape[0] != T:
+        raise ValueError("q, k_new and v_new must have the same number of rows")
+    _on_device(kv, stats, "stats", kv.dtype, (kv.k_pool.shape[0], kv.num_kv_heads, 2, D))
+    rot = 0
+    if turns is not None:
+        rot = 2 * turns.numel()
+        _on_device(kv, turns, "turns", torch.int64, (rot // 2,))
+    if positions is not None:
+        _on_device(kv, positions, "positions", torch.int32, (T,))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    os_ = _rows(kv, q_out, "q_out", Hq)
+    if q_out.shape[0] != T:
+        raise ValueError("q_out must have q's shape")
+    if T > 0:
+        _check("kv_append_rope", lib().kv_append_rope(
+            kv.ref(), _ptr(q), qs, Hq, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(cu_tokens), T,
+            _ptr(positions), _ptr(turns), rot, int(interleaved), _ptr(q_out), os_, _ptr(stats),
+            _stream(stream)))
+    return q_out
+
+
+def kv_prefill_attn_workspace_size(kv: PagedKV, num_q_heads: int, total_tokens: int,
+                                   num_splits: int = 0) -> int:
+    return int(lib().kv_prefill_attn_workspace_size(kv.ref(), int(num_q_heads),
+                                                    int(total_tokens), int(num_splits)))
+
+
+def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_splits: int = 0,
+                    out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of packed query rows [T][Hq][D] over the cache, which holds the rows'
+    own keys and values already: (out of the cache's dtype, lse float32)."""
+    _packed(kv, q, cu_tokens)
+    T, Hq, D = q.shape
+    qs = _rows(kv, q, "q")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    _on_device(kv, out, "out", kv.dtype, (T, Hq, D))
+    _on_device(kv, lse, "lse", torch.float32, (T, Hq))
+    if T == 0:
+        return out, lse
+    if workspace is None:
+        nbytes = kv_prefill_attn_workspace_size(kv, Hq, T, num_splits)
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+    _check("kv_prefill_attn", lib().kv_prefill_attn(
+        kv.ref(), _ptr(q), qs, Hq, _ptr(cu_tokens), T, float(sm_scale), int(num_splits),
+        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out, lse
 
 
 def kv_score_pages(kv: PagedKV, q, stats, scores=None, stream=None):
@@ -543,7 +654,8 @@ def kv_dropped_mass(kv: PagedKV, q, sm_scale: float, sel_idx, sel_cnt, delta=Non
     return delta
 
 
-KV_OP = {"decode_step": 0, "dropped_mass": 1, "entmax_decode_attn": 2, "entmax_decode_step": 3}
+KV_OP = {"decode_step": 0, "dropped_mass": 1, "entmax_decode_attn": 2, "entmax_decode_step": 3,
+         "prefill_attn": 4}
 
 
 def kv_workspace_size(op: str, kv: PagedKV, num_q_heads: int, k_max: int = 0,

@@ -12,6 +12,7 @@
 #include "attn_impl.cuh"
 #include "attn_mma.cuh"
 #include "kv_internal.cuh"
+#include "prefill.cuh"
 
 namespace skv {
 namespace {
@@ -201,6 +202,48 @@ bool score_select_fits(const kv_cache_desc* d, const DeviceState* st) {
   return score_select_smem(d->page_table_stride) + 16 * 1024 <= (size_t)st->smem_optin;
 }
 
+// Packed rows of `heads` heads: a row stride that holds them, 16-byte steps from a 16-byte
+// aligned base.
+kv_status check_rows(const kv_cache_desc* d, const void* p, int64_t stride, int heads) {
+  if (p == nullptr || stride < (int64_t)heads * d->head_dim) return KV_ERR_INVALID_ARG;
+  const int elem = d->dtype == KV_BF16 ? 2 : 4;
+  if (!aligned16(p) || stride % (16 / elem) != 0) return KV_ERR_MISALIGNED;
+  return KV_OK;
+}
+
+// Offsets and row count of a packed batch.
+kv_status check_packed(const kv_cache_desc* d, const int32_t* cu_tokens, int32_t total_tokens) {
+  if (total_tokens < 0 || (cu_tokens == nullptr && total_tokens != d->batch))
+    return KV_ERR_INVALID_ARG;
+  return KV_OK;
+}
+
+constexpr int kPrefillMaxSplits = 64;
+constexpr int kPrefillMinSplitKeys = 512;
+
+// Splits of the prompt attention: 1 when the row tiles alone fill the SMs, else as many as
+// still fit one wave, with at least kPrefillMinSplitKeys keys each at the table's capacity.
+int prefill_splits(const kv_cache_desc* d, int G, int total, int asked, const DeviceState* st) {
+  if (asked > 0) return asked;
+  const long tile = prefill_tile_tokens(d->dtype, G);
+  const long blocks = (total / tile + (total < d->batch ? total : d->batch)) * d->num_kv_heads;
+  long S = blocks > 0 ? st->sms / blocks : 1;
+  const long cap = (long)d->page_table_stride * d->page_size / kPrefillMinSplitKeys;
+  if (S > cap) S = cap;
+  if (S > kPrefillMaxSplits) S = kPrefillMaxSplits;
+  return S < 1 ? 1 : (int)S;
+}
+
+struct PrefillLayout { size_t acc, ml, total; };
+PrefillLayout prefill_layout(const kv_cache_desc* d, int Hq, int total, int S) {
+  PrefillLayout L{0, 0, 0};
+  if (S <= 1) return L;
+  const size_t rows = (size_t)total * Hq * S;
+  L.ml = round256(rows * d->head_dim * sizeof(float));
+  L.total = L.ml + round256(rows * 2 * sizeof(float));
+  return L;
+}
+
 __global__ void wait_selftest_kernel(unsigned long long limit_ns, DevCtx ctx) {
   __shared__ __align__(8) uint64_t bar;
   if (threadIdx.x == 0) {
@@ -287,6 +330,102 @@ kv_status kv_append_token(const kv_cache_desc* cache, const void* k_new, const v
   DevCtx ctx;
   if ((r = ctx_for_call(&ctx)) != KV_OK) return r;
   return from_cuda(launch_append(*cache, k_new, v_new, stats, ctx, stream));
+}
+
+kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
+  if (inv_freq == nullptr || turns == nullptr || n <= 0) return KV_ERR_INVALID_ARG;
+  for (int32_t j = 0; j < n; ++j) {
+    if (!isfinite(inv_freq[j])) return KV_ERR_INVALID_ARG;
+    const double t = inv_freq[j] / 6.283185307179586476925286766559;
+    const double frac = t - floor(t);                  // [0, 1]; 1 only by rounding
+    turns[j] = frac >= 1.0 ? 0 : (uint64_t)(frac * 18446744073709551616.0);
+  }
+  return KV_OK;
+}
+
+kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                         int32_t num_q_heads, const void* k_new, int64_t k_stride,
+                         const void* v_new, int64_t v_stride, const int32_t* cu_tokens,
+                         int32_t total_tokens, const int32_t* positions, const uint64_t* turns,
+                         int32_t rot_dim, int32_t interleaved, void* q_out, int64_t q_out_stride,
+                         void* stats, cudaStream_t stream) {
+  kv_status r = check_desc(cache);
+  if (r != KV_OK) return r;
+  if ((r = check_heads(cache, q, num_q_heads)) != KV_OK) return r;
+  if ((r = check_packed(cache, cu_tokens, total_tokens)) != KV_OK) return r;
+  if (rot_dim < 0 || rot_dim > cache->head_dim || (rot_dim > 0 && turns == nullptr) ||
+      stats == nullptr)
+    return KV_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return KV_ERR_UNSUPPORTED;
+  if ((r = check_rows(cache, q, q_stride, num_q_heads)) != KV_OK) return r;
+  if ((r = check_rows(cache, q_out, q_out_stride, num_q_heads)) != KV_OK) return r;
+  if ((r = check_rows(cache, k_new, k_stride, cache->num_kv_heads)) != KV_OK) return r;
+  if ((r = check_rows(cache, v_new, v_stride, cache->num_kv_heads)) != KV_OK) return r;
+  if (!aligned16(stats) || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0)
+    return KV_ERR_MISALIGNED;
+  if (work_numbers(cu_tokens, total_tokens, cache->batch, cache->page_size, 2) > INT32_MAX)
+    return KV_ERR_UNSUPPORTED;
+  if (total_tokens == 0) return KV_OK;
+  DevCtx ctx;
+  if ((r = ctx_for_call(&ctx)) != KV_OK) return r;
+  return from_cuda(launch_append_rope(*cache, cu_tokens, total_tokens, q, q_stride, num_q_heads,
+                                      k_new, k_stride, v_new, v_stride, positions, turns,
+                                      rot_dim, interleaved != 0, q_out, q_out_stride, stats, ctx,
+                                      stream));
+}
+
+size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_heads,
+                                      int32_t total_tokens, int32_t num_splits) {
+  if (check_desc(cache) != KV_OK || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 ||
+      total_tokens < 0 || num_splits < 0 || num_splits > kPrefillMaxSplits)
+    return 0;
+  const int G = num_q_heads / cache->num_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return 0;
+  DeviceState* st = nullptr;
+  if (num_splits == 0 && device_state(&st) != KV_OK) return 0;
+  const int S = prefill_splits(cache, G, total_tokens, num_splits, st);
+  return prefill_layout(cache, num_q_heads, total_tokens, S).total;
+}
+
+kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                          int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
+                          float sm_scale, int32_t num_splits, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  kv_status r = check_desc(cache);
+  if (r != KV_OK) return r;
+  if ((r = check_heads(cache, q, num_q_heads)) != KV_OK) return r;
+  if ((r = check_packed(cache, cu_tokens, total_tokens)) != KV_OK) return r;
+  if (out == nullptr || !(sm_scale > 0.f) || !isfinite(sm_scale) || num_splits < 0 ||
+      num_splits > kPrefillMaxSplits)
+    return KV_ERR_INVALID_ARG;
+  if ((r = check_rows(cache, q, q_stride, num_q_heads)) != KV_OK) return r;
+  if (!aligned16(out)) return KV_ERR_MISALIGNED;
+  const int G = num_q_heads / cache->num_kv_heads;
+  if (work_numbers(cu_tokens, total_tokens, cache->batch,
+                   prefill_tile_tokens(cache->dtype, G), 1) * cache->num_kv_heads > INT32_MAX)
+    return KV_ERR_UNSUPPORTED;
+  if (total_tokens == 0) return KV_OK;
+  DevCtx ctx;
+  DeviceState* st = nullptr;
+  if ((r = ctx_for_call(&ctx, &st)) != KV_OK) return r;
+  PrefillArgs a{};
+  a.S = prefill_splits(cache, G, total_tokens, num_splits, st);
+  const PrefillLayout L = prefill_layout(cache, num_q_heads, total_tokens, a.S);
+  if (L.total > 0) {
+    if (workspace == nullptr || workspace_bytes < L.total ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return KV_ERR_WORKSPACE;
+    a.part_acc = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.ml);
+  }
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.lse = lse;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.Hq = num_q_heads;
+  a.G = G;
+  return from_cuda(launch_prefill(*cache, cu_tokens, total_tokens, a, ctx, stream));
 }
 
 kv_status kv_score_pages(const kv_cache_desc* cache, const void* q, int32_t num_q_heads,
@@ -1066,6 +1205,8 @@ size_t kv_workspace_size(int32_t op, const kv_cache_desc* cache, int32_t num_q_h
       return kv_entmax_attn_workspace_size(cache, num_q_heads, k_max);
     case KV_OP_ENTMAX_DECODE_STEP:
       return kv_entmax_decode_step_workspace_size(cache, num_q_heads, k_max);
+    case KV_OP_PREFILL_ATTN:
+      return kv_prefill_attn_workspace_size(cache, num_q_heads, k_max, num_splits);
     default:
       return 0;
   }

@@ -1,0 +1,341 @@
+// Packed append with the rotary position applied on the way.
+//
+// A step's new tokens (whole prompts, chunks of prompts, or one token per sequence) arrive as
+// packed rows of queries, keys and values. Token i of sequence b's n_b goes to position
+// t = len_b - n_b + i. For each pair j of the first rot_dim columns
+//   (u, w) = (a cos x - b sin x, a sin x + b cos x),  x = pos * inv_freq_j,
+// with (a, b) = columns (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved. Queries go to
+// q_out, keys and values to their slots, and the min/max statistics of every page touched
+// follow from the stored keys alone, as kv_append_token keeps them for one token.
+//
+// Angles: the frequency is held in turns as a 64-bit fraction, so pos * turns modulo 2^64 is
+// the fraction of a turn exactly, however far the position; only its leading 32 bits become a
+// float, for sincospif. A product in 32-bit floats would be off by 2^-24 of the whole angle
+// (0.06 rad at position 10^6).
+//
+// Rounding: the rotation is done in float32 and rounded once to the cache's type; the
+// statistics are taken over the rounded keys, as a rebuild from the pool would.
+//
+// Bound: every row is read once and written once, so the floor is memory. A lane owns 16
+// columns of a row as two 16-byte (bf16) chunks that hold eight whole pairs, so no exchange
+// between lanes is needed and D/16 lanes cover a row; a warp moves 512/D rows at once. One
+// block per (page, KV head) lets the page's statistics be joined inside the block, without
+// atomics.
+#include "packed_rows.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kRopeThreads = 128;
+constexpr int kRopeWarps = kRopeThreads / 32;
+
+struct RopeArgs {
+  const void* q; const void* k; const void* v;      // packed rows
+  int64_t q_stride, k_stride, v_stride;             // elements between tokens
+  void* q_out; int64_t q_out_stride;
+  const int32_t* positions;                         // NULL: the cache position
+  const uint64_t* turns;                            // [rot_dim / 2]
+  void* stats;
+  int Hq, rot;
+};
+
+// Sixteen columns of a row as floats: two chunks of eight.
+struct Cols { float a[8], b[8]; };
+
+template <typename T> __device__ __forceinline__ void load8(const T* p, float* f);
+template <> __device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float* f) {
+  chunk_to_f32<bf16_t>(*reinterpret_cast<const uint4*>(p), f);
+}
+template <> __device__ __forceinline__ void load8<float>(const float* p, float* f) {
+  chunk_to_f32<float>(*reinterpret_cast<const uint4*>(p), f);
+  chunk_to_f32<float>(*reinterpret_cast<const uint4*>(p + 4), f + 4);
+}
+
+// Rounds to the storage type (to nearest even) and leaves the rounded values in f.
+template <typename T> __device__ __forceinline__ void store8(T* p, float* f);
+template <> __device__ __forceinline__ void store8<bf16_t>(bf16_t* p, float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <> __device__ __forceinline__ void store8<float>(float* p, float* f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// The two chunks of lane c of a row and, when they rotate, the first of their eight pairs.
+// Half-split pairs join chunk c with chunk c + rot/16; interleaved pairs lie inside chunks
+// 2c and 2c + 1; columns from rot on pass through.
+template <bool INTER>
+__device__ __forceinline__ void lane_chunks(int c, int rot, int* ca, int* cb, bool* turns) {
+  *turns = 16 * c < rot;
+  *ca = !INTER && *turns ? 8 * c : 16 * c;
+  *cb = !INTER && *turns ? 8 * c + rot / 2 : 16 * c + 8;
+}
+
+struct Angle { float cos[8], sin[8]; };
+
+__device__ __forceinline__ void angles_at(const uint64_t* f, int pos, Angle* x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint64_t turn = f[e] * (uint64_t)(int64_t)pos;      // modulo one turn
+    const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
+    sincospif(half_turns, &x->sin[e], &x->cos[e]);
+  }
+}
+
+template <bool INTER>
+__device__ __forceinline__ void rotate(Cols* r, const Angle& x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float& a = INTER ? (e < 4 ? r->a[2 * e] : r->b[2 * e - 8]) : r->a[e];
+    float& b = INTER ? (e < 4 ? r->a[2 * e + 1] : r->b[2 * e - 7]) : r->b[e];
+    const float u = a * x.cos[e] - b * x.sin[e];
+    const float w = a * x.sin[e] + b * x.cos[e];
+    a = u;
+    b = w;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void load_cols(const void* base, int64_t at, int ca, int cb, Cols* r) {
+  const T* p = static_cast<const T*>(base) + at;
+  load8<T>(p + ca, r->a);
+  load8<T>(p + cb, r->b);
+}
+template <typename T>
+__device__ __forceinline__ void store_cols(void* base, int64_t at, int ca, int cb, Cols* r) {
+  T* p = static_cast<T*>(base) + at;
+  store8<T>(p + ca, r->a);
+  store8<T>(p + cb, r->b);
+}
+
+template <typename T> __device__ __forceinline__ void store_stat(T* p, float v);
+template <> __device__ __forceinline__ void store_stat<bf16_t>(bf16_t* p, float v) {
+  p->bits = (uint16_t)(__float_as_uint(v) >> 16);             // exact: v is a bf16 value
+}
+template <> __device__ __forceinline__ void store_stat<float>(float* p, float v) { *p = v; }
+
+// Folds a key's extremes into a page's: a value replaces the old one only when strictly
+// smaller (larger), the rule of the full build.
+__device__ __forceinline__ float lower(float a, float b) { return b < a ? b : a; }
+__device__ __forceinline__ float upper(float a, float b) { return b > a ? b : a; }
+
+// ------------------------------------------------------------------------------------
+// Prompts and chunks: one block per (page touched, KV head).
+// ------------------------------------------------------------------------------------
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads)
+append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
+  constexpr int LPR = D / 16;            // lanes per row
+  constexpr int RPW = 32 / LPR;          // rows per warp step
+  __shared__ float sh_mn[kRopeWarps][D], sh_mx[kRopeWarps][D];
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_packed_rows(ctx, d, pr);
+  const int PS = d.page_size, Hkv = d.num_kv_heads, g = blockIdx.y;
+  int base;
+  const int b = find_sequence(pr, d.batch, PS, 2, blockIdx.x, &base);
+  const SeqRows sr = seq_rows(ctx, d, pr, b);
+  const int start = sr.len - sr.n;
+  const int page = start / PS + ((int)blockIdx.x - base);
+  if (sr.n == 0 || (int64_t)page * PS >= sr.len) return;
+  const int t0 = max(start, page * PS), t1 = min(sr.len - page * PS, PS) + page * PS;
+  const int P = d.page_table[(long)b * d.page_table_stride + page];
+  const bool mapped = P >= 0 && P < d.num_phys_pages;
+  if (!mapped && threadIdx.x == 0) flag(ctx, KV_DEVERR_BAD_PAGE);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane / LPR, c = lane % LPR;
+  int ca, cb;
+  bool turns;
+  lane_chunks<INTER>(c, a.rot, &ca, &cb, &turns);
+  uint64_t f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = turns ? a.turns[8 * c + e] : 0;
+  const int G = a.Hq / Hkv;
+  void* kp = const_cast<void*>(d.k_pool);
+  void* vp = const_cast<void*>(d.v_pool);
+
+  Cols mn, mx;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    mn.a[e] = mn.b[e] = INFINITY;
+    mx.a[e] = mx.b[e] = -INFINITY;
+  }
+  for (int t = t0 + warp * RPW + r; t < t1; t += kRopeWarps * RPW) {
+    const int64_t row = sr.row0 + (t - start);
+    Cols k, v;
+    load_cols<T>(a.k, row * a.k_stride + (int64_t)g * D, ca, cb, &k);
+    load_cols<T>(a.v, row * a.v_stride + (int64_t)g * D, ca, cb, &v);
+    Angle x;
+    if (turns) {
+      angles_at(f, a.positions != nullptr ? a.positions[row] : t, &x);
+      rotate<INTER>(&k, x);
+    }
+    if (mapped) {
+      const int64_t slot = (((int64_t)P * Hkv + g) * PS + (t - page * PS)) * D;
+      store_cols<T>(kp, slot, ca, cb, &k);
+      store_cols<T>(vp, slot, ca, cb, &v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mn.a[e] = lower(mn.a[e], k.a[e]);
+        mn.b[e] = lower(mn.b[e], k.b[e]);
+        mx.a[e] = upper(mx.a[e], k.a[e]);
+        mx.b[e] = upper(mx.b[e], k.b[e]);
+      }
+    }
+    for (int h = g * G; h < (g + 1) * G; ++h) {
+      Cols q;
+      load_cols<T>(a.q, row * a.q_stride + (int64_t)h * D, ca, cb, &q);
+      if (turns) rotate<INTER>(&q, x);
+      store_cols<T>(a.q_out, row * a.q_out_stride + (int64_t)h * D, ca, cb, &q);
+    }
+  }
+  if (!mapped) return;
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mn.a[e] = lower(mn.a[e], __shfl_xor_sync(0xffffffffu, mn.a[e], o));
+      mn.b[e] = lower(mn.b[e], __shfl_xor_sync(0xffffffffu, mn.b[e], o));
+      mx.a[e] = upper(mx.a[e], __shfl_xor_sync(0xffffffffu, mx.a[e], o));
+      mx.b[e] = upper(mx.b[e], __shfl_xor_sync(0xffffffffu, mx.b[e], o));
+    }
+  }
+  if (r == 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sh_mn[warp][ca + e] = mn.a[e];
+      sh_mn[warp][cb + e] = mn.b[e];
+      sh_mx[warp][ca + e] = mx.a[e];
+      sh_mx[warp][cb + e] = mx.b[e];
+    }
+  }
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i < D) {
+    T* row = static_cast<T*>(a.stats) + ((int64_t)P * Hkv + g) * 2 * D;
+    float lo = sh_mn[0][i], hi = sh_mx[0][i];
+#pragma unroll
+    for (int w = 1; w < kRopeWarps; ++w) {
+      lo = lower(lo, sh_mn[w][i]);
+      hi = upper(hi, sh_mx[w][i]);
+    }
+    if (t0 > page * PS) {                // the page held tokens before this call
+      lo = lower(load_elem<T>(row, i), lo);
+      hi = upper(load_elem<T>(row, D + i), hi);
+    }
+    store_stat<T>(row + i, lo);
+    store_stat<T>(row + D + i, hi);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// One token per sequence: D/16 lanes per row, every row of the token side by side, so a call
+// is one dependent chain (length, page, row) long.
+// ------------------------------------------------------------------------------------
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads)
+append_rope_single_kernel(kv_cache_desc d, RopeArgs a, DevCtx ctx) {
+  constexpr int LPR = D / 16;
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x, PS = d.page_size, Hkv = d.num_kv_heads;
+  const int task = blockIdx.y * (kRopeThreads / LPR) + threadIdx.x / LPR;
+  const int c = threadIdx.x % LPR;
+  if (task >= a.Hq + 2 * Hkv) return;
+  // tasks: the query heads, then the keys, then the values
+  const bool is_q = task < a.Hq, is_v = task >= a.Hq + Hkv;
+  const int head = is_q ? task : (task - a.Hq) % Hkv;
+  int ca, cb;
+  bool turns;
+  lane_chunks<INTER>(c, a.rot, &ca, &cb, &turns);
+  Cols x;
+  load_cols<T>(is_q ? a.q : is_v ? a.v : a.k,
+               b * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + (int64_t)head * D,
+               ca, cb, &x);
+  const int len = checked_len(ctx, d, b);
+  if (len == 0) return;                                    // nothing to append
+  if (turns && !is_v) {
+    uint64_t f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = a.turns[8 * c + e];
+    Angle y;
+    angles_at(f, a.positions != nullptr ? a.positions[b] : len - 1, &y);
+    rotate<INTER>(&x, y);
+  }
+  if (is_q) {
+    store_cols<T>(a.q_out, b * a.q_out_stride + (int64_t)head * D, ca, cb, &x);
+    return;
+  }
+  const int page = (len - 1) / PS, slot = (len - 1) % PS;
+  const int P = d.page_table[(long)b * d.page_table_stride + page];
+  if (P < 0 || P >= d.num_phys_pages) {
+    flag(ctx, KV_DEVERR_BAD_PAGE);
+    return;
+  }
+  store_cols<T>(const_cast<void*>(is_v ? d.v_pool : d.k_pool),
+                (((int64_t)P * Hkv + head) * PS + slot) * D, ca, cb, &x);
+  if (is_v) return;
+  const int64_t srow = ((int64_t)P * Hkv + head) * 2 * D;
+  Cols mn = x, mx = x;
+  if (slot > 0) {
+    load_cols<T>(a.stats, srow, ca, cb, &mn);
+    load_cols<T>(a.stats, srow + D, ca, cb, &mx);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mn.a[e] = lower(mn.a[e], x.a[e]);
+      mn.b[e] = lower(mn.b[e], x.b[e]);
+      mx.a[e] = upper(mx.a[e], x.a[e]);
+      mx.b[e] = upper(mx.b[e], x.b[e]);
+    }
+  }
+  store_cols<T>(a.stats, srow, ca, cb, &mn);
+  store_cols<T>(a.stats, srow + D, ca, cb, &mx);
+}
+
+template <typename T, int D, bool INTER>
+cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const RopeArgs& a, DevCtx ctx,
+                     cudaStream_t s) {
+  if (pr.cu == nullptr) {
+    const int rows = a.Hq + 2 * d.num_kv_heads;
+    dim3 grid(d.batch, ceil_div(rows, kRopeThreads / (D / 16)));
+    return launch_pdl(append_rope_single_kernel<T, D, INTER>, grid, dim3(kRopeThreads), 0, s, d,
+                      a, ctx);
+  }
+  dim3 grid((unsigned)work_numbers(pr.cu, pr.total, d.batch, d.page_size, 2), d.num_kv_heads);
+  return launch_pdl(append_rope_kernel<T, D, INTER>, grid, dim3(kRopeThreads), 0, s, d, pr, a,
+                    ctx);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const kv_cache_desc& d, const PackedRows& pr, const RopeArgs& a, bool inter,
+                     DevCtx ctx, cudaStream_t s) {
+  return inter ? launch_t<T, D, true>(d, pr, a, ctx, s) : launch_t<T, D, false>(d, pr, a, ctx, s);
+}
+
+}  // namespace
+
+cudaError_t launch_append_rope(const kv_cache_desc& d, const int32_t* cu, int total,
+                               const void* q, int64_t q_stride, int Hq, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride,
+                               const int32_t* positions, const uint64_t* turns, int rot,
+                               bool interleaved, void* q_out, int64_t q_out_stride, void* stats,
+                               DevCtx ctx, cudaStream_t s) {
+  const PackedRows pr{cu, total};
+  const RopeArgs a{q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, positions, turns,
+                   stats, Hq, rot};
+  if (d.dtype == KV_BF16)
+    return d.head_dim == 128 ? launch_d<bf16_t, 128>(d, pr, a, interleaved, ctx, s)
+                             : launch_d<bf16_t, 64>(d, pr, a, interleaved, ctx, s);
+  return d.head_dim == 128 ? launch_d<float, 128>(d, pr, a, interleaved, ctx, s)
+                           : launch_d<float, 64>(d, pr, a, interleaved, ctx, s);
+}
+
+}  // namespace skv

@@ -275,6 +275,14 @@ cudaError_t launch_dropped_mass(const kv_cache_desc& d, const void* q, int Hq,
 cudaError_t launch_wait_selftest(unsigned long long limit_ns, DevCtx ctx, cudaStream_t s);
 cudaError_t launch_append(const kv_cache_desc& d, const void* k_new, const void* v_new,
                           void* stats, DevCtx ctx, cudaStream_t s);
+// Packed append with rotation (append_rope.cu): cu NULL = one row per sequence; strides in
+// elements between tokens.
+cudaError_t launch_append_rope(const kv_cache_desc& d, const int32_t* cu, int total,
+                               const void* q, int64_t q_stride, int Hq, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride,
+                               const int32_t* positions, const uint64_t* turns, int rot,
+                               bool interleaved, void* q_out, int64_t q_out_stride, void* stats,
+                               DevCtx ctx, cudaStream_t s);
 
 // The single-launch decode step (bf16): cluster size for this shape on this device
 // (0 = use the four-kernel path), and its launcher.

@@ -1,0 +1,90 @@
+// Packed token rows: how the calls that take the new tokens of a whole batch find the sequence
+// a piece of work belongs to, on the device, from offsets the host never reads.
+//
+// The rows of sequence b are cu_tokens[b] .. cu_tokens[b+1]-1 (one row per sequence when
+// cu_tokens is NULL) and hold its last n_b tokens: row i of them is position len_b - n_b + i.
+#pragma once
+
+#include "kv_internal.cuh"
+
+namespace skv {
+
+struct PackedRows {
+  const int32_t* cu;    // [batch + 1], or NULL: row b is sequence b's one new token
+  int32_t total;        // rows in the packed tensors
+};
+
+// The new tokens of one sequence; n = 0 when there are none or the offsets are not usable.
+struct SeqRows {
+  int row0;   // first packed row
+  int n;      // rows
+  int len;    // sequence length, the new tokens included
+};
+
+// Offsets must rise from 0 and stay inside [0, total], and a sequence holds at least its new
+// tokens; anything else is flagged and the sequence is left out.
+__device__ __forceinline__ SeqRows seq_rows(const DevCtx& c, const kv_cache_desc& d,
+                                            const PackedRows& pr, int b) {
+  SeqRows s;
+  s.len = checked_len(c, d, b);
+  if (pr.cu == nullptr) {
+    s.row0 = b;
+    s.n = s.len > 0 ? 1 : 0;
+    return s;
+  }
+  const int c0 = pr.cu[b], c1 = pr.cu[b + 1];
+  s.row0 = c0;
+  s.n = c1 - c0;
+  if (c0 < 0 || c1 < c0 || c1 > pr.total || s.n > s.len) {
+    flag(c, KV_DEVERR_BAD_LEN);
+    s.n = 0;
+  }
+  return s;
+}
+
+// Every sequence of the batch, checked by one block, so that bad offsets are flagged even
+// where no block's search ends at them.
+__device__ __forceinline__ void check_packed_rows(const DevCtx& c, const kv_cache_desc& d,
+                                                  const PackedRows& pr) {
+  if (pr.cu == nullptr) return;
+  for (int b = threadIdx.x; b < d.batch; b += blockDim.x) (void)seq_rows(c, d, pr, b);
+  if (threadIdx.x == 0 && pr.cu[0] != 0) flag(c, KV_DEVERR_BAD_LEN);
+}
+
+// Work is numbered over the whole batch without knowing the lengths: sequence b owns the
+// numbers from base(b) = floor(cu[b] / unit) + spare * b up to base(b + 1). Cutting n rows
+// into pieces of `unit` takes at most floor(n / unit) + 1 pieces (spare = 1), or one more
+// when the cuts lie at multiples of `unit` of the positions (spare = 2), so each sequence's
+// range holds its pieces, and floor(total / unit) + spare * batch numbers hold them all.
+//
+// The sequence whose range holds `item`, found by one warp, 32 offsets at a time: one round of
+// loads for batches up to 32, two up to 1024. Sets *base to the range's first number.
+__device__ __forceinline__ int find_sequence(const PackedRows& pr, int batch, int unit,
+                                             int spare, int item, int* base) {
+  if (pr.cu == nullptr) {       // one row each: sequence b owns the number b
+    *base = item;
+    return item;
+  }
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = batch, at = 0;
+  for (;;) {
+    const int step = (hi - lo + 31) >> 5;
+    const int b = lo + lane * step;
+    const int first = b < hi ? pr.cu[b] / unit + spare * b : INT32_MAX;
+    int cnt = __popc(__ballot_sync(0xffffffffu, first <= item));
+    cnt = cnt < 1 ? 1 : cnt;
+    at = __shfl_sync(0xffffffffu, first, cnt - 1);
+    lo += (cnt - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) break;
+  }
+  *base = at;
+  return lo;
+}
+
+__host__ __device__ __forceinline__ long work_numbers(const int32_t* cu, int total, int batch,
+                                                      int unit, int spare) {
+  return cu == nullptr ? (long)batch : (long)(total / unit) + (long)spare * batch;
+}
+
+}  // namespace skv

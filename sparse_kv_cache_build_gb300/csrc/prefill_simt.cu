@@ -1,0 +1,241 @@
+// Causal prompt attention on the CUDA cores.
+//
+// One block takes 64 rows and walks their keys 64 at a time, with the running maximum and sum
+// of the softmax per row. 256 threads hold 4 x 4 of the 64 x 64 scores and 4 x D/16 of the
+// output each; the operands come from shared memory as 16-byte reads (rows padded by four
+// floats, so that the sixteen keys of a warp's read fall into different banks), the
+// probabilities go through the key tile's buffer once its scores are done.
+#include "prefill.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int R = kPrefillSimtRows;    // rows and keys of a tile
+constexpr int KT = 64;
+
+template <int D> struct SimtCfg {
+  static constexpr int LD = D + 4;                   // padded row, floats
+  static constexpr int PLD = KT + 4;
+  static constexpr size_t SMEM = sizeof(float) * 3 * R * LD;
+  static_assert(R * PLD <= KT * LD, "the probabilities fit the key buffer");
+};
+
+// Copies `rows` rows of D elements into padded shared rows as floats; row(i) gives the source
+// of row i, or NULL for zeros.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void stage_rows(float* dst, F row) {
+  constexpr int EPC = 16 / ElemTraits<T>::bytes;     // elements per 16-byte chunk
+  constexpr int CPR = D / EPC;
+  for (int i = threadIdx.x; i < R * CPR; i += kThreads) {
+    const int r = i / CPR, c = (i % CPR) * EPC;
+    const T* src = row(r);
+    float f[EPC];
+    if (src != nullptr) {
+      chunk_to_f32<T>(*reinterpret_cast<const uint4*>(src + c), f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) f[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < EPC; e += 4)
+      *reinterpret_cast<float4*>(dst + r * SimtCfg<D>::LD + c + e) =
+          make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+  }
+}
+
+template <typename T> __device__ __forceinline__ void store4(T* p, const float* f);
+template <> __device__ __forceinline__ void store4<float>(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, const float* f) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
+  using C = SimtCfg<D>;
+  constexpr int LD = C::LD, PLD = C::PLD, NC = D / 64;
+  extern __shared__ __align__(16) float sm[];
+  float* sq = sm;
+  float* sk = sq + R * LD;
+  float* sv = sk + KT * LD;
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0) check_packed_rows(ctx, d, pr);
+  PrefillItem it;
+  if (!prefill_item(ctx, d, pr, a, R / a.G, KT, &it)) {
+    if (pr.cu == nullptr && a.S == 1) empty_row<T, D>(a, it.b, it.g);
+    return;
+  }
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int rows = it.n_tok * a.G, Hkv = d.num_kv_heads, PS = d.page_size;
+  const T* q = static_cast<const T*>(a.q);
+  const T* kp = static_cast<const T*>(d.k_pool);
+  const T* vp = static_cast<const T*>(d.v_pool);
+  const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
+
+  stage_rows<T, D>(sq, [&](int r) -> const T* {
+    return r < rows ? q + (it.row0 + r / a.G) * a.q_stride +
+                          (int64_t)(it.g * a.G + r % a.G) * D
+                    : nullptr;
+  });
+  float m[4], l[4], o[4][4 * NC];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4 * NC; ++j) o[i][j] = 0.f;
+  }
+
+  for (int kt = it.kt0; kt < it.kt1; ++kt) {
+    const int u0 = kt * KT;
+    // keys past the sequence's end are zeros: whatever their slots hold stays out of the sums
+    auto row_of = [&](const T* pool, int i) -> const T* {
+      if (i >= it.len - u0) return nullptr;
+      const int u = u0 + i;
+      const int P = table[u / PS];
+      if (P < 0 || P >= d.num_phys_pages) {
+        flag(ctx, KV_DEVERR_BAD_PAGE);
+        return nullptr;
+      }
+      return pool + (((int64_t)P * Hkv + it.g) * PS + u % PS) * D;
+    };
+    __syncthreads();
+    stage_rows<T, D>(sk, [&](int i) { return row_of(kp, i); });
+    stage_rows<T, D>(sv, [&](int i) { return row_of(vp, i); });
+    __syncthreads();
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      float4 x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LD + c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        y[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+          s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+          s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+          s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+        }
+    }
+    __syncthreads();                     // the key buffer takes the probabilities
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int last = it.pos0 + (ty * 4 + i) / a.G;      // the row's last key
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = tx + 16 * j <= last - u0 ? s[i][j] * a.scale_log2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float now = fmaxf(m[i], top);
+      const float ref = now == -INFINITY ? 0.f : now;     // no key of this row yet
+      const float keep = exp2f(m[i] - ref);
+      m[i] = now;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - ref);
+        sum += p;
+        sk[(ty * 4 + i) * PLD + tx + 16 * j] = p;
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[i] = fmaf(l[i], keep, sum);
+#pragma unroll
+      for (int j = 0; j < 4 * NC; ++j) o[i][j] *= keep;
+    }
+    __syncwarp();                        // a row's sixteen writers are one half warp
+#pragma unroll 4
+    for (int u = 0; u < KT; u += 4) {
+      float4 p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        p[i] = *reinterpret_cast<const float4*>(sk + (ty * 4 + i) * PLD + u);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 v = *reinterpret_cast<const float4*>(sv + (u + e) * LD + 64 * c + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+            o[i][4 * c] = fmaf(w, v.x, o[i][4 * c]);
+            o[i][4 * c + 1] = fmaf(w, v.y, o[i][4 * c + 1]);
+            o[i][4 * c + 2] = fmaf(w, v.z, o[i][4 * c + 2]);
+            o[i][4 * c + 3] = fmaf(w, v.w, o[i][4 * c + 3]);
+          }
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+    if (r >= rows) continue;
+    const int64_t row = (int64_t)(it.row0 + r / a.G) * a.Hq + it.g * a.G + r % a.G;
+    if (a.S > 1) {
+      float* acc = a.part_acc + (row * a.S + it.s) * D;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) store4<float>(acc + 64 * c + 4 * tx, o[i] + 4 * c);
+      if (tx == 0) {
+        a.part_ml[(row * a.S + it.s) * 2] = m[i];
+        a.part_ml[(row * a.S + it.s) * 2 + 1] = l[i];
+      }
+      continue;
+    }
+    const float inv = 1.f / l[i];                 // every row sees its own token: l > 0
+#pragma unroll
+    for (int j = 0; j < 4 * NC; ++j) o[i][j] *= inv;
+    T* dst = static_cast<T*>(a.out) + row * D;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) store4<T>(dst + 64 * c + 4 * tx, o[i] + 4 * c);
+    if (tx == 0 && a.lse != nullptr) a.lse[row] = (m[i] + log2f(l[i])) * kLn2;
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
+                     DevCtx ctx, cudaStream_t s) {
+  auto kern = prefill_simt_kernel<T, D>;
+  const size_t smem = SimtCfg<D>::SMEM;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const long items = work_numbers(pr.cu, pr.total, d.batch, R / a.G, 1);
+  dim3 grid((unsigned)(items * d.num_kv_heads), a.S);
+  return launch_pdl(kern, grid, dim3(kThreads), smem, s, d, pr, a, ctx);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
+                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
+  if (d.dtype == KV_BF16)
+    return d.head_dim == 128 ? launch_t<bf16_t, 128>(d, pr, a, ctx, s)
+                             : launch_t<bf16_t, 64>(d, pr, a, ctx, s);
+  return d.head_dim == 128 ? launch_t<float, 128>(d, pr, a, ctx, s)
+                           : launch_t<float, 64>(d, pr, a, ctx, s);
+}
+
+}  // namespace skv
