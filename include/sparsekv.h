@@ -249,6 +249,8 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
  * split: workspace may then be NULL); it holds nothing between calls, and calls that overlap
  * on the GPU need one each. Bad offsets and lengths are flagged on the device and the sequence
  * left out; an unmapped page is flagged and not read, and its sequence's rows are unspecified.
+ * KV_ERR_UNSUPPORTED for bf16 pools of 2^31 rows (num_phys_pages * num_kv_heads * page_size)
+ * or more.
  */
 size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_heads,
                                       int32_t total_tokens, int32_t num_splits);

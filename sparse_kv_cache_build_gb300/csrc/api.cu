@@ -404,6 +404,9 @@ kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_s
   if (work_numbers(cu_tokens, total_tokens, cache->batch,
                    prefill_tile_tokens(cache->dtype, G), 1) * cache->num_kv_heads > INT32_MAX)
     return KV_ERR_UNSUPPORTED;
+  if (cache->dtype == KV_BF16 &&
+      (int64_t)cache->num_phys_pages * cache->num_kv_heads * cache->page_size > INT32_MAX)
+    return KV_ERR_UNSUPPORTED;                    // TMA row coordinates are 32-bit
   if (total_tokens == 0) return KV_OK;
   DevCtx ctx;
   DeviceState* st = nullptr;

@@ -76,12 +76,15 @@ cudaError_t merge_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillA
 
 }  // namespace
 
-int prefill_tile_tokens(int dtype, int G) { return kPrefillSimtRows / G; }
+int prefill_tile_tokens(int dtype, int G) {
+  return (dtype == KV_BF16 ? kPrefillMmaRows : kPrefillSimtRows) / G;
+}
 
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
   const PackedRows pr{cu, total};
-  cudaError_t e = launch_prefill_simt(d, pr, a, ctx, s);
+  cudaError_t e = d.dtype == KV_BF16 ? launch_prefill_mma(d, pr, a, ctx, s)
+                                     : launch_prefill_simt(d, pr, a, ctx, s);
   if (e != cudaSuccess || a.S == 1) return e;
   if (d.dtype == KV_BF16)
     return d.head_dim == 128 ? merge_t<bf16_t, 128>(d, pr, a, ctx, s)

@@ -75,6 +75,8 @@ cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
 cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
                                 const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
-constexpr int kPrefillSimtRows = 64;
+cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
+                               const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
+constexpr int kPrefillSimtRows = 64, kPrefillMmaRows = 256;      // rows of a tile
 
 }  // namespace skv

@@ -1,4 +1,4 @@
-// Causal prompt attention on the CUDA cores.
+// Causal prompt attention for fp32 caches, on the CUDA cores.
 //
 // One block takes 64 rows and walks their keys 64 at a time, with the running maximum and sum
 // of the softmax per row. 256 threads hold 4 x 4 of the 64 x 64 scores and 4 x D/16 of the
@@ -21,42 +21,25 @@ template <int D> struct SimtCfg {
   static_assert(R * PLD <= KT * LD, "the probabilities fit the key buffer");
 };
 
-// Copies `rows` rows of D elements into padded shared rows as floats; row(i) gives the source
-// of row i, or NULL for zeros.
-template <typename T, int D, typename F>
+// Copies R rows of D elements into padded shared rows; row(i) gives the source of row i, or NULL
+// for zeros.
+template <int D, typename F>
 __device__ __forceinline__ void stage_rows(float* dst, F row) {
-  constexpr int EPC = 16 / ElemTraits<T>::bytes;     // elements per 16-byte chunk
-  constexpr int CPR = D / EPC;
+  constexpr int CPR = D / 4;                         // 16-byte chunks of a row
   for (int i = threadIdx.x; i < R * CPR; i += kThreads) {
-    const int r = i / CPR, c = (i % CPR) * EPC;
-    const T* src = row(r);
-    float f[EPC];
-    if (src != nullptr) {
-      chunk_to_f32<T>(*reinterpret_cast<const uint4*>(src + c), f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) f[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < EPC; e += 4)
-      *reinterpret_cast<float4*>(dst + r * SimtCfg<D>::LD + c + e) =
-          make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+    const int r = i / CPR, c = (i % CPR) * 4;
+    const float* src = row(r);
+    *reinterpret_cast<float4*>(dst + r * SimtCfg<D>::LD + c) =
+        src != nullptr ? *reinterpret_cast<const float4*>(src + c)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
-template <typename T> __device__ __forceinline__ void store4(T* p, const float* f);
-template <> __device__ __forceinline__ void store4<float>(float* p, const float* f) {
+__device__ __forceinline__ void store4(float* p, const float* f) {
   *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
 }
-template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, const float* f) {
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-}
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
 prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
   using C = SimtCfg<D>;
@@ -70,17 +53,17 @@ prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
   if (blockIdx.x == 0 && blockIdx.y == 0) check_packed_rows(ctx, d, pr);
   PrefillItem it;
   if (!prefill_item(ctx, d, pr, a, R / a.G, KT, &it)) {
-    if (pr.cu == nullptr && a.S == 1) empty_row<T, D>(a, it.b, it.g);
+    if (pr.cu == nullptr && a.S == 1) empty_row<float, D>(a, it.b, it.g);
     return;
   }
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int rows = it.n_tok * a.G, Hkv = d.num_kv_heads, PS = d.page_size;
-  const T* q = static_cast<const T*>(a.q);
-  const T* kp = static_cast<const T*>(d.k_pool);
-  const T* vp = static_cast<const T*>(d.v_pool);
+  const float* q = static_cast<const float*>(a.q);
+  const float* kp = static_cast<const float*>(d.k_pool);
+  const float* vp = static_cast<const float*>(d.v_pool);
   const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
 
-  stage_rows<T, D>(sq, [&](int r) -> const T* {
+  stage_rows<D>(sq, [&](int r) -> const float* {
     return r < rows ? q + (it.row0 + r / a.G) * a.q_stride +
                           (int64_t)(it.g * a.G + r % a.G) * D
                     : nullptr;
@@ -97,7 +80,7 @@ prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
   for (int kt = it.kt0; kt < it.kt1; ++kt) {
     const int u0 = kt * KT;
     // keys past the sequence's end are zeros: whatever their slots hold stays out of the sums
-    auto row_of = [&](const T* pool, int i) -> const T* {
+    auto row_of = [&](const float* pool, int i) -> const float* {
       if (i >= it.len - u0) return nullptr;
       const int u = u0 + i;
       const int P = table[u / PS];
@@ -108,8 +91,8 @@ prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
       return pool + (((int64_t)P * Hkv + it.g) * PS + u % PS) * D;
     };
     __syncthreads();
-    stage_rows<T, D>(sk, [&](int i) { return row_of(kp, i); });
-    stage_rows<T, D>(sv, [&](int i) { return row_of(vp, i); });
+    stage_rows<D>(sk, [&](int i) { return row_of(kp, i); });
+    stage_rows<D>(sv, [&](int i) { return row_of(vp, i); });
     __syncthreads();
     float s[4][4];
 #pragma unroll
@@ -197,7 +180,7 @@ prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
     if (a.S > 1) {
       float* acc = a.part_acc + (row * a.S + it.s) * D;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) store4<float>(acc + 64 * c + 4 * tx, o[i] + 4 * c);
+      for (int c = 0; c < NC; ++c) store4(acc + 64 * c + 4 * tx, o[i] + 4 * c);
       if (tx == 0) {
         a.part_ml[(row * a.S + it.s) * 2] = m[i];
         a.part_ml[(row * a.S + it.s) * 2 + 1] = l[i];
@@ -207,17 +190,17 @@ prefill_simt_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
     const float inv = 1.f / l[i];                 // every row sees its own token: l > 0
 #pragma unroll
     for (int j = 0; j < 4 * NC; ++j) o[i][j] *= inv;
-    T* dst = static_cast<T*>(a.out) + row * D;
+    float* dst = static_cast<float*>(a.out) + row * D;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) store4<T>(dst + 64 * c + 4 * tx, o[i] + 4 * c);
+    for (int c = 0; c < NC; ++c) store4(dst + 64 * c + 4 * tx, o[i] + 4 * c);
     if (tx == 0 && a.lse != nullptr) a.lse[row] = (m[i] + log2f(l[i])) * kLn2;
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
                      DevCtx ctx, cudaStream_t s) {
-  auto kern = prefill_simt_kernel<T, D>;
+  auto kern = prefill_simt_kernel<D>;
   const size_t smem = SimtCfg<D>::SMEM;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -231,11 +214,7 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
 
 cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
                                 const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
-  if (d.dtype == KV_BF16)
-    return d.head_dim == 128 ? launch_t<bf16_t, 128>(d, pr, a, ctx, s)
-                             : launch_t<bf16_t, 64>(d, pr, a, ctx, s);
-  return d.head_dim == 128 ? launch_t<float, 128>(d, pr, a, ctx, s)
-                           : launch_t<float, 64>(d, pr, a, ctx, s);
+  return d.head_dim == 128 ? launch_t<128>(d, pr, a, ctx, s) : launch_t<64>(d, pr, a, ctx, s);
 }
 
 }  // namespace skv
