@@ -242,21 +242,24 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
  * probabilities are rounded to bf16 before they meet the values. Rows that belong to no
  * sequence are left as they were; with cu_tokens = NULL the row of an empty sequence gets
  * out = 0 and lse = -inf. Cached tokens must be finite; what lies in a page past its
- * sequence's end has no influence. Results do not depend on timing (no atomics).
- * num_splits: 0 chooses how many ways the keys of a row are split (1 when the rows alone fill
- * the GPU); 1 .. 64 asks for that many. workspace: device, 256-byte aligned,
- * kv_prefill_attn_workspace_size() bytes for the same arguments (0 when the keys are not
- * split: workspace may then be NULL); it holds nothing between calls, and calls that overlap
- * on the GPU need one each. Bad offsets and lengths are flagged on the device and the sequence
- * left out; an unmapped page is flagged and not read, and its sequence's rows are unspecified.
+ * sequence's end has no influence. The same call gives the same bits (no atomics); where a
+ * row's keys are cut, and so its last bits, depends on the whole batch unless num_shares = 1.
+ * num_shares: the work (row tiles by their keys, cut inside a row's keys where need be) is
+ * divided evenly among this many blocks whatever the lengths; 0 takes as many as the GPU holds
+ * at once, 1 .. 1024 asks for that many. workspace: device, 256-byte aligned,
+ * kv_prefill_attn_workspace_size() bytes for the same arguments (two row tiles of float32
+ * partials per share; 0 for one share: workspace may then be NULL); it holds nothing between
+ * calls, and calls that overlap on the GPU need one each. Bad offsets and lengths are flagged
+ * on the device and the sequence left out; an unmapped page is flagged and not read, and its
+ * sequence's rows are unspecified.
  * KV_ERR_UNSUPPORTED for bf16 pools of 2^31 rows (num_phys_pages * num_kv_heads * page_size)
  * or more.
  */
 size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_heads,
-                                      int32_t total_tokens, int32_t num_splits);
+                                      int32_t total_tokens, int32_t num_shares);
 kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
                           int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
-                          float sm_scale, int32_t num_splits, void* out, float* lse,
+                          float sm_scale, int32_t num_shares, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
@@ -651,7 +654,7 @@ kv_status kv_entmax_decode_step(const kv_cache_desc* cache, const void* q, int32
  * kv_entmax_attn_workspace_size(cache, num_q_heads, k_max as sel_stride, 0 = every page);
  * KV_OP_ENTMAX_DECODE_STEP: kv_entmax_decode_step_workspace_size(cache, num_q_heads,
  * k_max); KV_OP_PREFILL_ATTN: kv_prefill_attn_workspace_size(cache, num_q_heads, k_max as
- * total_tokens, num_splits)). Arguments a given op does not use are ignored. Every other call of this library
+ * total_tokens, num_splits as num_shares)). Arguments a given op does not use are ignored. Every other call of this library
  * takes no workspace. Returns 0 for an unknown op or a bad argument.
  */
 typedef enum {

@@ -378,12 +378,12 @@ def kv_append_rope(kv: PagedKV, q, k_new, v_new, stats, turns=None, cu_tokens=No
 
 
 def kv_prefill_attn_workspace_size(kv: PagedKV, num_q_heads: int, total_tokens: int,
-                                   num_splits: int = 0) -> int:
+                                   num_shares: int = 0) -> int:
     return int(lib().kv_prefill_attn_workspace_size(kv.ref(), int(num_q_heads),
-                                                    int(total_tokens), int(num_splits)))
+                                                    int(total_tokens), int(num_shares)))
 
 
-def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_splits: int = 0,
+def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares: int = 0,
                     out=None, lse=None, workspace=None, stream=None):
     """Causal attention of packed query rows [T][Hq][D] over the cache, which holds the rows'
     own keys and values already: (out of the cache's dtype, lse float32)."""
@@ -399,10 +399,10 @@ def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_splits:
     if T == 0:
         return out, lse
     if workspace is None:
-        nbytes = kv_prefill_attn_workspace_size(kv, Hq, T, num_splits)
+        nbytes = kv_prefill_attn_workspace_size(kv, Hq, T, num_shares)
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
     _check("kv_prefill_attn", lib().kv_prefill_attn(
-        kv.ref(), _ptr(q), qs, Hq, _ptr(cu_tokens), T, float(sm_scale), int(num_splits),
+        kv.ref(), _ptr(q), qs, Hq, _ptr(cu_tokens), T, float(sm_scale), int(num_shares),
         _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
     return out, lse
 

@@ -218,27 +218,21 @@ kv_status check_packed(const kv_cache_desc* d, const int32_t* cu_tokens, int32_t
   return KV_OK;
 }
 
-constexpr int kPrefillMaxSplits = 64;
-constexpr int kPrefillMinSplitKeys = 512;
+constexpr int kPrefillMaxShares = 1024;
 
-// Splits of the prompt attention: 1 when the row tiles alone fill the SMs, else as many as
-// still fit one wave, with at least kPrefillMinSplitKeys keys each at the table's capacity.
-int prefill_splits(const kv_cache_desc* d, int G, int total, int asked, const DeviceState* st) {
-  if (asked > 0) return asked;
-  const long tile = prefill_tile_tokens(d->dtype, G);
-  const long blocks = (total / tile + (total < d->batch ? total : d->batch)) * d->num_kv_heads;
-  long S = blocks > 0 ? st->sms / blocks : 1;
-  const long cap = (long)d->page_table_stride * d->page_size / kPrefillMinSplitKeys;
-  if (S > cap) S = cap;
-  if (S > kPrefillMaxSplits) S = kPrefillMaxSplits;
-  return S < 1 ? 1 : (int)S;
+// Blocks the prompt attention divides a batch among: as many as are resident at once.
+int prefill_shares(const kv_cache_desc* d, int asked, const DeviceState* st) {
+  return asked > 0 ? asked : st->sms * prefill_blocks_per_sm(d->dtype);
 }
 
-struct PrefillLayout { size_t acc, ml, total; };
-PrefillLayout prefill_layout(const kv_cache_desc* d, int Hq, int total, int S) {
+// Two parts per block, of a tile's rows or all the rows there are.
+struct PrefillLayout { int rows; size_t ml, total; };
+PrefillLayout prefill_layout(const kv_cache_desc* d, int G, int total, int shares) {
   PrefillLayout L{0, 0, 0};
-  if (S <= 1) return L;
-  const size_t rows = (size_t)total * Hq * S;
+  if (shares <= 1 || total <= 0) return L;
+  const int tile = prefill_tile_rows(d->dtype);
+  L.rows = (int64_t)total * G < tile ? total * G : tile;
+  const size_t rows = (size_t)2 * shares * L.rows;
   L.ml = round256(rows * d->head_dim * sizeof(float));
   L.total = L.ml + round256(rows * 2 * sizeof(float));
   return L;
@@ -375,35 +369,30 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
 }
 
 size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_heads,
-                                      int32_t total_tokens, int32_t num_splits) {
+                                      int32_t total_tokens, int32_t num_shares) {
   if (check_desc(cache) != KV_OK || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 ||
-      total_tokens < 0 || num_splits < 0 || num_splits > kPrefillMaxSplits)
+      total_tokens < 0 || num_shares < 0 || num_shares > kPrefillMaxShares)
     return 0;
   const int G = num_q_heads / cache->num_kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8) return 0;
   DeviceState* st = nullptr;
-  if (num_splits == 0 && device_state(&st) != KV_OK) return 0;
-  const int S = prefill_splits(cache, G, total_tokens, num_splits, st);
-  return prefill_layout(cache, num_q_heads, total_tokens, S).total;
+  if (num_shares == 0 && device_state(&st) != KV_OK) return 0;
+  return prefill_layout(cache, G, total_tokens, prefill_shares(cache, num_shares, st)).total;
 }
 
 kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
                           int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
-                          float sm_scale, int32_t num_splits, void* out, float* lse,
+                          float sm_scale, int32_t num_shares, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   kv_status r = check_desc(cache);
   if (r != KV_OK) return r;
   if ((r = check_heads(cache, q, num_q_heads)) != KV_OK) return r;
   if ((r = check_packed(cache, cu_tokens, total_tokens)) != KV_OK) return r;
-  if (out == nullptr || !(sm_scale > 0.f) || !isfinite(sm_scale) || num_splits < 0 ||
-      num_splits > kPrefillMaxSplits)
+  if (out == nullptr || !(sm_scale > 0.f) || !isfinite(sm_scale) || num_shares < 0 ||
+      num_shares > kPrefillMaxShares)
     return KV_ERR_INVALID_ARG;
   if ((r = check_rows(cache, q, q_stride, num_q_heads)) != KV_OK) return r;
   if (!aligned16(out)) return KV_ERR_MISALIGNED;
-  const int G = num_q_heads / cache->num_kv_heads;
-  if (work_numbers(cu_tokens, total_tokens, cache->batch,
-                   prefill_tile_tokens(cache->dtype, G), 1) * cache->num_kv_heads > INT32_MAX)
-    return KV_ERR_UNSUPPORTED;
   if (cache->dtype == KV_BF16 &&
       (int64_t)cache->num_phys_pages * cache->num_kv_heads * cache->page_size > INT32_MAX)
     return KV_ERR_UNSUPPORTED;                    // TMA row coordinates are 32-bit
@@ -412,22 +401,24 @@ kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_s
   DeviceState* st = nullptr;
   if ((r = ctx_for_call(&ctx, &st)) != KV_OK) return r;
   PrefillArgs a{};
-  a.S = prefill_splits(cache, G, total_tokens, num_splits, st);
-  const PrefillLayout L = prefill_layout(cache, num_q_heads, total_tokens, a.S);
-  if (L.total > 0) {
-    if (workspace == nullptr || workspace_bytes < L.total ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-      return KV_ERR_WORKSPACE;
-    a.part_acc = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.ml);
-  }
   a.q = q;
   a.q_stride = q_stride;
   a.out = out;
   a.lse = lse;
   a.scale_log2 = sm_scale * kLog2e;
   a.Hq = num_q_heads;
-  a.G = G;
+  a.G = num_q_heads / cache->num_kv_heads;
+  while (1 << a.log_g < a.G) ++a.log_g;
+  a.NC = prefill_shares(cache, num_shares, st);
+  const PrefillLayout L = prefill_layout(cache, a.G, total_tokens, a.NC);
+  if (L.total > 0) {
+    if (workspace == nullptr || workspace_bytes < L.total ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return KV_ERR_WORKSPACE;
+    a.part_acc = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.ml);
+    a.part_rows = L.rows;
+  }
   return from_cuda(launch_prefill(*cache, cu_tokens, total_tokens, a, ctx, stream));
 }
 

@@ -1,96 +1,143 @@
-// Causal prompt attention: the choice of kernel, and the merge of its splits.
+// Causal prompt attention: the choice of kernel, and the join of the items its blocks shared.
 #include "prefill.cuh"
 
 namespace skv {
 namespace {
 
-template <typename T> __device__ __forceinline__ void store_out(T* p, float a, float b);
-template <> __device__ __forceinline__ void store_out<bf16_t>(bf16_t* p, float a, float b) {
+constexpr int kMergeWarps = 8;
+constexpr int kMergeRowGroups = 8;       // blocks per border, each with a share of the rows
+
+template <typename T> __device__ __forceinline__ void store2(T* p, float a, float b);
+template <> __device__ __forceinline__ void store2<bf16_t>(bf16_t* p, float a, float b) {
   uint32_t w;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
   *reinterpret_cast<uint32_t*>(p) = w;
 }
-template <> __device__ __forceinline__ void store_out<float>(float* p, float a, float b) {
+template <> __device__ __forceinline__ void store2<float>(float* p, float a, float b) {
   *reinterpret_cast<float2*>(p) = make_float2(a, b);
 }
 
-// out = sum_s acc_s 2^(m_s - M) / L with M = max m_s, L = sum_s l_s 2^(m_s - M). One block of
-// D/2 threads per (row, head), two columns each: with few rows the blocks are few, and a
-// block's partials are all loaded before the first is used. Splits without keys for a row
-// (m = -inf) carry no weight and their accumulators are not read.
-constexpr int kMergeBatch = 8;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(D / 2)
-prefill_merge_kernel(kv_cache_desc d, PackedRows pr, PrefillArgs a, DevCtx ctx) {
+// Border number c = blockIdx.x + 1 between blocks c - 1 and c: if it cuts an item, and is the
+// first that does, joins the item's parts row by row:
+//   out = sum_p acc_p 2^(m_p - M) / L,  M = max_p m_p,  L = sum_p l_p 2^(m_p - M).
+// The parts are those of blocks c - 1, c, ... up to the one that reaches the item's end. One
+// warp per row, lanes over the parts for (m, l) and over the columns for the accumulators,
+// whose loads are independent of one another. A part without keys for a row (m = -inf) has no
+// accumulator to read.
+template <typename T, typename S, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+prefill_merge_kernel(const __grid_constant__ kv_cache_desc d,
+                     const __grid_constant__ PackedRows pr,
+                     const __grid_constant__ PrefillArgs a, const __grid_constant__ DevCtx ctx) {
+  __shared__ LineScratch scratch;
+  constexpr int PAIRS = D / 64;            // column pairs per lane
+  // lengths and offsets are older than the attention kernel, which let this one start only
+  // after its own wait for them; its parts are read after the wait below
   pdl_trigger();
-  pdl_wait();
-  const int row = blockIdx.x, h = blockIdx.y, c = 2 * threadIdx.x;
-  int base;
-  const int b = find_sequence(pr, d.batch, 1, 0, row, &base);
-  const SeqRows sr = seq_rows(ctx, d, pr, b);
-  const int64_t at = (int64_t)row * a.Hq + h;
-  T* dst = static_cast<T*>(a.out) + at * D + c;
-  if (row >= sr.row0 + sr.n || row < sr.row0) {
-    // not a row of any sequence: left as it was, but for an empty sequence's own row
-    if (pr.cu == nullptr) {
-      store_out<T>(dst, 0.f, 0.f);
-      if (c == 0 && a.lse != nullptr) a.lse[at] = -INFINITY;
-    }
-    return;
-  }
-  const float* ml = a.part_ml + at * a.S * 2;
-  const float* acc = a.part_acc + at * a.S * D + c;
-  float M = -INFINITY;
-  for (int s = 0; s < a.S; ++s) M = fmaxf(M, ml[2 * s]);
-  float L = 0.f, x = 0.f, y = 0.f;
-  for (int s0 = 0; s0 < a.S; s0 += kMergeBatch) {
-    float2 v[kMergeBatch];
-    float w[kMergeBatch];
+  const int c = blockIdx.x + 1;
+  const LinePlace at = find_place<S>(ctx, d, pr, a, c, &scratch);
+  PrefillItem it;
+  int left = 0, prev = 0;
+  bool cut = false;
+  const int64_t y = at.total * c / a.NC;
+  if (at.total > 0 && y < at.total) {
+    const ItemWalk<S> walk(d, pr, a, ctx, y, y + 1, at.b, at.before, 0);
+    if (walk.first(&it)) {
+      left = walk.first_before(y);
+      prev = walk.first_before(at.total * (c - 1) / a.NC);
+      cut = left > 0 && left < it.nk && prev == 0;
+      if (cut) {
+        // the block that reaches the item's end
+        int end = c;
+        while (walk.first_before(at.total * (end + 1) / a.NC) < it.nk) ++end;
+        pdl_wait();
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int rows = it.n_tok << a.log_g;
+        for (int row = blockIdx.y * kMergeWarps + warp; row < rows;
+             row += kMergeRowGroups * kMergeWarps) {
+          float M = -INFINITY, L = 0.f;
+          float2 acc[PAIRS];
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) {
-      const int s = s0 + i;
-      const float m = s < a.S ? ml[2 * s] : -INFINITY;
-      w[i] = m == -INFINITY ? 0.f : exp2f(m - M);
-      v[i] = m == -INFINITY ? make_float2(0.f, 0.f)
-                            : *reinterpret_cast<const float2*>(acc + (int64_t)s * D);
-      if (m != -INFINITY) L = fmaf(ml[2 * s + 1], w[i], L);
-    }
+          for (int p = 0; p < PAIRS; ++p) acc[p] = make_float2(0.f, 0.f);
+          for (int j0 = c - 1; j0 <= end; j0 += 32) {
+            const int j = j0 + lane;
+            // block c - 1 ends with this item, the others begin with it
+            const int64_t mine = (int64_t)(j == c - 1 ? 2 * j + 1 : 2 * j) * a.part_rows + row;
+            float m = -INFINITY, l = 0.f;
+            if (j <= end && walk.first_before(at.total * j / a.NC) <
+                                walk.first_before(at.total * (j + 1) / a.NC)) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + mine);
+              m = ml.x;
+              l = ml.y;
+            }
+            float now = fmaxf(M, m);
 #pragma unroll
-    for (int i = 0; i < kMergeBatch; ++i) {
-      x = fmaf(v[i].x, w[i], x);
-      y = fmaf(v[i].y, w[i], y);
+            for (int o = 16; o > 0; o >>= 1)
+              now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+            if (now == -INFINITY) continue;
+            const float keep = exp2f(M - now), w = exp2f(m - now);
+            M = now;
+            float sum = l * w;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            L = fmaf(L, keep, sum);
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) {
+              acc[p].x *= keep;
+              acc[p].y *= keep;
+            }
+            const int parts = min(32, end + 1 - j0);
+#pragma unroll 8
+            for (int e = 0; e < parts; ++e) {
+              const float we = __shfl_sync(0xffffffffu, w, e);
+              const int64_t from = __shfl_sync(0xffffffffu, mine, e);
+              if (we == 0.f) continue;             // no keys, or nothing left of them
+              const float2* src = reinterpret_cast<const float2*>(a.part_acc + from * D) + lane;
+#pragma unroll
+              for (int p = 0; p < PAIRS; ++p) {
+                const float2 v = __ldcg(src + 32 * p);
+                acc[p].x = fmaf(v.x, we, acc[p].x);
+                acc[p].y = fmaf(v.y, we, acc[p].y);
+              }
+            }
+          }
+          const int64_t out_row = (int64_t)(it.row0 + (row >> a.log_g)) * a.Hq + it.g * a.G +
+                                  (row & (a.G - 1));
+          const float inv = 1.f / L;               // every row sees its own token: L > 0
+          T* dst = static_cast<T*>(a.out) + out_row * D + 2 * lane;
+#pragma unroll
+          for (int p = 0; p < PAIRS; ++p) store2<T>(dst + 64 * p, acc[p].x * inv, acc[p].y * inv);
+          if (lane == 0 && a.lse != nullptr) a.lse[out_row] = (M + log2f(L)) * kLn2;
+        }
+      }
     }
   }
-  const float inv = 1.f / L;             // every row sees its own token: L > 0
-  store_out<T>(dst, x * inv, y * inv);
-  if (c == 0 && a.lse != nullptr) a.lse[at] = (M + log2f(L)) * kLn2;
+  if (!cut) pdl_wait();
 }
 
-template <typename T, int D>
+template <typename T, typename S, int D>
 cudaError_t merge_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
                     DevCtx ctx, cudaStream_t s) {
-  return launch_pdl(prefill_merge_kernel<T, D>, dim3(pr.total, a.Hq), dim3(D / 2), 0, s, d, pr,
-                    a, ctx);
+  return launch_pdl(prefill_merge_kernel<T, S, D>, dim3(a.NC - 1, kMergeRowGroups),
+                    dim3(kMergeWarps * 32), 0, s, d, pr, a, ctx);
 }
 
 }  // namespace
 
-int prefill_tile_tokens(int dtype, int G) {
-  return (dtype == KV_BF16 ? kPrefillMmaRows : kPrefillSimtRows) / G;
-}
+int prefill_tile_rows(int dtype) { return dtype == KV_BF16 ? MmaShape::rows : SimtShape::rows; }
+int prefill_blocks_per_sm(int dtype) { return dtype == KV_BF16 ? 1 : 2; }
 
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
   const PackedRows pr{cu, total};
-  cudaError_t e = d.dtype == KV_BF16 ? launch_prefill_mma(d, pr, a, ctx, s)
-                                     : launch_prefill_simt(d, pr, a, ctx, s);
-  if (e != cudaSuccess || a.S == 1) return e;
-  if (d.dtype == KV_BF16)
-    return d.head_dim == 128 ? merge_t<bf16_t, 128>(d, pr, a, ctx, s)
-                             : merge_t<bf16_t, 64>(d, pr, a, ctx, s);
-  return d.head_dim == 128 ? merge_t<float, 128>(d, pr, a, ctx, s)
-                           : merge_t<float, 64>(d, pr, a, ctx, s);
+  const bool bf = d.dtype == KV_BF16;
+  cudaError_t e = bf ? launch_prefill_mma(d, pr, a, ctx, s) : launch_prefill_simt(d, pr, a, ctx, s);
+  if (e != cudaSuccess || a.NC == 1) return e;
+  if (bf)
+    return d.head_dim == 128 ? merge_t<bf16_t, MmaShape, 128>(d, pr, a, ctx, s)
+                             : merge_t<bf16_t, MmaShape, 64>(d, pr, a, ctx, s);
+  return d.head_dim == 128 ? merge_t<float, SimtShape, 128>(d, pr, a, ctx, s)
+                           : merge_t<float, SimtShape, 64>(d, pr, a, ctx, s);
 }
 
 }  // namespace skv

@@ -12,9 +12,12 @@
 // One warp feeds K and V tiles through a ring by TMA, page by page (a page of one KV head is
 // PS dense rows of the pool).
 //
-// A block with at most 128 rows (single tokens, drafts, a prompt's tail) gives both warpgroups
+// An item with at most 128 rows (single tokens, drafts, a prompt's tail) gives both warpgroups
 // the same rows and alternating key tiles instead, and joins their (m, l, O) at the end: the
 // same pipeline, with the softmax still under the other warpgroup's products.
+//
+// A block walks its share of the batch's items (prefill.cuh) without stopping between them:
+// loads and products run ahead into the next item while a warpgroup writes its output.
 //
 // The running maximum is lazy: O and l are rescaled only when a row's maximum grows by more
 // than 2^8, so that almost no tile pays for it; P stays below 2^8 and every sum is float32.
@@ -33,11 +36,11 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 384;          // two softmax warpgroups, then products and loads
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kRows = kPrefillMmaRows;  // rows of a block, two tiles
-constexpr int kKeys = 128;             // keys of a tile
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
+constexpr int kItems = 4;              // items known ahead
+constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;     // (2 * 216 + 72) * 128 = 384 * 168
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;     // (2 * 208 + 88) * 128 = 384 * 168
 constexpr float kLazy = 8.f;           // log2 of the growth that forces a rescale
 
 template <int D> struct Cfg {
@@ -47,18 +50,33 @@ template <int D> struct Cfg {
   static constexpr size_t OFF_Q = 0;                            // from a 1024-aligned base
   static constexpr size_t OFF_RING = 2 * TILE_BYTES;
   static constexpr size_t OFF_BAR = OFF_RING + (size_t)STAGES * TILE_BYTES;
-  static constexpr int BARS = 2 * STAGES + 9;
-  static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;
-  static constexpr size_t SMEM = OFF_MISC + 16 + 1024;          // + alignment slack
-  static_assert((size_t)STAGES * TILE_BYTES >= 128 * (size_t)(D + 2) * 4, "join buffer");
+  static constexpr int BARS = 2 * STAGES + 13 + 2 * kItems;
+  static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;        // TMEM base, then [2][128] (m, l)
+  static constexpr size_t OFF_ITEMS = OFF_MISC + 8;
+  static constexpr size_t OFF_ML = OFF_ITEMS + kItems * sizeof(PrefillItem);
+  static constexpr size_t SMEM = OFF_ML + 1024 + 1024;          // + alignment slack
+  static_assert(SMEM <= 227 * 1024 - 512, "beside the scan's scratch");
 };
 
-// The block's plan: which key tiles each warpgroup takes and where they lie in the ring.
+// An item's plan: which key tiles each warpgroup takes and where they lie in the ring, counted
+// from the item's first slot.
 struct Plan {
   bool wide;      // two row tiles; else one, with the key tiles dealt out in turn
-  int n;          // key tiles of the block
+  int n;          // key tiles of the item (or of the block's part of it)
   int n0, n1;     // key tiles of each warpgroup
 
+  __device__ __forceinline__ Plan(const PrefillItem& it, int log_g) {
+    wide = (it.n_tok << log_g) > 128;
+    n = it.kt1 - it.kt0;
+    if (wide) {
+      // the first tile's rows end earlier: its last keys may lie a tile before the item's
+      n0 = max(0, min(n, (it.pos0 + (127 >> log_g)) / kKeys + 1 - it.kt0));
+      n1 = n;
+    } else {
+      n0 = (n + 1) / 2;
+      n1 = n / 2;
+    }
+  }
   __device__ __forceinline__ int tiles(int w) const { return w == 0 ? n0 : n1; }
   __device__ __forceinline__ int tile(int w, int i) const { return wide ? i : 2 * i + w; }
   // Ring slots in the order of first use: K0 V0 K1 V1 ..., or (dealt out) K0 K1 V0 K2 V1 K3 ...
@@ -81,14 +99,26 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// 16 bytes from global to shared memory; zeros when `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// A value that is the same in every lane, said so that the compiler keeps it, and what follows
+// from it, in uniform registers: the products' descriptors come from there.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
-                   const __grid_constant__ CUtensorMap map_v, kv_cache_desc d, PackedRows pr,
-                   PrefillArgs a, int log_g, DevCtx ctx) {
+                   const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ kv_cache_desc d,
+                   const __grid_constant__ PackedRows pr, const __grid_constant__ PrefillArgs a,
+                   const __grid_constant__ DevCtx ctx) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ LineScratch scratch;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~(uintptr_t)1023);
   uint8_t* ring = sm + C::OFF_RING;
@@ -97,14 +127,20 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* empty = bar + C::STAGES;             // [STAGES] its last product is done
   uint64_t* s_full = bar + 2 * C::STAGES;        // [2] S of a warpgroup is in TMEM
   uint64_t* p_full = s_full + 2;                 // [2] its P is in TMEM, O rescaled
-  uint64_t* o_done = p_full + 2;                 // [2] its last product is done
-  uint64_t* q_full = o_done + 2;                 // the rows are in shared memory
-  uint64_t* v_land = q_full + 1;                 // the last V tile, before its tail is zeroed
+  uint64_t* q_full = p_full + 2;                 // [2] its rows are in shared memory
+  uint64_t* o_done = q_full + 2;                 // [2] its last product of an item is done
+  uint64_t* o_free = o_done + 2;                 // [2] its O has been read
+  uint64_t* joined = o_free + 2;                 // the second warpgroup's (m, l) are written
+  uint64_t* v_land = joined + 1;                 // the last V tile, before its tail is zeroed
   uint64_t* drained = v_land + 1;                // after a timeout: no product in flight
+  uint64_t* item_full = drained + 1;             // [kItems] an item is in shared memory
+  uint64_t* item_free = item_full + kItems;      // [kItems] every warp is done with it
+  PrefillItem* items = reinterpret_cast<PrefillItem*>(sm + C::OFF_ITEMS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* box = reinterpret_cast<float*>(sm + C::OFF_ML);          // [2][128]: m, l
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int log_g = a.log_g;
 
-  pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(full + i, 1);
@@ -113,272 +149,353 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 1);
       mbar_init(p_full + w, 4);                  // one arrival per softmax warp
+      mbar_init(q_full + w, 4);
       mbar_init(o_done + w, 1);
+      mbar_init(o_free + w, 4);
     }
-    mbar_init(q_full, 8);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_free + i, 10);              // eight softmax warps, products, loads
+    }
+    mbar_init(joined, 4);
     mbar_init(v_land, 1);
     mbar_init(drained, 1);
     fence_mbar_init();
   }
   pdl_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_packed_rows(ctx, d, pr);
-  PrefillItem it;
-  if (!prefill_item(ctx, d, pr, a, kRows >> log_g, kKeys, &it)) {
-    if (pr.cu == nullptr && a.S == 1) empty_row<bf16_t, D>(a, it.b, it.g);
-    return;
-  }
+  pdl_trigger();       // not earlier: the merge reads lengths before it waits for this kernel
+  finish_empty<bf16_t, D>(ctx, d, pr, a);
+  const LinePlace at = find_place<MmaShape>(ctx, d, pr, a, blockIdx.x, &scratch);
+  const int64_t lo = at.total * blockIdx.x / a.NC, hi = at.total * (blockIdx.x + 1) / a.NC;
+  if (lo >= hi) return;
   if (warp == kMmaWarp) tc::alloc(tmem_slot, kTmemCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
-
-  const int rows = it.n_tok << log_g;
-  Plan plan;
-  plan.wide = rows > 128;
-  plan.n = it.kt1 - it.kt0;
-  if (plan.wide) {
-    // the first tile's rows end earlier: its last keys may lie a tile before the block's
-    const int last0 = it.pos0 + (127 >> log_g);
-    plan.n0 = max(0, min(plan.n, last0 / kKeys + 1 - it.kt0));
-    plan.n1 = plan.n;
-  } else {
-    plan.n0 = (plan.n + 1) / 2;
-    plan.n1 = plan.n / 2;
-  }
-  const int keys = it.pos0 + it.n_tok;           // keys from here on are nobody's
+  const uint32_t tmem = uniform(*tmem_slot);
+  // Item number j of the block, for the warp that asks; its last has no key tiles.
+  auto item_ready = [&](int j) {
+    return mbar_wait_bounded(item_full + j % kItems, (j / kItems) & 1, ctx.wait_ns);
+  };
+  auto item_done = [&](int j) {
+    __syncwarp();
+    if (lane == 0) arrive(item_free + j % kItems);
+  };
 
   if (warp < 8) {
     tc::more_regs<kRegsSoftmax>();
-    const int w = warp >> 2, r = tid & 127;      // warpgroup, TMEM lane
-    // ---- the rows, into 128-byte swizzled shared rows (zeros past the block's last row)
-    {
-      constexpr int CH = D / 8;                  // 16-byte chunks of a row
-      const int total = (plan.wide ? 256 : 128) * CH;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q);
-      for (int i = tid; i < total; i += 256) {
-        const int row = i / CH, c = i % CH;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows)
-          v = *reinterpret_cast<const uint4*>(
-              q + (int64_t)(it.row0 + (row >> log_g)) * a.q_stride +
-              (int64_t)(it.g * a.G + (row & (a.G - 1))) * D + c * 8);
-        uint8_t* dst = sm + C::OFF_Q + (row >> 7) * C::TILE_BYTES + (c >> 3) * 16384 +
-                       (row & 127) * 128 + (((c & 7) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = v;
-      }
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive(q_full);
-    }
-    // ---- softmax
-    const int row = plan.wide ? w * 128 + r : r;
-    const int last = it.pos0 + (row >> log_g);                    // the row's last key
-    const int warp_row = row - lane;
-    const bool idle = warp_row >= rows;                           // no row in this warp
-    const int warp_first = it.pos0 + (warp_row >> log_g);         // its first row's last key
+    const int w = warp >> 2, r = tid & 127;                       // warpgroup, TMEM lane
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // TMEM lane 32 * (warp % 4)
     const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * 128;
-    const int n = plan.tiles(w);
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
-    float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      ok = mbar_wait_bounded(s_full + w, i & 1, ctx.wait_ns);
+    int tiles_seen = 0, items_seen = 0, joins_seen = 0;           // for the barriers' phases
+
+    // This warpgroup's rows into 128-byte swizzled shared rows (zeros past the item's last).
+    auto fetch_rows = [&](const PrefillItem& it, bool wide) {
+      constexpr int CH = D / 8;                  // 16-byte chunks of a row
+      const uint16_t* q = static_cast<const uint16_t*>(a.q);
+      const uint32_t dst = smem_addr(sm + C::OFF_Q) + w * C::TILE_BYTES;
+      const int rows = it.n_tok << log_g;
+#pragma unroll 4
+      for (int i = r; i < 128 * CH; i += 128) {
+        const int row = i / CH, c = i % CH, src = wide ? w * 128 + row : row;
+        const bool have = src < rows;
+        const int tok = have ? src >> log_g : 0, head = have ? src & (a.G - 1) : 0;
+        copy16(dst + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
+               q + (int64_t)(it.row0 + tok) * a.q_stride + (int64_t)(it.g * a.G + head) * D + c * 8,
+               have ? 16 : 0);
+      }
+    };
+    auto rows_ready = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive(q_full + w);
+    };
+
+    bool first = true;
+    for (int j = 0;; ++j) {
+      ok = item_ready(j);
       if (!ok) break;
-      tc::fence_after();
-      if (!idle) {
-        const int u0 = (it.kt0 + plan.tile(w, i)) * kKeys;
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, s + 32 * c);
-        tc::wait_ld();
-        if (warp_first - u0 < kKeys - 1) {                        // on the border
-          const int seen = last - u0;
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > seen) s[c] = 0xff800000u;
+      const PrefillItem it = items[j % kItems];
+      if (it.kt0 >= it.kt1) break;
+      const Plan plan(it, log_g);
+      const int n = plan.tiles(w), rows = it.n_tok << log_g;
+      if (first) {
+        first = false;
+        if (n > 0) {
+          fetch_rows(it, plan.wide);
+          rows_ready();
         }
-        float top[4];
+      }
+      bool rows_ahead = false;
+      auto fetch_ahead = [&] {                   // the next item's rows, if it has any for w
+        ok = item_ready(j + 1);
+        if (!ok) return;
+        const PrefillItem next = items[(j + 1) % kItems];
+        const Plan plan2(next, log_g);
+        rows_ahead = plan2.tiles(w) > 0;
+        if (rows_ahead) fetch_rows(next, plan2.wide);
+      };
+      const int row = plan.wide ? w * 128 + r : r;
+      const int last = it.pos0 + (row >> log_g);                  // the row's last key
+      const int warp_row = row - lane;
+      const bool idle = warp_row >= rows;                         // no row in this warp
+      const int warp_first = it.pos0 + (warp_row >> log_g);       // its first row's last key
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < n; ++i) {
+        ok = mbar_wait_bounded(s_full + w, tiles_seen & 1, ctx.wait_ns);
+        if (!ok) break;
+        ++tiles_seen;
+        tc::fence_after();
+        // the item's last scores are done: its rows may be overwritten
+        if (i == n - 1) fetch_ahead();
+        if (!ok) break;
+        if (!idle) {
+          const int u0 = (it.kt0 + plan.tile(w, i)) * kKeys;
+          uint32_t s[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          top[c] = __uint_as_float(s[c]);
+          for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, s + 32 * c);
+          tc::wait_ld();
+          if (warp_first - u0 < kKeys - 1) {                      // on the border
+            const int seen = last - u0;
 #pragma unroll
-          for (int e = 4; e < 128; e += 4) top[c] = fmaxf(top[c], __uint_as_float(s[e + c]));
+            for (int c = 0; c < 128; ++c)
+              if (c > seen) s[c] = 0xff800000u;
+          }
+          float top[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            top[c] = __uint_as_float(s[c]);
+#pragma unroll
+            for (int e = 4; e < 128; e += 4) top[c] = fmaxf(top[c], __uint_as_float(s[e + c]));
+          }
+          const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+          if (__any_sync(0xffffffffu, now > m + kLazy)) {
+            // s_full follows the products before it: O is complete up to tile i - 1
+            const float next = now > m + kLazy ? now : m;
+            const float f = next == -INFINITY ? 1.f : exp2f(m - next);
+            m = next;
+            l *= f;
+            if (i > 0) {
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tc::ld32(to + c, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tc::st32(to + c, o);
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;             // no key of this row yet
+          const float2 ref2 = make_float2(-ref, -ref);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float2 x = make_float2(__uint_as_float(s[64 * h + 2 * e]),
+                                     __uint_as_float(s[64 * h + 2 * e + 1]));
+              x = tc::fma2(x, scale2, ref2);
+              x.x = tc::exp2_approx(x.x);
+              x.y = tc::exp2_approx(x.y);
+              sum[e & 1] = tc::add2(sum[e & 1], x);
+              p[e] = tc::pack_bf16(x.x, x.y);
+            }
+            tc::st32(ts + 32 * h, p);
+          }
+          sum[0] = tc::add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+          tc::wait_st();
         }
-        const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-        if (__any_sync(0xffffffffu, now > m + kLazy)) {
-          // s_full(i) follows the products before it: O is complete up to tile i - 1
-          const float next = now > m + kLazy ? now : m;
-          const float f = next == -INFINITY ? 1.f : exp2f(m - next);
-          m = next;
-          l *= f;
-          if (i > 0) {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(p_full + w);
+      }
+      if (!ok) break;
+      if (n == 0) fetch_ahead();
+      if (!ok) break;
+      if (rows_ahead) rows_ready();
+      // ---- output
+      const bool join = !plan.wide && plan.n1 > 0;
+      if (n > 0) ok = mbar_wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
+      if (!ok) break;
+      if (join && w == 1) {
+        box[r] = m;
+        box[128 + r] = l;
+        __syncwarp();
+        if (lane == 0) arrive(joined);
+      }
+      if (n > 0) ++items_seen;
+      if (join && w == 0) {
+        // the other warpgroup's last product: it has one for each of this one's joins
+        ok = mbar_wait_bounded(joined, joins_seen & 1, ctx.wait_ns);
+        if (!ok) break;
+        ++joins_seen;
+      }
+      if (!idle && (plan.wide || w == 0)) {
+        tc::fence_after();
+        float f0 = 1.f, f1 = 0.f;
+        if (join) {
+          const float m1 = box[r];
+          const float both = fmaxf(m, m1);
+          f0 = m == -INFINITY ? 0.f : exp2f(m - both);
+          f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - both);
+          l = l * f0 + box[128 + r] * f1;
+          m = both;
+        }
+        const bool mine = row < rows, whole = it.part < 0;
+        const int64_t at_row = (int64_t)(it.row0 + (row >> log_g)) * a.Hq + it.g * a.G +
+                               (row & (a.G - 1));
+        const int64_t at_part = (int64_t)it.part * a.part_rows + row;
+        if (whole) {                               // every row sees its own token: l > 0
+          const float inv = 1.f / l;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        if (n > 0) {
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tc::ld32(to + c, o);
+          for (int c = 0; c < D; c += 32) {
+            uint32_t raw[32];
+            float o[32];
+            tc::ld32(to + c, raw);
+            tc::wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]) * f0;
+            if (join) {
+              tc::ld32(to + 128 + c, raw);
               tc::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc::st32(to + c, o);
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(raw[e]), f1, o[e]);
+            }
+            if (!mine) continue;
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at_row * D + c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                dst[e] = make_uint4(tc::pack_bf16(o[8 * e], o[8 * e + 1]),
+                                    tc::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                    tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                                    tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+            } else {
+              float4* dst = reinterpret_cast<float4*>(a.part_acc + at_part * D + c);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;               // no key of this row yet
-        const float2 ref2 = make_float2(-ref, -ref);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 x = make_float2(__uint_as_float(s[64 * h + 2 * e]),
-                                   __uint_as_float(s[64 * h + 2 * e + 1]));
-            x = tc::fma2(x, scale2, ref2);
-            x.x = tc::exp2_approx(x.x);
-            x.y = tc::exp2_approx(x.y);
-            sum[e & 1] = tc::add2(sum[e & 1], x);
-            p[e] = tc::pack_bf16(x.x, x.y);
-          }
-          tc::st32(ts + 32 * h, p);
+        if (mine && whole && a.lse != nullptr) a.lse[at_row] = (m + log2f(l)) * kLn2;
+        if (mine && !whole) {                      // m = -inf: the part has no key for this row
+          a.part_ml[2 * at_part] = m;
+          a.part_ml[2 * at_part + 1] = l;
         }
-        sum[0] = tc::add2(sum[0], sum[1]);
-        l += sum[0].x + sum[0].y;
-        tc::wait_st();
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) arrive(p_full + w);
+      if (lane == 0) {
+        if (plan.wide ? n > 0 : w == 0) arrive(o_free + w);
+        if (join && w == 0) arrive(o_free + 1);
+      }
+      item_done(j);
     }
-    // ---- output
-    if (ok && n > 0) ok = mbar_wait_bounded(o_done + w, 0, ctx.wait_ns);
-    const bool join = !plan.wide && plan.n1 > 0;
-    if (join) {
-      // the ring is free once both warpgroups' products are done
-      if (ok) ok = mbar_wait_bounded(o_done + (w ^ 1), 0, ctx.wait_ns);
-      tc::fence_after();
-      float* box = reinterpret_cast<float*>(ring);                // [D + 2][128]
-      if (w == 1 && ok && !idle) {
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tc::ld32(to + c, o);
-          tc::wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) box[(c + e) * 128 + r] = __uint_as_float(o[e]);
-        }
-        box[D * 128 + r] = m;
-        box[(D + 1) * 128 + r] = l;
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-    }
-    if (!ok) {
-      if (lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
-    } else if (!idle && (plan.wide || w == 0)) {
-      tc::fence_after();
-      const float* box = reinterpret_cast<const float*>(ring);
-      float f0 = 1.f, f1 = 0.f;
-      if (join) {
-        const float m1 = box[D * 128 + r];
-        const float both = fmaxf(m, m1);
-        f0 = m == -INFINITY ? 0.f : exp2f(m - both);
-        f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - both);
-        l = l * f0 + box[(D + 1) * 128 + r] * f1;
-        m = both;
-      }
-      const int64_t at = (int64_t)(it.row0 + (row >> log_g)) * a.Hq + it.g * a.G +
-                         (row & (a.G - 1));
-      const bool mine = row < rows;
-      if (a.S == 1) f0 /= l, f1 /= l;            // every row sees its own token: l > 0
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t raw[32];
-        float o[32];
-        if (n > 0) {
-          tc::ld32(to + c, raw);
-          tc::wait_ld();
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          o[e] = n > 0 ? __uint_as_float(raw[e]) * f0 : 0.f;
-          if (join) o[e] = fmaf(box[(c + e) * 128 + r], f1, o[e]);
-        }
-        if (!mine) continue;
-        if (a.S == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * D + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(tc::pack_bf16(o[8 * e], o[8 * e + 1]),
-                                tc::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
-                                tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.part_acc + (at * a.S + it.s) * D + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        }
-      }
-      if (mine) {
-        if (a.S == 1) {
-          if (a.lse != nullptr) a.lse[at] = (m + log2f(l)) * kLn2;
-        } else {
-          a.part_ml[(at * a.S + it.s) * 2] = m;
-          a.part_ml[(at * a.S + it.s) * 2 + 1] = l;
-        }
-      }
-    }
-    tc::fence_before();
+    if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
   } else {
     tc::fewer_regs<kRegsOther>();
-    if (warp == kMmaWarp && lane == 0 && plan.n > 0) {
+    if (warp == kMmaWarp) {
       // ---- products
       constexpr uint32_t id_s = tc::idesc(kKeys, false), id_o = tc::idesc(D, true);
-      const uint32_t q_addr = smem_addr(sm + C::OFF_Q), ring_addr = smem_addr(ring);
-      bool ok = mbar_wait_bounded(q_full, 0, ctx.wait_ns);
-      auto landed = [&](int slot) {
-        return mbar_wait_bounded(full + slot % C::STAGES, (slot / C::STAGES) & 1, ctx.wait_ns);
+      const uint64_t q_desc = tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q)), 16);
+      const uint64_t k_desc = tc::smem_desc(uniform(smem_addr(ring)), 16);
+      const uint64_t v_desc = tc::smem_desc(uniform(smem_addr(ring)), 16384);
+      bool ok = true;
+      int base = 0;                                  // ring slots of the items before
+      int seen0 = 0, seen1 = 0, items0 = 0, items1 = 0;
+      // Two barriers at once: both are tested before either is waited for.
+      auto wait2 = [&](uint64_t* x, int px, uint64_t* y, int py) {
+        const bool rx = mbar_try_wait(x, px), ry = mbar_try_wait(y, py);
+        bool good = ok;
+        if (!rx) good = good && mbar_wait_bounded(x, px, ctx.wait_ns);
+        if (!ry) good = good && mbar_wait_bounded(y, py, ctx.wait_ns);
+        ok = __all_sync(0xffffffffu, good);
       };
-      auto scores = [&](int w, int i) {
-        const int slot = plan.k_slot(plan.tile(w, i));
-        ok = ok && landed(slot);
-        if (!ok) return;
-        tc::fence_after();
-        const uint32_t qa = q_addr + (plan.wide ? w * C::TILE_BYTES : 0);
-        const uint32_t ka = ring_addr + (slot % C::STAGES) * C::TILE_BYTES;
+      for (int j = 0;; ++j) {
+        ok = __all_sync(0xffffffffu, item_ready(j));
+        if (!ok) break;
+        Plan plan(items[j % kItems], log_g);
+        if (plan.n <= 0) break;
+        item_done(j);
+        plan.wide = uniform(plan.wide);
+        plan.n = uniform(plan.n);
+        plan.n0 = uniform(plan.n0);
+        plan.n1 = uniform(plan.n1);
+        auto scores = [&](int w, int i) {
+          const int slot = base + plan.k_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+          const int items = w == 0 ? items0 : items1;
+          if (i == 0)
+            wait2(q_full + w, items & 1, full + stage, (slot / C::STAGES) & 1);
+          else if (!plan.wide || w == 0 || i >= plan.n0)         // else it was seen for w = 0
+            wait2(full + stage, (slot / C::STAGES) & 1, full + stage, (slot / C::STAGES) & 1);
+          if (!ok) return;
+          tc::fence_after();
+          if (tc::elect()) {
+            const uint64_t qd = q_desc + (uint64_t)(w * (C::TILE_BYTES >> 4));
+            const uint64_t kd = k_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          tc::mma_ss(tmem + w * 128, tc::smem_desc(qa + off, 16), tc::smem_desc(ka + off, 16),
-                     id_s, k > 0);
-        }
-        tc::commit(s_full + w);
-        if (!plan.wide || w == 1) tc::commit(empty + slot % C::STAGES);
-      };
-      auto values = [&](int w, int i) {
-        const int slot = plan.v_slot(plan.tile(w, i));
-        ok = ok && mbar_wait_bounded(p_full + w, i & 1, ctx.wait_ns) && landed(slot);
-        if (!ok) return;
-        tc::fence_after();
-        const uint32_t va = ring_addr + (slot % C::STAGES) * C::TILE_BYTES;
+            for (int k = 0; k < D / 16; ++k) {
+              const int step = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+              tc::mma_ss(tmem + w * 128, qd + step, kd + step, id_s, k > 0);
+            }
+            tc::commit(s_full + w);
+            if (!plan.wide || w == 1) tc::commit(empty + stage);
+          }
+          __syncwarp();
+        };
+        auto values = [&](int w, int i) {
+          const int slot = base + plan.v_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+          int& seen = w == 0 ? seen0 : seen1;
+          const int items = w == 0 ? items0 : items1;
+          wait2(p_full + w, seen & 1, full + stage, (slot / C::STAGES) & 1);
+          ++seen;
+          if (i == 0 && items > 0)                   // O of the item before has been read
+            wait2(o_free + w, (items - 1) & 1, o_free + w, (items - 1) & 1);
+          if (!ok) return;
+          tc::fence_after();
+          if (tc::elect()) {
+            const uint64_t vd = v_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          tc::mma_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8,
-                     tc::smem_desc(va + k * 2048, 16384), id_o, i > 0 || k > 0);
-        if (!plan.wide || w == 1) tc::commit(empty + slot % C::STAGES);
-        if (i + 1 == plan.tiles(w)) tc::commit(o_done + w);
-      };
-      for (int w = 0; w < 2; ++w)
-        if (plan.tiles(w) > 0) scores(w, 0);
-      for (int i = 0; ok && i < max(plan.n0, plan.n1); ++i)
-        for (int w = 0; w < 2; ++w) {
-          if (i < plan.tiles(w)) values(w, i);
-          if (i + 1 < plan.tiles(w)) scores(w, i + 1);
+            for (int k = 0; k < kKeys / 16; ++k)
+              tc::mma_ts(tmem + 256 + w * 128, tmem + w * 128 + k * 8, vd + k * (2048 >> 4), id_o,
+                         i > 0 || k > 0);
+            if (!plan.wide || w == 1) tc::commit(empty + stage);
+            if (i + 1 == plan.tiles(w)) tc::commit(o_done + w);
+          }
+          __syncwarp();
+        };
+        if (plan.n0 > 0) scores(0, 0);
+        if (plan.n1 > 0) scores(1, 0);
+        const int most = max(plan.n0, plan.n1);
+        for (int i = 0; ok && i < most; ++i) {
+          if (i < plan.n0) values(0, i);
+          if (i + 1 < plan.n0) scores(0, i + 1);
+          if (i < plan.n1) values(1, i);
+          if (i + 1 < plan.n1) scores(1, i + 1);
         }
+        items0 += plan.n0 > 0;
+        items1 += plan.n1 > 0;
+        if (!ok) break;
+        base += 2 * plan.n;
+      }
+      __syncwarp();
       if (!ok) {
-        flag(ctx, KV_DEVERR_TIMEOUT);
-        tc::commit(drained);
+        if (tc::elect()) {
+          flag(ctx, KV_DEVERR_TIMEOUT);
+          tc::commit(drained);
+        }
         (void)mbar_wait_bounded(drained, 0, ctx.wait_ns);
       }
     } else if (warp == kLoadWarp) {
@@ -386,66 +503,110 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       const int PS = d.page_size, per_tile = kKeys / PS;
       const int copies = per_tile * C::HALVES;
       const int page = lane % per_tile, half = lane / per_tile;
-      const uint32_t box = (uint32_t)PS * 128;
-      const uint32_t dst = smem_addr(ring) + half * 16384 + page * box;
-      const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
+      const uint32_t box_bytes = (uint32_t)PS * 128;
+      const uint32_t dst = smem_addr(ring) + half * 16384 + page * box_bytes;
       bool ok = true;
-      int used = 0;
-      auto load = [&](const CUtensorMap* map, int t, int slot, bool values) {
-        if (!ok) return;
-        const int stage = slot % C::STAGES;
-        const int64_t key = (int64_t)(it.kt0 + t) * kKeys + page * PS;   // of the lane's page
-        int P = -1;
-        const bool wanted = lane < copies && key < keys;
-        if (wanted) {
-          P = __ldg(table + (int)(key / PS));
-          if (P < 0 || P >= d.num_phys_pages) {
-            flag(ctx, KV_DEVERR_BAD_PAGE);
-            P = -1;
+      int base = 0, used = 0, tails = 0;
+      for (int j = 0;; ++j) {
+        ok = __all_sync(0xffffffffu, ok && item_ready(j));
+        if (!ok) break;
+        const PrefillItem it = items[j % kItems];
+        if (it.kt0 >= it.kt1) break;
+        item_done(j);
+        const Plan plan(it, log_g);
+        const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
+        const int keys = it.pos0 + it.n_tok;         // keys from here on are nobody's
+        const int pages = (int)(((int64_t)keys + PS - 1) / PS);
+        // The table's entries 32 at a time, one to a lane: those of the tile being loaded, the
+        // ones before (V tiles come up to two tiles after their K tile) and the ones ahead.
+        auto entries = [&](int chunk) {
+          const int p = chunk * 32 + lane;
+          int P = -1;
+          if (p < pages) {
+            P = __ldg(table + p);
+            if (P < 0 || P >= d.num_phys_pages) {
+              flag(ctx, KV_DEVERR_BAD_PAGE);
+              P = -1;
+            }
+          }
+          return P;
+        };
+        int chunk = it.kt0 * per_tile / 32;
+        int e0 = -1, e1 = entries(chunk), e2 = entries(chunk + 1);
+        auto load = [&](const CUtensorMap* map, int t, bool values) {
+          if (!ok) return;
+          const int first = (it.kt0 + t) * per_tile;
+          if (first / 32 > chunk) {
+            e0 = e1;
+            e1 = e2;
+            e2 = entries(++chunk + 1);
+          }
+          int P = __shfl_sync(0xffffffffu, first / 32 == chunk ? e1 : e0, (first + page) & 31);
+          if (lane >= copies) P = -1;
+          const int slot = base + (values ? plan.v_slot(t) : plan.k_slot(t));
+          const int stage = slot % C::STAGES;
+          if (slot >= C::STAGES)
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(
+                empty + stage, (slot / C::STAGES - 1) & 1, ctx.wait_ns));
+          if (!ok) return;
+          // the item's last key lies inside this tile: the V rows after it become zeros
+          const int valid = min(kKeys, keys - (it.kt0 + t) * kKeys);
+          const bool tail = values && valid < kKeys;
+          uint64_t* land = tail ? v_land : full + stage;
+          const int boxes = __popc(__ballot_sync(0xffffffffu, P >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(land, boxes * box_bytes);
+          __syncwarp();
+          if (P >= 0)
+            tma_page(dst + stage * C::TILE_BYTES, map, half * 64,
+                     (P * d.num_kv_heads + it.g) * PS, land);
+          used = slot + 1;
+          if (!tail) return;
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(v_land, tails & 1, ctx.wait_ns));
+          ++tails;
+          uint8_t* tile = ring + stage * C::TILE_BYTES;
+          for (int i = valid * 8 + lane; i < kKeys * 8; i += 32)
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h)
+              *reinterpret_cast<uint4*>(tile + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive(full + stage);
+        };
+        if (plan.wide) {
+          for (int t = 0; t < plan.n; ++t) {
+            load(&map_k, t, false);
+            load(&map_v, t, true);
+          }
+        } else {
+          for (int t = 0; t < min(2, plan.n); ++t) load(&map_k, t, false);
+          for (int t = 0; t < plan.n; ++t) {
+            load(&map_v, t, true);
+            if (t + 2 < plan.n) load(&map_k, t + 2, false);
           }
         }
-        if (slot >= C::STAGES)
-          ok = mbar_wait_bounded(empty + stage, (slot / C::STAGES - 1) & 1, ctx.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        // the item's last key lies inside this tile: the V rows after it become zeros
-        const int valid = (int)min((int64_t)kKeys, (int64_t)keys - (int64_t)(it.kt0 + t) * kKeys);
-        const bool tail = values && valid < kKeys;
-        uint64_t* land = tail ? v_land : full + stage;
-        const int boxes = __popc(__ballot_sync(0xffffffffu, P >= 0));
-        if (lane == 0) mbar_arrive_expect_tx(land, boxes * box);
-        __syncwarp();
-        if (P >= 0)
-          tma_page(dst + stage * C::TILE_BYTES, map, half * 64,
-                   (P * d.num_kv_heads + it.g) * PS, land);
-        used = slot + 1;
-        if (!tail) return;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(v_land, 0, ctx.wait_ns));
-        uint8_t* tile = ring + stage * C::TILE_BYTES;
-        for (int i = valid * 8 + lane; i < kKeys * 8; i += 32)
-#pragma unroll
-          for (int h = 0; h < C::HALVES; ++h)
-            *reinterpret_cast<uint4*>(tile + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive(full + stage);
-      };
-      if (plan.wide) {
-        for (int t = 0; t < plan.n; ++t) {
-          load(&map_k, t, plan.k_slot(t), false);
-          load(&map_v, t, plan.v_slot(t), true);
-        }
-      } else {
-        for (int t = 0; t < min(2, plan.n); ++t) load(&map_k, t, plan.k_slot(t), false);
-        for (int t = 0; t < plan.n; ++t) {
-          load(&map_v, t, plan.v_slot(t), true);
-          if (t + 2 < plan.n) load(&map_k, t + 2, plan.k_slot(t + 2), false);
-        }
+        base += 2 * plan.n;
       }
       if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
       // no copy may be in flight when the block's shared memory goes
       for (int slot = max(0, used - C::STAGES); slot < used; ++slot)
         (void)mbar_wait_bounded(full + slot % C::STAGES, (slot / C::STAGES) & 1, ctx.wait_ns);
+    } else if (warp == kItemWarp) {
+      // ---- the block's items, and after the last one an item without key tiles
+      ItemWalk<MmaShape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
+      bool ok = true, more = true;
+      for (int j = 0; ok && more; ++j) {
+        PrefillItem it;
+        more = walk.next(&it);
+        if (!more) it.kt0 = it.kt1 = 0;
+        if (j >= kItems)
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(item_free + j % kItems,
+                                                         (j / kItems - 1) & 1, ctx.wait_ns));
+        if (ok && lane == 0) {
+          items[j % kItems] = it;
+          arrive(item_full + j % kItems);
+        }
+      }
+      if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
     }
     __syncwarp();
   }
@@ -472,10 +633,7 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(1, std::memory_order_release);
   }
-  const int log_g = a.G == 1 ? 0 : a.G == 2 ? 1 : a.G == 4 ? 2 : 3;
-  const long items = work_numbers(pr.cu, pr.total, d.batch, kRows / a.G, 1);
-  dim3 grid((unsigned)(items * d.num_kv_heads), a.S);
-  return launch_pdl(kern, grid, dim3(kThreads), C::SMEM, s, mk, mv, d, pr, a, log_g, ctx);
+  return launch_pdl(kern, dim3(a.NC), dim3(kThreads), C::SMEM, s, mk, mv, d, pr, a, ctx);
 }
 
 }  // namespace

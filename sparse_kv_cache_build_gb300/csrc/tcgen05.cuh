@@ -104,6 +104,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(add) : "memory");
 }
 
+// True in one lane of a converged warp. The products are issued under it, in code the whole
+// warp walks: descriptors then stay in uniform registers. Issued by `lane == 0` in divergent
+// code instead, each product cost about 110 cycles of its issuing thread against the 64 it
+// takes to run.
+__device__ __forceinline__ bool elect() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok));
+  return ok != 0;
+}
+
 // A warpgroup's registers per thread, from the block's launch total.
 template <int N> __device__ __forceinline__ void more_regs() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));

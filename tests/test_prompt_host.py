@@ -38,12 +38,12 @@ def append(lib, d=None, **kw):
 
 
 def attn(lib, d=None, **kw):
-    a = dict(q=512, q_stride=1024, Hq=8, cu=64, total=3, scale=0.1, splits=1, out=1024, lse=NULL,
+    a = dict(q=512, q_stride=1024, Hq=8, cu=64, total=3, scale=0.1, shares=1, out=1024, lse=NULL,
              ws=NULL, bytes=0)
     a.update(kw)
     return lib.kv_prefill_attn(
         ctypes.byref(d or desc()), a["q"], a["q_stride"], a["Hq"], a["cu"], a["total"],
-        a["scale"], a["splits"], a["out"], a["lse"], a["ws"], a["bytes"], NULL)
+        a["scale"], a["shares"], a["out"], a["lse"], a["ws"], a["bytes"], NULL)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -73,7 +73,7 @@ def test_append_refuses_bad_caches_and_accepts_nothing_to_do(lib):
 @pytest.mark.parametrize("kw,status", [
     (dict(q=NULL), -1), (dict(out=NULL), -1), (dict(total=-1), -1), (dict(cu=NULL), -1),
     (dict(scale=0.0), -1), (dict(scale=-1.0), -1), (dict(scale=math.inf), -1),
-    (dict(scale=math.nan), -1), (dict(splits=-1), -1), (dict(splits=65), -1), (dict(Hq=6), -2),
+    (dict(scale=math.nan), -1), (dict(shares=-1), -1), (dict(shares=1025), -1), (dict(Hq=6), -2),
     (dict(Hq=7), -1), (dict(q_stride=1016), -1), (dict(q_stride=1028), -7), (dict(q=520), -7),
     (dict(out=1032), -7),
 ])
@@ -89,13 +89,13 @@ def test_attention_accepts_nothing_to_do(lib):
 def test_workspace_size_formula(lib):
     d = desc()
     r256 = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    for T, S in ((5, 2), (100, 7)):
-        rows = T * 8 * S
+    for T, S in ((5, 2), (100, 7)):               # tiles of 256 rows, four heads to a token
+        rows = 2 * S * min(256, T * 4)
         want = r256(rows * 128 * 4) + r256(rows * 8)
         assert lib.kv_prefill_attn_workspace_size(ctypes.byref(d), 8, T, S) == want
         assert lib.kv_workspace_size(4, ctypes.byref(d), 8, T, S) == want
     assert lib.kv_prefill_attn_workspace_size(ctypes.byref(d), 8, 100, 1) == 0
-    for bad in ((0, 5, 2), (6, 5, 2), (8, -1, 2), (8, 5, 65), (8, 5, -1)):
+    for bad in ((0, 5, 2), (6, 5, 2), (8, -1, 2), (8, 5, 1025), (8, 5, -1)):
         assert lib.kv_prefill_attn_workspace_size(ctypes.byref(d), *bad) == 0
     assert lib.kv_prefill_attn_workspace_size(NULL, 8, 5, 2) == 0
 
