@@ -42,6 +42,24 @@ bool encode_pool_map(CUtensorMap* map, const void* pool, const kv_cache_desc& d)
          CUDA_SUCCESS;
 }
 
+}  // namespace
+
+bool rows_tensor_map(CUtensorMap* map, const void* rows, int64_t stride, int heads, int head_dim,
+                     int total, int box_heads, int box_tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)total};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t elem_strides[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(rows), dims, strides, box,
+            elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+namespace {
+
 // Encoded maps of recently used pools: a map depends only on the pool's address and shape,
 // so a decode loop over one cache encodes its two maps once instead of on every launch.
 struct MapEntry {

@@ -297,6 +297,11 @@ cudaError_t launch_fused_step(const kv_cache_desc& d, int G, int CL, const void*
 // (thread-safe); false if it cannot be encoded.
 bool pool_tensor_map(CUtensorMap* map, const void* pool, const kv_cache_desc& d);
 
+// The 3-D TMA tensor map of packed bf16 rows [total][heads][head_dim] with `stride` elements
+// between tokens: boxes of 64 columns x box_heads heads x box_tokens tokens, 128-byte swizzle.
+bool rows_tensor_map(CUtensorMap* map, const void* rows, int64_t stride, int heads, int head_dim,
+                     int total, int box_heads, int box_tokens);
+
 // Dynamic shared memory bytes of the attention kernel for this shape (0 = unsupported).
 size_t split_attn_smem_bytes(int dtype, int head_dim, int group_size);
 

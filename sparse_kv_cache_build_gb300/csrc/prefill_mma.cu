@@ -36,7 +36,7 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 384;          // two softmax warpgroups, then products and loads
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kRowWarp = 11;
 constexpr int kItems = 4;              // items known ahead
 constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
@@ -46,11 +46,12 @@ constexpr float kLazy = 8.f;           // log2 of the growth that forces a resca
 template <int D> struct Cfg {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE_BYTES = HALVES * 128 * 128;         // 128 rows of D bf16
-  static constexpr int STAGES = D == 128 ? 5 : 8;
+  static constexpr int STAGES = D == 128 ? 4 : 8;
   static constexpr size_t OFF_Q = 0;                            // from a 1024-aligned base
   static constexpr size_t OFF_RING = 2 * TILE_BYTES;
-  static constexpr size_t OFF_BAR = OFF_RING + (size_t)STAGES * TILE_BYTES;
-  static constexpr int BARS = 2 * STAGES + 13 + 2 * kItems;
+  static constexpr size_t OFF_OUT = OFF_RING + (size_t)STAGES * TILE_BYTES;   // 4 KB a warp
+  static constexpr size_t OFF_BAR = OFF_OUT + 8 * 4096;
+  static constexpr int BARS = 2 * STAGES + 15 + 2 * kItems;
   static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;        // TMEM base, then [2][128] (m, l)
   static constexpr size_t OFF_ITEMS = OFF_MISC + 8;
   static constexpr size_t OFF_ML = OFF_ITEMS + kItems * sizeof(PrefillItem);
@@ -99,10 +100,14 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// 16 bytes from global to shared memory; zeros when `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+// 64 columns of a tile's rows: G heads of 128 / G tokens of the query tensor [T][Hq][D].
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head,
+                                         int token, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token),
+        "r"(smem_addr(bar)) : "memory");
 }
 
 // A value that is the same in every lane, said so that the compiler keeps it, and what follows
@@ -113,6 +118,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
+                   const __grid_constant__ CUtensorMap map_q,
                    const __grid_constant__ kv_cache_desc d,
                    const __grid_constant__ PackedRows pr, const __grid_constant__ PrefillArgs a,
                    const __grid_constant__ DevCtx ctx) {
@@ -128,7 +134,8 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* s_full = bar + 2 * C::STAGES;        // [2] S of a warpgroup is in TMEM
   uint64_t* p_full = s_full + 2;                 // [2] its P is in TMEM, O rescaled
   uint64_t* q_full = p_full + 2;                 // [2] its rows are in shared memory
-  uint64_t* o_done = q_full + 2;                 // [2] its last product of an item is done
+  uint64_t* q_free = q_full + 2;                 // [2] its last scores of an item are done
+  uint64_t* o_done = q_free + 2;                 // [2] its last product of an item is done
   uint64_t* o_free = o_done + 2;                 // [2] its O has been read
   uint64_t* joined = o_free + 2;                 // the second warpgroup's (m, l) are written
   uint64_t* v_land = joined + 1;                 // the last V tile, before its tail is zeroed
@@ -149,13 +156,14 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 1);
       mbar_init(p_full + w, 4);                  // one arrival per softmax warp
-      mbar_init(q_full + w, 4);
+      mbar_init(q_full + w, 1);
+      mbar_init(q_free + w, 1);
       mbar_init(o_done + w, 1);
       mbar_init(o_free + w, 4);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_free + i, 10);              // eight softmax warps, products, loads
+      mbar_init(item_free + i, 11);              // eight softmax warps, products, two of loads
     }
     mbar_init(joined, 4);
     mbar_init(v_land, 1);
@@ -173,7 +181,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
-  // Item number j of the block, for the warp that asks; its last has no key tiles.
+  // Item number j of the block, for the warp that asks; the last one has no key tiles.
   auto item_ready = [&](int j) {
     return mbar_wait_bounded(item_full + j % kItems, (j / kItems) & 1, ctx.wait_ns);
   };
@@ -191,30 +199,6 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     bool ok = true;
     int tiles_seen = 0, items_seen = 0, joins_seen = 0;           // for the barriers' phases
 
-    // This warpgroup's rows into 128-byte swizzled shared rows (zeros past the item's last).
-    auto fetch_rows = [&](const PrefillItem& it, bool wide) {
-      constexpr int CH = D / 8;                  // 16-byte chunks of a row
-      const uint16_t* q = static_cast<const uint16_t*>(a.q);
-      const uint32_t dst = smem_addr(sm + C::OFF_Q) + w * C::TILE_BYTES;
-      const int rows = it.n_tok << log_g;
-#pragma unroll 4
-      for (int i = r; i < 128 * CH; i += 128) {
-        const int row = i / CH, c = i % CH, src = wide ? w * 128 + row : row;
-        const bool have = src < rows;
-        const int tok = have ? src >> log_g : 0, head = have ? src & (a.G - 1) : 0;
-        copy16(dst + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4),
-               q + (int64_t)(it.row0 + tok) * a.q_stride + (int64_t)(it.g * a.G + head) * D + c * 8,
-               have ? 16 : 0);
-      }
-    };
-    auto rows_ready = [&] {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      tc::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive(q_full + w);
-    };
-
-    bool first = true;
     for (int j = 0;; ++j) {
       ok = item_ready(j);
       if (!ok) break;
@@ -222,22 +206,6 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (it.kt0 >= it.kt1) break;
       const Plan plan(it, log_g);
       const int n = plan.tiles(w), rows = it.n_tok << log_g;
-      if (first) {
-        first = false;
-        if (n > 0) {
-          fetch_rows(it, plan.wide);
-          rows_ready();
-        }
-      }
-      bool rows_ahead = false;
-      auto fetch_ahead = [&] {                   // the next item's rows, if it has any for w
-        ok = item_ready(j + 1);
-        if (!ok) return;
-        const PrefillItem next = items[(j + 1) % kItems];
-        const Plan plan2(next, log_g);
-        rows_ahead = plan2.tiles(w) > 0;
-        if (rows_ahead) fetch_rows(next, plan2.wide);
-      };
       const int row = plan.wide ? w * 128 + r : r;
       const int last = it.pos0 + (row >> log_g);                  // the row's last key
       const int warp_row = row - lane;
@@ -249,9 +217,6 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         if (!ok) break;
         ++tiles_seen;
         tc::fence_after();
-        // the item's last scores are done: its rows may be overwritten
-        if (i == n - 1) fetch_ahead();
-        if (!ok) break;
         if (!idle) {
           const int u0 = (it.kt0 + plan.tile(w, i)) * kKeys;
           uint32_t s[128];
@@ -317,9 +282,6 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         if (lane == 0) arrive(p_full + w);
       }
       if (!ok) break;
-      if (n == 0) fetch_ahead();
-      if (!ok) break;
-      if (rows_ahead) rows_ready();
       // ---- output
       const bool join = !plan.wide && plan.n1 > 0;
       if (n > 0) ok = mbar_wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
@@ -357,36 +319,70 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           f0 *= inv;
           f1 *= inv;
         }
-        if (n > 0) {
+        // Through 4 KB of the warp's own shared memory, 128 bytes of each of its 32 rows at a
+        // time, so that eight lanes write one row's 128 bytes: a lane per row would touch 32
+        // lines with every store (6000 cycles an item against 1500).
+        uint8_t* stage = sm + C::OFF_OUT + warp * 4096;
+        auto columns = [&](int c, float* o) {      // 32 columns from c on, scaled and joined
+          uint32_t raw[32];
+          tc::ld32(to + c, raw);
+          tc::wait_ld();
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t raw[32];
-            float o[32];
-            tc::ld32(to + c, raw);
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]) * f0;
+          if (join) {
+            tc::ld32(to + 128 + c, raw);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]) * f0;
-            if (join) {
-              tc::ld32(to + 128 + c, raw);
-              tc::wait_ld();
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(raw[e]), f1, o[e]);
+          }
+        };
+        auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) =
+              make_uint4(x, y, z, u);
+        };
+        auto flush = [&](uint8_t* base, int64_t row_bytes, bool packed) {
+          __syncwarp();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(raw[e]), f1, o[e]);
-            }
-            if (!mine) continue;
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at_row * D + c);
+          for (int e = 0; e < 8; ++e) {
+            const int k = 4 * e + (lane >> 3), chunk = lane & 7, out_row = warp_row + k;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + k * 128 +
+                                                            ((chunk ^ (k & 7)) << 4));
+            const int64_t index = packed ? (int64_t)(out_row >> log_g) * a.Hq + (out_row & (a.G - 1))
+                                         : out_row;
+            if (out_row < rows) *reinterpret_cast<uint4*>(base + index * row_bytes + chunk * 16) = v;
+          }
+          __syncwarp();
+        };
+        if (n > 0 && whole) {
+          uint8_t* out = reinterpret_cast<uint8_t*>(
+              static_cast<uint16_t*>(a.out) + ((int64_t)it.row0 * a.Hq + it.g * a.G) * D);
+#pragma unroll
+          for (int c = 0; c < D; c += 64) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float o[32];
+              columns(c + 32 * h, o);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                dst[e] = make_uint4(tc::pack_bf16(o[8 * e], o[8 * e + 1]),
-                                    tc::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                    tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
-                                    tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-            } else {
-              float4* dst = reinterpret_cast<float4*>(a.part_acc + at_part * D + c);
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                put(4 * h + e, tc::pack_bf16(o[8 * e], o[8 * e + 1]),
+                    tc::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                    tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                    tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
             }
+            flush(out + c * 2, D * 2, true);
+          }
+        } else if (n > 0) {
+          uint8_t* out = reinterpret_cast<uint8_t*>(a.part_acc +
+                                                    (int64_t)it.part * a.part_rows * D);
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            columns(c, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              put(e, __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                  __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+            flush(out + c * 4, D * 4, false);
           }
         }
         if (mine && whole && a.lse != nullptr) a.lse[at_row] = (m + log2f(l)) * kLn2;
@@ -451,6 +447,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
               tc::mma_ss(tmem + w * 128, qd + step, kd + step, id_s, k > 0);
             }
             tc::commit(s_full + w);
+            if (i + 1 == plan.tiles(w)) tc::commit(q_free + w);
             if (!plan.wide || w == 1) tc::commit(empty + stage);
           }
           __syncwarp();
@@ -607,6 +604,40 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         }
       }
       if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
+    } else if (warp == kRowWarp) {
+      // ---- rows: a warpgroup's tile of an item, as soon as the item before is done with it
+      bool ok = true;
+      int loaded[2] = {0, 0};
+      for (int j = 0;; ++j) {
+        ok = __all_sync(0xffffffffu, item_ready(j));
+        if (!ok) break;
+        const PrefillItem it = items[j % kItems];
+        if (it.kt0 >= it.kt1) break;
+        item_done(j);
+        const Plan plan(it, log_g);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (plan.tiles(w) == 0) continue;
+          if (loaded[w] > 0)
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(q_free + w, (loaded[w] - 1) & 1,
+                                                                ctx.wait_ns));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(q_full + w, C::TILE_BYTES);
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h)
+              tma_rows(smem_addr(sm + C::OFF_Q) + w * C::TILE_BYTES + h * 16384, &map_q, 64 * h,
+                       it.g * a.G, it.row0 + (plan.wide ? (w * 128) >> log_g : 0), q_full + w);
+          }
+          __syncwarp();
+          ++loaded[w];
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (loaded[w] > 0) (void)mbar_wait_bounded(q_full + w, (loaded[w] - 1) & 1, ctx.wait_ns);
     }
     __syncwarp();
   }
@@ -619,8 +650,9 @@ template <int D>
 cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
                      DevCtx ctx, cudaStream_t s) {
   using C = Cfg<D>;
-  CUtensorMap mk, mv;
-  if (!pool_tensor_map(&mk, d.k_pool, d) || !pool_tensor_map(&mv, d.v_pool, d))
+  CUtensorMap mk, mv, mq;
+  if (!pool_tensor_map(&mk, d.k_pool, d) || !pool_tensor_map(&mv, d.v_pool, d) ||
+      !rows_tensor_map(&mq, a.q, a.q_stride, a.Hq, D, pr.total, a.G, 128 / a.G))
     return cudaErrorInvalidValue;
   auto kern = prefill_mma_kernel<D>;
   // set once per device; setting it twice from two threads is harmless
@@ -633,7 +665,7 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(1, std::memory_order_release);
   }
-  return launch_pdl(kern, dim3(a.NC), dim3(kThreads), C::SMEM, s, mk, mv, d, pr, a, ctx);
+  return launch_pdl(kern, dim3(a.NC), dim3(kThreads), C::SMEM, s, mk, mv, mq, d, pr, a, ctx);
 }
 
 }  // namespace
