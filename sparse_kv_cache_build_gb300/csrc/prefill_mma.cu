@@ -4,17 +4,14 @@
 // warpgroup, and walks their keys 128 at a time:
 //   S = Q K^T    128 x 128 x D,   Q and K from shared memory, S in TMEM
 //   P = 2^(scale_log2 S - m)      one thread per row: its warpgroup reads S from TMEM, keeps
-//                                 m and l in registers and writes P to TMEM as bf16
+//                                 m and l in registers and writes P back over S as bf16
 //   O += P V     128 x D x 128,   P from TMEM, V from shared memory, O in TMEM
-// The products of both warpgroups alternate, with the scores one tile ahead:
-//   ... Q0 K(j+1) | P0 V(j) | Q1 K(j+1) | P1 V(j) | Q0 K(j+2) | ...
-// so that between the scores of a tile and the product that needs its P lie three other
-// products (1536 cycles at D = 128) in which its softmax runs. This takes P out of S's place:
-// TMEM's 512 columns hold O and P of both warpgroups (2 x 128 and 2 x 64 at D = 128) and one S
-// of 128 columns, which both use in turn (a warpgroup reads S into registers at once, and the
-// products that write it wait for that). With P over S instead, the next scores wait for the
-// product before them, and a tile's round trip (softmax and both of its products one after the
-// other, 3100 cycles) bounds the rate, not the 2048 cycles of products.
+// One warp issues the products, the two warpgroups' in turn:
+//   ... P0 V(j), Q0 K(j+1) | P1 V(j), Q1 K(j+1) | P0 V(j+1), Q0 K(j+2) | ...
+// so that one warpgroup's softmax runs under the other's products. A tile's round trip (scores,
+// softmax, P V) bounds the rate, not the products alone; P is handed over in two halves, so
+// that half of P V runs under the softmax of the other half. Measured and dropped: one S for
+// both warpgroups and P beside it, scores a tile ahead (the hand-over of S then bounds it).
 // One warp feeds K and V tiles through a ring by TMA, page by page (a page of one KV head is
 // PS dense rows of the pool).
 //
@@ -42,7 +39,7 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 384;          // two softmax warpgroups, then products and loads
-constexpr int kScoreWarp = 8, kValueWarp = 9, kLoadWarp = 10, kItemWarp = 11;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
 constexpr int kItems = 4;              // items known ahead
 constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
@@ -57,16 +54,13 @@ template <int D> struct Cfg {
   static constexpr size_t OFF_RING = 2 * TILE_BYTES;
   static constexpr size_t OFF_OUT = OFF_RING + (size_t)STAGES * TILE_BYTES;   // 4 KB a warp
   static constexpr size_t OFF_BAR = OFF_OUT + 8 * 4096;
-  static constexpr int BARS = 2 * STAGES + 18 + 2 * kItems;
-  // TMEM columns: O of both warpgroups, P of both, then one S for both (or, at D = 64, two)
-  static constexpr int COL_O = 0, COL_P = 2 * D, COL_S = 2 * D + 128;
-  static constexpr int S_STEP = D == 64 ? 128 : 0;              // from one warpgroup's S to the other's
-  static_assert(COL_S + S_STEP + 128 <= kTmemCols, "TMEM");
-  static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;        // TMEM base, then [2][128] (m, l)
+  static constexpr int BARS = 2 * STAGES + 17 + 2 * kItems;
+  static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;        // TMEM base, items, [2][128] (m, l)
   static constexpr size_t OFF_ITEMS = OFF_MISC + 8;
   static constexpr size_t OFF_ML = OFF_ITEMS + kItems * sizeof(PrefillItem);
   static constexpr size_t SMEM = OFF_ML + 1024 + 1024;          // + alignment slack
-  static_assert(SMEM <= 227 * 1024 - 512, "beside the scan's scratch");
+  static_assert(SMEM <= 227 * 1024 - sizeof(LineScratch), "shared memory");
+  static constexpr int COL_O = 0, COL_S = 2 * D;                // TMEM: two O, two S with P over it
 };
 
 // An item's plan: which key tiles each warpgroup takes and where they lie in the ring, counted
@@ -90,13 +84,12 @@ struct Plan {
   }
   __device__ __forceinline__ int tiles(int w) const { return w == 0 ? n0 : n1; }
   __device__ __forceinline__ int tile(int w, int i) const { return wide ? i : 2 * i + w; }
-  // Ring slots in the order of first use: K0 K1 V0 K2 V1 ..., or (dealt out) K0 K1 K2 V0 K3 V1 ...
+  // Ring slots in the order of first use: K0 V0 K1 V1 ..., or (dealt out) K0 K1 V0 K2 V1 K3 ...
   __device__ __forceinline__ int k_slot(int t) const {
-    return wide ? (t < 1 ? t : 2 * t - 1) : t < 2 ? t : 2 * t - 2;
+    return wide ? 2 * t : t < 2 ? t : 2 * t - 1;
   }
   __device__ __forceinline__ int v_slot(int t) const {
-    const int ahead = wide ? 1 : 2;              // K tiles before the first V tile's partner
-    return t + ahead < n ? 2 * t + ahead + 1 : n + t;
+    return wide || t == n - 1 ? 2 * t + 1 : 2 * t + 2;
   }
 };
 
@@ -143,16 +136,16 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* full = bar;                          // [STAGES] a K or V tile has landed
   uint64_t* empty = bar + C::STAGES;             // [STAGES] its last product is done
   uint64_t* s_full = bar + 2 * C::STAGES;        // [2] S of a warpgroup is in TMEM
-  uint64_t* s_free = s_full + 2;                 // [2] a warpgroup has read its S
-  uint64_t* p_full = s_free + 2;                 // [2] its P is in TMEM, O rescaled
-  uint64_t* pv_done = p_full + 2;                // [2] its last product with V is done
-  uint64_t* q_full = pv_done + 2;                 // [2] its rows are in shared memory
+  uint64_t* p_half = s_full + 2;                 // [2] P of its first 64 keys is there, O rescaled
+  uint64_t* p_full = p_half + 2;                 // [2] all of its P is in TMEM
+  uint64_t* o_done = p_full + 2;                 // [2] its last product of an item is done
+  uint64_t* q_full = o_done + 2;                 // [2] its rows are in shared memory
   uint64_t* q_free = q_full + 2;                 // [2] its last scores of an item are done
   uint64_t* o_free = q_free + 2;                 // [2] its O has been read
   uint64_t* joined = o_free + 2;                 // the second warpgroup's (m, l) are written
   uint64_t* v_land = joined + 1;                 // the last V tile, before its tail is zeroed
-  uint64_t* drained = v_land + 1;                // [2] after a timeout: no product in flight
-  uint64_t* item_full = drained + 2;             // [kItems] an item is in shared memory
+  uint64_t* drained = v_land + 1;                // after a timeout: no product in flight
+  uint64_t* item_full = drained + 1;             // [kItems] an item is in shared memory
   uint64_t* item_free = item_full + kItems;      // [kItems] every warp is done with it
   PrefillItem* items = reinterpret_cast<PrefillItem*>(sm + C::OFF_ITEMS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
@@ -170,18 +163,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       mbar_init(p_full + w, 4);                  // one arrival per softmax warp
       mbar_init(q_full + w, 1);
       mbar_init(q_free + w, 1);
-      mbar_init(s_free + w, 4);
-      mbar_init(pv_done + w, 1);
+      mbar_init(p_half + w, 4);
+      mbar_init(o_done + w, 1);
       mbar_init(o_free + w, 4);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_free + i, 11);              // eight softmax warps, products, loads
+      mbar_init(item_free + i, 10);              // eight softmax warps, products, loads
     }
     mbar_init(joined, 4);
     mbar_init(v_land, 1);
     mbar_init(drained, 1);
-    mbar_init(drained + 1, 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -190,7 +182,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   const LinePlace at = find_place<MmaShape>(ctx, d, pr, a, blockIdx.x, &scratch);
   const int64_t lo = at.total * blockIdx.x / a.NC, hi = at.total * (blockIdx.x + 1) / a.NC;
   if (lo >= hi) return;
-  if (warp == kScoreWarp) tc::alloc(tmem_slot, kTmemCols);
+  if (warp == kMmaWarp) tc::alloc(tmem_slot, kTmemCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -208,11 +200,10 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     tc::more_regs<kRegsSoftmax>();
     const int w = warp >> 2, r = tid & 127;                       // warpgroup, TMEM lane
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;            // TMEM lane 32 * (warp % 4)
-    const uint32_t ts = tmem + lanes + C::COL_S + w * C::S_STEP;
-    const uint32_t tp = tmem + lanes + C::COL_P + w * 64, to = tmem + lanes + C::COL_O + w * D;
+    const uint32_t ts = tmem + lanes + C::COL_S + w * 128, to = tmem + lanes + C::COL_O + w * D;
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
-    int tiles_seen = 0, joins_seen = 0;                           // for the barriers' phases
+    int tiles_seen = 0, items_seen = 0, joins_seen = 0;           // for the barriers' phases
 
     for (int j = 0;; ++j) {
       ok = item_ready(j);
@@ -230,19 +221,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       for (int i = 0; i < n; ++i) {
         ok = mbar_wait_bounded(s_full + w, tiles_seen & 1, ctx.wait_ns);
         if (!ok) break;
+        ++tiles_seen;
         tc::fence_after();
         uint32_t s[128];
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, ref2;
         if (!idle) {
+          const int u0 = (it.kt0 + plan.tile(w, i)) * kKeys;
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, s + 32 * c);
           tc::wait_ld();
-        }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(s_free + w);
-        const int u0 = (it.kt0 + plan.tile(w, i)) * kKeys;
-        float next = m;
-        if (!idle) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tc::after_wait(s + 32 * c);
           if (warp_first - u0 < kKeys - 1) {                      // on the border
             const int seen = last - u0;
 #pragma unroll
@@ -259,18 +248,10 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                                 __uint_as_float(s[32 * c + e + 1]));
             top[c] = fmaxf(top[c], __uint_as_float(s[32 * c + 31]));
           }
-          const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-          if (now > m + kLazy) next = now;
-        }
-        // the product before has read the old P, and O is complete up to tile i - 1
-        if (i > 0) {
-          ok = mbar_wait_bounded(pv_done + w, (tiles_seen - 1) & 1, ctx.wait_ns);
-          if (!ok) break;
-        }
-        ++tiles_seen;
-        if (!idle) {
-          tc::fence_after();
-          if (__any_sync(0xffffffffu, next > m)) {
+          const float now = tc::max3(fmaxf(top[0], top[1]), top[2], top[3]) * a.scale_log2;
+          if (__any_sync(0xffffffffu, now > m + kLazy)) {
+            // s_full follows the products before it: O is complete up to tile i - 1
+            const float next = now > m + kLazy ? now : m;
             const float f = next == -INFINITY ? 1.f : exp2f(m - next);
             m = next;
             l *= f;
@@ -287,10 +268,11 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;             // no key of this row yet
-          const float2 ref2 = make_float2(-ref, -ref);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          ref2 = make_float2(-ref, -ref);
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2; ++h) {
+          if (!idle) {
             uint32_t p[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -302,20 +284,20 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
               sum[e & 1] = tc::add2(sum[e & 1], x);
               p[e] = tc::pack_bf16(x.x, x.y);
             }
-            tc::st32(tp + 32 * h, p);
+            tc::st32(ts + 32 * h, p);
+            tc::wait_st();
           }
-          sum[0] = tc::add2(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
-          tc::wait_st();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) arrive((h == 0 ? p_half : p_full) + w);
         }
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(p_full + w);
+        sum[0] = tc::add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
       }
       if (!ok) break;
       // ---- output
       const bool join = !plan.wide && plan.n1 > 0;
-      if (n > 0) ok = mbar_wait_bounded(pv_done + w, (tiles_seen - 1) & 1, ctx.wait_ns);
+      if (n > 0) ok = mbar_wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
       if (!ok) break;
       if (join && w == 1) {
         box[r] = m;
@@ -323,6 +305,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         __syncwarp();
         if (lane == 0) arrive(joined);
       }
+      if (n > 0) ++items_seen;
       if (join && w == 0) {
         // the other warpgroup's last product: it has one for each of this one's joins
         ok = mbar_wait_bounded(joined, joins_seen & 1, ctx.wait_ns);
@@ -432,102 +415,120 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
   } else {
     tc::fewer_regs<kRegsOther>();
-    if (warp == kScoreWarp || warp == kValueWarp) {
-      // ---- products: one warp issues the scores, the other the products with V, so that the
-      // waits of one lie under the other's products (both in one warp left the tensor core idle
-      // for about 200 cycles after every eight products)
+    if (warp == kMmaWarp) {
+      // ---- products
       bool ok = true;
       int base = 0;                                  // ring slots of the items before
-      int items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0, s_last = -1;   // for the phases
+      int items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0;           // for the barriers' phases
       auto wait = [&](uint64_t* x, int parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(x, parity))) return;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(x, parity, ctx.wait_ns)) && ok;
       };
-      const bool is_score = warp == kScoreWarp;
       const uint64_t q_desc = tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q)), 16);
-      const uint64_t ring_desc = tc::smem_desc(uniform(smem_addr(ring)), is_score ? 16 : 16384);
-      for (int j = 0;; ++j) {
-        ok = __all_sync(0xffffffffu, item_ready(j));
-        if (!ok) break;
+      const uint64_t k_desc = tc::smem_desc(uniform(smem_addr(ring)), 16);
+      const uint64_t v_desc = tc::smem_desc(uniform(smem_addr(ring)), 16384);
+      auto uniform_plan = [&](int j) {
         Plan plan(items[j % kItems], log_g);
-        if (plan.n <= 0) break;
-        item_done(j);
         plan.wide = uniform(plan.wide);
         plan.n = uniform(plan.n);
         plan.n0 = uniform(plan.n0);
         plan.n1 = uniform(plan.n1);
-        auto scores = [&](int w, int i) {
-          const int slot = base + plan.k_slot(plan.tile(w, i)), stage = slot % C::STAGES;
-          if (i == 0) wait(q_full + w, (w == 0 ? items0 : items1) & 1);
-          if (!plan.wide || w == 0 || i >= plan.n0)              // else it was seen for w = 0
-            wait(full + stage, (slot / C::STAGES) & 1);
-          // whoever had S before has read it
-          const int before = C::S_STEP ? w : s_last, tiles = before == 0 ? tiles0 : tiles1;
-          if (before >= 0 && tiles > 0) wait(s_free + before, (tiles - 1) & 1);
-          if (w == 0) ++tiles0;
-          else ++tiles1;
-          s_last = w;
-          if (!ok) return;
-          tc::fence_after();
-          if (tc::elect()) {
-            constexpr uint32_t id = tc::idesc(kKeys, false);
-            const uint64_t qd = q_desc + (uint64_t)(w * (C::TILE_BYTES >> 4));
-            const uint64_t kd = ring_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
+        return plan;
+      };
+      // Tile i of warpgroup w, of an item whose ring slots begin at `first`; `items`: the
+      // warpgroup's items before it.
+      auto scores_wait = [&](const Plan& plan, int first, int w, int i, int items) {
+        const int slot = first + plan.k_slot(plan.tile(w, i));
+        if (i == 0) wait(q_full + w, items & 1);
+        if (!plan.wide || w == 0 || i >= plan.n0)                // else it was seen for w = 0
+          wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
+      };
+      auto scores = [&](const Plan& plan, int first, int w, int i) {
+        const int slot = first + plan.k_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+        constexpr uint32_t id = tc::idesc(kKeys, false);
+        const uint64_t qd = q_desc + (uint64_t)(w * (C::TILE_BYTES >> 4));
+        const uint64_t kd = k_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const int step = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-              tc::mma_ss(tmem + C::COL_S + w * C::S_STEP, qd + step, kd + step, id, k > 0);
-            }
-            tc::commit(s_full + w);
-            if (i + 1 == plan.tiles(w)) tc::commit(q_free + w);
-            if (!plan.wide || w == 1) tc::commit(empty + stage);
-          }
-          __syncwarp();
-        };
-        auto values = [&](int w, int i) {
-          const int slot = base + plan.v_slot(plan.tile(w, i)), stage = slot % C::STAGES;
-          const int tiles = w == 0 ? tiles0++ : tiles1++, items = w == 0 ? items0 : items1;
-          if (!plan.wide || w == 0 || i >= plan.n0) wait(full + stage, (slot / C::STAGES) & 1);
-          if (i == 0 && items > 0) wait(o_free + w, (items - 1) & 1);     // it has been read
-          wait(p_full + w, tiles & 1);
-          if (!ok) return;
-          tc::fence_after();
-          if (tc::elect()) {
-            constexpr uint32_t id = tc::idesc(D, true);
-            const uint64_t vd = ring_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              tc::mma_ts(tmem + C::COL_O + w * D, tmem + C::COL_P + w * 64 + k * 8,
-                         vd + k * (2048 >> 4), id, i > 0 || k > 0);
-            tc::commit(pv_done + w);
-            if (!plan.wide || w == 1) tc::commit(empty + stage);
-          }
-          __syncwarp();
-        };
+        for (int k = 0; k < D / 16; ++k) {
+          const int step = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+          tc::mma_ss(tmem + C::COL_S + w * 128, qd + step, kd + step, id, k > 0);
+        }
+        tc::commit(s_full + w);
+        if (i + 1 == plan.tiles(w)) tc::commit(q_free + w);
+        if (!plan.wide || w == 1) tc::commit(empty + stage);
+      };
+      bool early = false;          // this item's first scores were issued with the last's end
+      ok = __all_sync(0xffffffffu, item_ready(0));
+      Plan plan = uniform_plan(0), next = plan;
+      for (int j = 0; ok && plan.n > 0; ++j) {
         const int most = max(plan.n0, plan.n1);
-        if (is_score) {
-          for (int i = 0; ok && i < most; ++i) {
-            if (i < plan.n0) scores(0, i);
-            if (i < plan.n1) scores(1, i);
-          }
-        } else {
-          for (int i = 0; ok && i < most; ++i) {
-            if (i < plan.n0) values(0, i);
-            if (i < plan.n1) values(1, i);
+        if (!early) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || plan.tiles(w) == 0) continue;
+            scores_wait(plan, base, w, 0, w == 0 ? items0 : items1);
+            if (ok) tc::fence_after();
+            if (ok && tc::elect()) scores(plan, base, w, 0);
+            __syncwarp();
           }
         }
+        early = false;
+        for (int i = 0; ok && i < most; ++i) {
+          if (i == most - 1) {                         // what follows
+            ok = __all_sync(0xffffffffu, item_ready(j + 1));
+            if (!ok) break;
+            next = uniform_plan(j + 1);
+            early = plan.wide && plan.n0 == plan.n1 && next.wide && next.n0 > 0;
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || i >= plan.tiles(w)) continue;
+            const int slot = base + plan.v_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+            const int tiles = w == 0 ? tiles0++ : tiles1++, before = w == 0 ? items0 : items1;
+            const bool more = i + 1 < plan.tiles(w), go_on = more || early;
+            const Plan& to = more ? plan : next;
+            const int to_base = more ? base : base + 2 * plan.n, to_i = more ? i + 1 : 0;
+            if (!plan.wide || w == 0 || i >= plan.n0) wait(full + stage, (slot / C::STAGES) & 1);
+            if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);   // it has been read
+            wait(p_half + w, tiles & 1);
+            if (!ok) continue;
+            tc::fence_after();
+            constexpr uint32_t id = tc::idesc(D, true);
+            const uint64_t vd = v_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
+            auto values = [&](int h) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                tc::mma_ts(tmem + C::COL_O + w * D, tmem + C::COL_S + w * 128 + k * 8,
+                           vd + k * (2048 >> 4), id, i > 0 || k > 0);
+            };
+            if (tc::elect()) values(0);
+            __syncwarp();
+            if (go_on) scores_wait(to, to_base, w, to_i, before + 1);
+            wait(p_full + w, tiles & 1);
+            if (!ok) continue;
+            tc::fence_after();
+            if (tc::elect()) {
+              values(1);
+              if (!plan.wide || w == 1) tc::commit(empty + stage);
+              if (!more) tc::commit(o_done + w);
+              if (go_on) scores(to, to_base, w, to_i);
+            }
+            __syncwarp();
+          }
+        }
+        item_done(j);
         items0 += plan.n0 > 0;
         items1 += plan.n1 > 0;
-        if (!ok) break;
         base += 2 * plan.n;
+        plan = next;
       }
       __syncwarp();
       if (!ok) {
         if (tc::elect()) {
           flag(ctx, KV_DEVERR_TIMEOUT);
-          tc::commit(drained + !is_score);
+          tc::commit(drained);
         }
-        (void)mbar_wait_bounded(drained + !is_score, 0, ctx.wait_ns);
+        (void)mbar_wait_bounded(drained, 0, ctx.wait_ns);
       }
     } else if (warp == kLoadWarp) {
       // ---- loads: one page half (64 columns) per lane
@@ -603,11 +604,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           __syncwarp();
           if (lane == 0) arrive(full + stage);
         };
-        const int lead = plan.wide ? 1 : 2;
-        for (int t = 0; t < min(lead, plan.n); ++t) load(&map_k, t, false);
-        for (int t = 0; t < plan.n; ++t) {
-          if (t + lead < plan.n) load(&map_k, t + lead, false);
-          load(&map_v, t, true);
+        if (plan.wide) {
+          for (int t = 0; t < plan.n; ++t) {
+            load(&map_k, t, false);
+            load(&map_v, t, true);
+          }
+        } else {
+          for (int t = 0; t < min(2, plan.n); ++t) load(&map_k, t, false);
+          for (int t = 0; t < plan.n; ++t) {
+            load(&map_v, t, true);
+            if (t + 2 < plan.n) load(&map_k, t + 2, false);
+          }
         }
         base += 2 * plan.n;
       }
@@ -664,7 +671,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   }
   __syncthreads();
   tc::fence_after();
-  if (warp == kScoreWarp) tc::dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tc::dealloc(tmem, kTmemCols);
 }
 
 template <int D>
