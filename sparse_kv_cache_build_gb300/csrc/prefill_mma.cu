@@ -6,8 +6,9 @@
 //   P = 2^(scale_log2 S - m)      one thread per row: its warpgroup reads S from TMEM, keeps
 //                                 m and l in registers and writes P back over S as bf16
 //   O += P V     128 x D x 128,   P from TMEM, V from shared memory, O in TMEM
-// A warp for each warpgroup issues its products, P V(j) and then Q K(j+1), so that one
-// warpgroup's softmax runs under the other's products. A tile's round trip (scores,
+// One warp issues the products, the two warpgroups' in turn:
+//   ... P0 V(j), Q0 K(j+1) | P1 V(j), Q1 K(j+1) | P0 V(j+1), Q0 K(j+2) | ...
+// so that one warpgroup's softmax runs under the other's products. A tile's round trip (scores,
 // softmax, P V) bounds the rate, not the products alone; P is handed over in two halves, so
 // that half of P V runs under the softmax of the other half. Measured and dropped: one S for
 // both warpgroups and P beside it, scores a tile ahead (the hand-over of S then bounds it).
@@ -38,7 +39,7 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 384;          // two softmax warpgroups, then products and loads
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kItemWarp = 11;   // 8 and 9 issue products
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
 constexpr int kItems = 4;              // items known ahead
 constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
@@ -53,7 +54,7 @@ template <int D> struct Cfg {
   static constexpr size_t OFF_RING = 2 * TILE_BYTES;
   static constexpr size_t OFF_OUT = OFF_RING + (size_t)STAGES * TILE_BYTES;   // 4 KB a warp
   static constexpr size_t OFF_BAR = OFF_OUT + 8 * 4096;
-  static constexpr int BARS = 2 * STAGES + 20 + 2 * kItems;
+  static constexpr int BARS = 2 * STAGES + 17 + 2 * kItems;
   static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;        // TMEM base, items, [2][128] (m, l)
   static constexpr size_t OFF_ITEMS = OFF_MISC + 8;
   static constexpr size_t OFF_ML = OFF_ITEMS + kItems * sizeof(PrefillItem);
@@ -143,9 +144,8 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* o_free = q_free + 2;                 // [2] its O has been read
   uint64_t* joined = o_free + 2;                 // the second warpgroup's (m, l) are written
   uint64_t* v_land = joined + 1;                 // the last V tile, before its tail is zeroed
-  uint64_t* drained = v_land + 1;                // [2] after a timeout: no product in flight
-  uint64_t* turn = drained + 2;                  // [2] the other warpgroup's products are issued
-  uint64_t* item_full = turn + 2;                // [kItems] an item is in shared memory
+  uint64_t* drained = v_land + 1;                // after a timeout: no product in flight
+  uint64_t* item_full = drained + 1;             // [kItems] an item is in shared memory
   uint64_t* item_free = item_full + kItems;      // [kItems] every warp is done with it
   PrefillItem* items = reinterpret_cast<PrefillItem*>(sm + C::OFF_ITEMS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
@@ -156,12 +156,11 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 2);                   // one arrival per warpgroup
+      mbar_init(empty + i, 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 1);
       mbar_init(p_full + w, 4);                  // one arrival per softmax warp
-      mbar_init(turn + w, 1);
       mbar_init(q_full + w, 1);
       mbar_init(q_free + w, 1);
       mbar_init(p_half + w, 4);
@@ -170,12 +169,11 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_free + i, 11);              // eight softmax warps, products, loads
+      mbar_init(item_free + i, 10);              // eight softmax warps, products, loads
     }
     mbar_init(joined, 4);
     mbar_init(v_land, 1);
     mbar_init(drained, 1);
-    mbar_init(drained + 1, 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -417,20 +415,16 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
   } else {
     tc::fewer_regs<kRegsOther>();
-    if (warp < kMmaWarp + 2) {
-      // ---- products of warpgroup w. A warp for each: the waits of one lie under the other's
-      // products (one warp for both left the tensor core idle for a third of the time)
-      const int w = warp - kMmaWarp;
+    if (warp == kMmaWarp) {
+      // ---- products
       bool ok = true;
       int base = 0;                                  // ring slots of the items before
-      int items_seen = 0, tiles_seen = 0, other_seen = 0;           // for the barriers' phases
+      int items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0;           // for the barriers' phases
       auto wait = [&](uint64_t* x, int parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(x, parity))) return;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(x, parity, ctx.wait_ns)) && ok;
       };
-      const uint32_t s_tmem = tmem + C::COL_S + w * 128, o_tmem = tmem + C::COL_O + w * D;
-      const uint64_t q_desc =
-          tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q) + w * C::TILE_BYTES), 16);
+      const uint64_t q_desc = tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q)), 16);
       const uint64_t k_desc = tc::smem_desc(uniform(smem_addr(ring)), 16);
       const uint64_t v_desc = tc::smem_desc(uniform(smem_addr(ring)), 16384);
       auto uniform_plan = [&](int j) {
@@ -441,100 +435,90 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         plan.n1 = uniform(plan.n1);
         return plan;
       };
-      // A tile that the other warpgroup does not use is released for both.
-      auto release = [&](int stage, bool shared) {
-        tc::commit(empty + stage);
-        if (!shared) tc::commit(empty + stage);
+      // Tile i of warpgroup w, of an item whose ring slots begin at `first`; `items`: the
+      // warpgroup's items before it.
+      auto scores_wait = [&](const Plan& plan, int first, int w, int i, int items) {
+        const int slot = first + plan.k_slot(plan.tile(w, i));
+        if (i == 0) wait(q_full + w, items & 1);
+        if (!plan.wide || w == 0 || i >= plan.n0)                // else it was seen for w = 0
+          wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
       };
-      // Scores of a tile in ring slot `slot`; `last`: of the item.
-      auto scores = [&](int slot, bool shared, bool last) {
-        const int stage = slot % C::STAGES;
+      auto scores = [&](const Plan& plan, int first, int w, int i) {
+        const int slot = first + plan.k_slot(plan.tile(w, i)), stage = slot % C::STAGES;
         constexpr uint32_t id = tc::idesc(kKeys, false);
+        const uint64_t qd = q_desc + (uint64_t)(w * (C::TILE_BYTES >> 4));
         const uint64_t kd = k_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int step = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-          tc::mma_ss(s_tmem, q_desc + step, kd + step, id, k > 0);
+          tc::mma_ss(tmem + C::COL_S + w * 128, qd + step, kd + step, id, k > 0);
         }
         tc::commit(s_full + w);
-        if (last) tc::commit(q_free + w);
-        release(stage, shared);
+        if (i + 1 == plan.tiles(w)) tc::commit(q_free + w);
+        if (!plan.wide || w == 1) tc::commit(empty + stage);
       };
-      bool early = false;          // the item's first scores were issued with the last's end
+      bool early = false;          // this item's first scores were issued with the last's end
       ok = __all_sync(0xffffffffu, item_ready(0));
-      Plan plan = uniform_plan(0);
+      Plan plan = uniform_plan(0), next = plan;
       for (int j = 0; ok && plan.n > 0; ++j) {
-        const int n = plan.tiles(w);
-        const int both = plan.wide ? plan.n0 : 0;      // tiles that both warpgroups use
-        if (n > 0 && !early) {
-          const int slot = base + plan.k_slot(plan.tile(w, 0));
-          wait(q_full + w, items_seen & 1);
-          wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
-          if (!ok) break;
-          tc::fence_after();
-          if (tc::elect()) scores(slot, 0 < both, n == 1);
-          __syncwarp();
+        const int most = max(plan.n0, plan.n1);
+        if (!early) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || plan.tiles(w) == 0) continue;
+            scores_wait(plan, base, w, 0, w == 0 ? items0 : items1);
+            if (ok) tc::fence_after();
+            if (ok && tc::elect()) scores(plan, base, w, 0);
+            __syncwarp();
+          }
         }
         early = false;
-        Plan next = plan;
-        for (int i = 0; ok && i < n; ++i) {
-          const int slot = base + plan.v_slot(plan.tile(w, i)), stage = slot % C::STAGES;
-          int k_slot = base + plan.k_slot(plan.tile(w, i + 1));
-          bool k_shared = i + 1 < both, k_last = i + 2 == n, go_on = true;
-          if (i + 1 == n) {                            // on to the next item, if it has tiles
+        for (int i = 0; ok && i < most; ++i) {
+          if (i == most - 1) {                         // what follows
             ok = __all_sync(0xffffffffu, item_ready(j + 1));
             if (!ok) break;
             next = uniform_plan(j + 1);
-            early = go_on = next.tiles(w) > 0;
-            k_slot = base + 2 * plan.n + next.k_slot(next.tile(w, 0));
-            k_shared = next.wide && next.n0 > 0;
-            k_last = next.tiles(w) == 1;
+            early = plan.wide && plan.n0 == plan.n1 && next.wide && next.n0 > 0;
           }
-          wait(full + stage, (slot / C::STAGES) & 1);
-          if (i == 0 && items_seen > 0) wait(o_free + w, (items_seen - 1) & 1);
-          wait(p_half + w, tiles_seen & 1);
-          if (!ok) break;
-          tc::fence_after();
-          constexpr uint32_t id = tc::idesc(D, true);
-          const uint64_t vd = v_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
-          auto values = [&](int h) {
 #pragma unroll
-            for (int k = 4 * h; k < 4 * h + 4; ++k)
-              tc::mma_ts(o_tmem, s_tmem + k * 8, vd + k * (2048 >> 4), id, i > 0 || k > 0);
-          };
-          if (tc::elect()) values(0);
-          __syncwarp();
-          if (go_on) {
-            if (i + 1 == n) wait(q_full + w, (items_seen + 1) & 1);
-            wait(full + k_slot % C::STAGES, (k_slot / C::STAGES) & 1);
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || i >= plan.tiles(w)) continue;
+            const int slot = base + plan.v_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+            const int tiles = w == 0 ? tiles0++ : tiles1++, before = w == 0 ? items0 : items1;
+            const bool more = i + 1 < plan.tiles(w), go_on = more || early;
+            const Plan& to = more ? plan : next;
+            const int to_base = more ? base : base + 2 * plan.n, to_i = more ? i + 1 : 0;
+            if (!plan.wide || w == 0 || i >= plan.n0) wait(full + stage, (slot / C::STAGES) & 1);
+            if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);   // it has been read
+            wait(p_half + w, tiles & 1);
+            if (!ok) continue;
+            tc::fence_after();
+            constexpr uint32_t id = tc::idesc(D, true);
+            const uint64_t vd = v_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
+            auto values = [&](int h) {
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                tc::mma_ts(tmem + C::COL_O + w * D, tmem + C::COL_S + w * 128 + k * 8,
+                           vd + k * (2048 >> 4), id, i > 0 || k > 0);
+            };
+            if (tc::elect()) values(0);
+            __syncwarp();
+            if (go_on) scores_wait(to, to_base, w, to_i, before + 1);
+            wait(p_full + w, tiles & 1);
+            if (!ok) continue;
+            tc::fence_after();
+            if (tc::elect()) {
+              values(1);
+              if (!plan.wide || w == 1) tc::commit(empty + stage);
+              if (!more) tc::commit(o_done + w);
+              if (go_on) scores(to, to_base, w, to_i);
+            }
+            __syncwarp();
           }
-          wait(p_full + w, tiles_seen & 1);
-          // The warpgroups take turns: left to themselves they fall into step, and then both
-          // softmaxes, and both warpgroups' products, get in each other's way.
-          const int theirs = w == 0 ? i - 1 : i;
-          if (theirs >= 0 && theirs < plan.tiles(w ^ 1))
-            wait(turn + w, (other_seen + theirs) & 1);
-          if (!ok) break;
-          ++tiles_seen;
-          tc::fence_after();
-          if (tc::elect()) {
-            values(1);
-            release(stage, i < both);
-            if (i + 1 == n) tc::commit(o_done + w);
-            if (go_on) scores(k_slot, k_shared, k_last);
-            arrive(turn + (w ^ 1));
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (n == 0) {
-          ok = __all_sync(0xffffffffu, item_ready(j + 1));
-          if (!ok) break;
-          next = uniform_plan(j + 1);
         }
         item_done(j);
-        items_seen += n > 0;
-        other_seen += plan.tiles(w ^ 1);
+        items0 += plan.n0 > 0;
+        items1 += plan.n1 > 0;
         base += 2 * plan.n;
         plan = next;
       }
@@ -542,9 +526,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok) {
         if (tc::elect()) {
           flag(ctx, KV_DEVERR_TIMEOUT);
-          tc::commit(drained + w);
+          tc::commit(drained);
         }
-        (void)mbar_wait_bounded(drained + w, 0, ctx.wait_ns);
+        (void)mbar_wait_bounded(drained, 0, ctx.wait_ns);
       }
     } else if (warp == kLoadWarp) {
       // ---- loads: one page half (64 columns) per lane
