@@ -39,7 +39,7 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 384;          // two softmax warpgroups, then products and loads
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kReadyWarp = 11;
 constexpr int kItems = 4;              // items known ahead
 constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
@@ -160,16 +160,16 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 1);
-      mbar_init(p_full + w, 4);                  // one arrival per softmax warp
+      mbar_init(p_full + w, 5);                  // the softmax warps', and the ready warp's
       mbar_init(q_full + w, 1);
       mbar_init(q_free + w, 1);
-      mbar_init(p_half + w, 4);
+      mbar_init(p_half + w, 5);
       mbar_init(o_done + w, 1);
       mbar_init(o_free + w, 4);
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_free + i, 10);              // eight softmax warps, products, loads
+      mbar_init(item_free + i, 11);              // eight softmax warps, products, loads, ready
     }
     mbar_init(joined, 4);
     mbar_init(v_land, 1);
@@ -415,14 +415,25 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
   } else {
     tc::fewer_regs<kRegsOther>();
-    if (warp == kMmaWarp) {
-      // ---- products
+    if (warp == kMmaWarp || warp == kReadyWarp) {
+      // ---- products, and what they need beside P. The time between two batches of products is
+      // lost to the tensor core, so the warp that issues them waits for as little as it can: a
+      // second warp walks the same batches a little ahead, waits for their V and K tiles, rows
+      // and O, and adds its arrival to the softmax warps' at p_half and p_full.
+      const bool issues = warp == kMmaWarp;
       bool ok = true;
       int base = 0;                                  // ring slots of the items before
       int items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0;           // for the barriers' phases
       auto wait = [&](uint64_t* x, int parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(x, parity))) return;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(x, parity, ctx.wait_ns)) && ok;
+      };
+      auto wait_slot = [&](int slot) {
+        wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
+      };
+      auto say = [&](uint64_t* x) {
+        __syncwarp();
+        if (lane == 0) arrive(x);
       };
       const uint64_t q_desc = tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q)), 16);
       const uint64_t k_desc = tc::smem_desc(uniform(smem_addr(ring)), 16);
@@ -435,16 +446,10 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         plan.n1 = uniform(plan.n1);
         return plan;
       };
-      // Tile i of warpgroup w, of an item whose ring slots begin at `first`; `items`: the
-      // warpgroup's items before it.
-      auto scores_wait = [&](const Plan& plan, int first, int w, int i, int items) {
-        const int slot = first + plan.k_slot(plan.tile(w, i));
-        if (i == 0) wait(q_full + w, items & 1);
-        if (!plan.wide || w == 0 || i >= plan.n0)                // else it was seen for w = 0
-          wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
-      };
-      auto scores = [&](const Plan& plan, int first, int w, int i) {
-        const int slot = first + plan.k_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+      // Scores of warpgroup w's tile in ring slot `slot`; `done`: w is its last reader; `last`:
+      // of the item.
+      auto scores = [&](int w, int slot, bool done, bool last) {
+        const int stage = slot % C::STAGES;
         constexpr uint32_t id = tc::idesc(kKeys, false);
         const uint64_t qd = q_desc + (uint64_t)(w * (C::TILE_BYTES >> 4));
         const uint64_t kd = k_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
@@ -454,21 +459,24 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           tc::mma_ss(tmem + C::COL_S + w * 128, qd + step, kd + step, id, k > 0);
         }
         tc::commit(s_full + w);
-        if (i + 1 == plan.tiles(w)) tc::commit(q_free + w);
-        if (!plan.wide || w == 1) tc::commit(empty + stage);
+        if (last) tc::commit(q_free + w);
+        if (done) tc::commit(empty + stage);
       };
       bool early = false;          // this item's first scores were issued with the last's end
       ok = __all_sync(0xffffffffu, item_ready(0));
       Plan plan = uniform_plan(0), next = plan;
       for (int j = 0; ok && plan.n > 0; ++j) {
         const int most = max(plan.n0, plan.n1);
-        if (!early) {
+        if (!early && issues) {
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || plan.tiles(w) == 0) continue;
-            scores_wait(plan, base, w, 0, w == 0 ? items0 : items1);
-            if (ok) tc::fence_after();
-            if (ok && tc::elect()) scores(plan, base, w, 0);
+            const int slot = base + plan.k_slot(plan.tile(w, 0));
+            wait(q_full + w, (w == 0 ? items0 : items1) & 1);
+            wait_slot(slot);
+            if (!ok) continue;
+            tc::fence_after();
+            if (tc::elect()) scores(w, slot, !plan.wide || w == 1, plan.tiles(w) == 1);
             __syncwarp();
           }
         }
@@ -483,35 +491,49 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || i >= plan.tiles(w)) continue;
-            const int slot = base + plan.v_slot(plan.tile(w, i)), stage = slot % C::STAGES;
+            const int slot = base + plan.v_slot(plan.tile(w, i));
             const int tiles = w == 0 ? tiles0++ : tiles1++, before = w == 0 ? items0 : items1;
             const bool more = i + 1 < plan.tiles(w), go_on = more || early;
-            const Plan& to = more ? plan : next;
-            const int to_base = more ? base : base + 2 * plan.n, to_i = more ? i + 1 : 0;
-            if (!plan.wide || w == 0 || i >= plan.n0) wait(full + stage, (slot / C::STAGES) & 1);
-            if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);   // it has been read
-            wait(p_half + w, tiles & 1);
-            if (!ok) continue;
-            tc::fence_after();
+            const int k_slot = more ? base + plan.k_slot(plan.tile(w, i + 1)) : base + 2 * plan.n;
+            if (!issues) {
+              // The tile's scores are there: so is every tile before, whose barriers' phases
+              // (of two kinds) could otherwise be taken for those waited for here.
+              wait(s_full + w, tiles & 1);
+              wait_slot(slot);
+              if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);   // it has been read
+              if (!ok) continue;
+              say(p_half + w);
+              if (go_on) {
+                if (!more) wait(q_full + w, (before + 1) & 1);
+                wait_slot(k_slot);
+                if (!ok) continue;
+              }
+              say(p_full + w);
+              continue;
+            }
+            const bool done = !plan.wide || w == 1;
+            const bool last = more ? i + 2 == plan.tiles(w) : next.tiles(w) == 1;
             constexpr uint32_t id = tc::idesc(D, true);
-            const uint64_t vd = v_desc + (uint64_t)(stage * (C::TILE_BYTES >> 4));
+            const uint64_t vd = v_desc + (uint64_t)(slot % C::STAGES * (C::TILE_BYTES >> 4));
             auto values = [&](int h) {
 #pragma unroll
               for (int k = 4 * h; k < 4 * h + 4; ++k)
                 tc::mma_ts(tmem + C::COL_O + w * D, tmem + C::COL_S + w * 128 + k * 8,
                            vd + k * (2048 >> 4), id, i > 0 || k > 0);
             };
+            wait(p_half + w, tiles & 1);
+            if (!ok) continue;
+            tc::fence_after();
             if (tc::elect()) values(0);
             __syncwarp();
-            if (go_on) scores_wait(to, to_base, w, to_i, before + 1);
             wait(p_full + w, tiles & 1);
             if (!ok) continue;
             tc::fence_after();
             if (tc::elect()) {
               values(1);
-              if (!plan.wide || w == 1) tc::commit(empty + stage);
               if (!more) tc::commit(o_done + w);
-              if (go_on) scores(to, to_base, w, to_i);
+              if (done) tc::commit(empty + slot % C::STAGES);
+              if (go_on) scores(w, k_slot, more ? done : w == 1, last);
             }
             __syncwarp();
           }
@@ -526,9 +548,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok) {
         if (tc::elect()) {
           flag(ctx, KV_DEVERR_TIMEOUT);
-          tc::commit(drained);
+          if (issues) tc::commit(drained);
         }
-        (void)mbar_wait_bounded(drained, 0, ctx.wait_ns);
+        if (issues) (void)mbar_wait_bounded(drained, 0, ctx.wait_ns);
       }
     } else if (warp == kLoadWarp) {
       // ---- loads: one page half (64 columns) per lane

@@ -516,6 +516,25 @@ def test_same_results_every_time_and_on_other_streams(shares):
         assert torch.equal(o, out) and torch.equal(x, lse)
 
 
+@pytest.mark.parametrize("new,past,PS", [((1,), (20000,), 16), ((5, 2, 1, 7), (9000, 3000, 12345, 1),
+                                                               16),
+                                         ((700, 1, 64, 300), (0, 5000, 900, 33), 64)])
+def test_the_same_bits_call_after_call(new, past, PS):
+    """Calls that follow one another without a pause: a tile read before it has landed, or a
+    buffer given back too early, shows as other bits in one of many calls."""
+    c = Case(new, past, "bf16", 128, 4, Hkv=8, PS=PS)
+    ref, ref_lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu)
+    ws = torch.empty((skv.kv_prefill_attn_workspace_size(c.kv, c.Hq, c.T),), dtype=torch.uint8,
+                     device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(60):
+        for _ in range(5):
+            out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu, workspace=ws)
+        differ += (out != ref).sum() + (lse != ref_lse).sum()
+    assert_no_device_error()
+    assert int(differ) == 0
+
+
 def test_captured_and_replayed_with_new_contents():
     """Append and attention captured into one graph; a replay reads the buffers as they are
     then (other rows, a longer cache), and two graphs share a workspace one after the other."""
