@@ -38,7 +38,7 @@ struct PrefillArgs {
 template <int R, int KT, int WIDE> struct TileShape {
   static constexpr int rows = R, keys = KT, narrow = WIDE;
 };
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 5;
 constexpr int kMinPart = 2;      // a border leaves an item at least this many key tiles
 
 // One sequence's rows as items, the same for each of its KV heads.
