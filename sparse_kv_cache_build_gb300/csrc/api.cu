@@ -226,15 +226,16 @@ int prefill_shares(const kv_cache_desc* d, int asked, const DeviceState* st) {
 }
 
 // Two parts per block, of a tile's rows or all the rows there are.
-struct PrefillLayout { int rows; size_t ml, total; };
+struct PrefillLayout { int rows; size_t ml, notes, total; };
 PrefillLayout prefill_layout(const kv_cache_desc* d, int G, int total, int shares) {
-  PrefillLayout L{0, 0, 0};
+  PrefillLayout L{0, 0, 0, 0};
   if (shares <= 1 || total <= 0) return L;
   const int tile = prefill_tile_rows(d->dtype);
   L.rows = (int64_t)total * G < tile ? total * G : tile;
   const size_t rows = (size_t)2 * shares * L.rows;
   L.ml = round256(rows * d->head_dim * sizeof(float));
-  L.total = L.ml + round256(rows * 2 * sizeof(float));
+  L.notes = L.ml + round256(rows * 2 * sizeof(float));
+  L.total = L.notes + round256((size_t)shares * sizeof(BorderNote));
   return L;
 }
 
@@ -417,6 +418,7 @@ kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_s
       return KV_ERR_WORKSPACE;
     a.part_acc = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.ml);
+    a.notes = reinterpret_cast<BorderNote*>(static_cast<char*>(workspace) + L.notes);
     a.part_rows = L.rows;
   }
   return from_cuda(launch_prefill(*cache, cu_tokens, total_tokens, a, ctx, stream));

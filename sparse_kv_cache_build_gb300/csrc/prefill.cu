@@ -24,102 +24,87 @@ template <> __device__ __forceinline__ void store2<float>(float* p, float a, flo
 // warp per row, lanes over the parts for (m, l) and over the columns for the accumulators,
 // whose loads are independent of one another. A part without keys for a row (m = -inf) has no
 // accumulator to read.
-template <typename T, typename S, int D>
+template <typename T, int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-prefill_merge_kernel(const __grid_constant__ kv_cache_desc d,
-                     const __grid_constant__ PackedRows pr,
-                     const __grid_constant__ PrefillArgs a, const __grid_constant__ DevCtx ctx) {
-  __shared__ LineScratch scratch;
+prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int PAIRS = D / 64;            // column pairs per lane
-  // lengths and offsets are older than the attention kernel, which let this one start only
-  // after its own wait for them; its parts are read after the wait below
   pdl_trigger();
-  const int c = blockIdx.x + 1;
-  const LinePlace at = find_place<S>(ctx, d, pr, a, c, &scratch);
-  PrefillItem it;
-  int left = 0, prev = 0;
-  bool cut = false;
-  const int64_t y = at.total * c / a.NC;
-  if (at.total > 0 && y < at.total) {
-    const ItemWalk<S> walk(d, pr, a, ctx, y, y + 1, at.b, at.before, 0);
-    if (walk.first(&it)) {
-      left = walk.first_before(y);
-      prev = walk.first_before(at.total * (c - 1) / a.NC);
-      cut = left > 0 && left < it.nk && prev == 0;
-      if (cut) {
-        // the block that reaches the item's end
-        int end = c;
-        while (walk.first_before(at.total * (end + 1) / a.NC) < it.nk) ++end;
-        pdl_wait();
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int rows = it.n_tok << a.log_g;
-        for (int row = blockIdx.y * kMergeWarps + warp; row < rows;
-             row += kMergeRowGroups * kMergeWarps) {
-          float M = -INFINITY, L = 0.f;
-          float2 acc[PAIRS];
+  pdl_wait();
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const BorderNote it = a.notes[c], before = a.notes[c - 1];
+  auto continues = [&](const BorderNote& n) {
+    return n.row0 == it.row0 && n.g == it.g && n.kt0 > 0 && n.kt0 < n.nk;
+  };
+  if (!continues(it) || continues(before)) return;
+  const int rows = it.n_tok << a.log_g;
+  for (int row = blockIdx.y * kMergeWarps + warp; row < rows;
+       row += kMergeRowGroups * kMergeWarps) {
+    float M = -INFINITY, L = 0.f;
+    float2 acc[PAIRS];
 #pragma unroll
-          for (int p = 0; p < PAIRS; ++p) acc[p] = make_float2(0.f, 0.f);
-          for (int j0 = c - 1; j0 <= end; j0 += 32) {
-            const int j = j0 + lane;
-            // block c - 1 ends with this item, the others begin with it
-            const int64_t mine = (int64_t)(j == c - 1 ? 2 * j + 1 : 2 * j) * a.part_rows + row;
-            float m = -INFINITY, l = 0.f;
-            if (j <= end && walk.first_before(at.total * j / a.NC) <
-                                walk.first_before(at.total * (j + 1) / a.NC)) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + mine);
-              m = ml.x;
-              l = ml.y;
-            }
-            float now = fmaxf(M, m);
+    for (int p = 0; p < PAIRS; ++p) acc[p] = make_float2(0.f, 0.f);
+    bool more = true;
+    for (int j0 = c - 1; more; j0 += 32) {
+      // block c - 1 ends with this item, the others begin with it
+      const int j = j0 + lane;
+      BorderNote n = it;
+      if (j >= c && j < a.NC) n = a.notes[j];
+      const bool part = j == c - 1 || (j < a.NC && continues(n));
+      const int parts = __popc(__ballot_sync(0xffffffffu, part));       // the first lanes
+      more = parts == 32;
+      const int64_t mine = (int64_t)(j == c - 1 ? 2 * j + 1 : 2 * j) * a.part_rows + row;
+      float m = -INFINITY, l = 0.f;
+      if (part && (j == c - 1 || n.kt1 > n.kt0)) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + mine);
+        m = ml.x;
+        l = ml.y;
+      }
+      float now = fmaxf(M, m);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-              now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-            if (now == -INFINITY) continue;
-            const float keep = exp2f(M - now), w = exp2f(m - now);
-            M = now;
-            float sum = l * w;
+      for (int o = 16; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+      if (now == -INFINITY) continue;
+      const float keep = exp2f(M - now), w = exp2f(m - now);
+      M = now;
+      float sum = l * w;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            L = fmaf(L, keep, sum);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      L = fmaf(L, keep, sum);
 #pragma unroll
-            for (int p = 0; p < PAIRS; ++p) {
-              acc[p].x *= keep;
-              acc[p].y *= keep;
-            }
-            const int parts = min(32, end + 1 - j0);
+      for (int p = 0; p < PAIRS; ++p) {
+        acc[p].x *= keep;
+        acc[p].y *= keep;
+      }
 #pragma unroll 8
-            for (int e = 0; e < parts; ++e) {
-              const float we = __shfl_sync(0xffffffffu, w, e);
-              const int64_t from = __shfl_sync(0xffffffffu, mine, e);
-              if (we == 0.f) continue;             // no keys, or nothing left of them
-              const float2* src = reinterpret_cast<const float2*>(a.part_acc + from * D) + lane;
+      for (int e = 0; e < parts; ++e) {
+        const float we = __shfl_sync(0xffffffffu, w, e);
+        const int64_t from = __shfl_sync(0xffffffffu, mine, e);
+        float2 v[PAIRS];
 #pragma unroll
-              for (int p = 0; p < PAIRS; ++p) {
-                const float2 v = __ldcg(src + 32 * p);
-                acc[p].x = fmaf(v.x, we, acc[p].x);
-                acc[p].y = fmaf(v.y, we, acc[p].y);
-              }
-            }
-          }
-          const int64_t out_row = (int64_t)(it.row0 + (row >> a.log_g)) * a.Hq + it.g * a.G +
-                                  (row & (a.G - 1));
-          const float inv = 1.f / L;               // every row sees its own token: L > 0
-          T* dst = static_cast<T*>(a.out) + out_row * D + 2 * lane;
+        for (int p = 0; p < PAIRS; ++p)          // no keys, or nothing left of them: not read
+          v[p] = we == 0.f ? make_float2(0.f, 0.f)
+                           : __ldcg(reinterpret_cast<const float2*>(a.part_acc + from * D) + lane +
+                                    32 * p);
 #pragma unroll
-          for (int p = 0; p < PAIRS; ++p) store2<T>(dst + 64 * p, acc[p].x * inv, acc[p].y * inv);
-          if (lane == 0 && a.lse != nullptr) a.lse[out_row] = (M + log2f(L)) * kLn2;
+        for (int p = 0; p < PAIRS; ++p) {
+          acc[p].x = fmaf(v[p].x, we, acc[p].x);
+          acc[p].y = fmaf(v[p].y, we, acc[p].y);
         }
       }
     }
+    const int64_t out_row = (int64_t)(it.row0 + (row >> a.log_g)) * a.Hq + it.g * a.G +
+                            (row & (a.G - 1));
+    const float inv = 1.f / L;                     // every row sees its own token: L > 0
+    T* dst = static_cast<T*>(a.out) + out_row * D + 2 * lane;
+#pragma unroll
+    for (int p = 0; p < PAIRS; ++p) store2<T>(dst + 64 * p, acc[p].x * inv, acc[p].y * inv);
+    if (lane == 0 && a.lse != nullptr) a.lse[out_row] = (M + log2f(L)) * kLn2;
   }
-  if (!cut) pdl_wait();
 }
 
-template <typename T, typename S, int D>
-cudaError_t merge_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
-                    DevCtx ctx, cudaStream_t s) {
-  return launch_pdl(prefill_merge_kernel<T, S, D>, dim3(a.NC - 1, kMergeRowGroups),
-                    dim3(kMergeWarps * 32), 0, s, d, pr, a, ctx);
+template <typename T, int D>
+cudaError_t merge_t(const PrefillArgs& a, cudaStream_t s) {
+  return launch_pdl(prefill_merge_kernel<T, D>, dim3(a.NC - 1, kMergeRowGroups),
+                    dim3(kMergeWarps * 32), 0, s, a);
 }
 
 }  // namespace
@@ -133,11 +118,8 @@ cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
   const bool bf = d.dtype == KV_BF16;
   cudaError_t e = bf ? launch_prefill_mma(d, pr, a, ctx, s) : launch_prefill_simt(d, pr, a, ctx, s);
   if (e != cudaSuccess || a.NC == 1) return e;
-  if (bf)
-    return d.head_dim == 128 ? merge_t<bf16_t, MmaShape, 128>(d, pr, a, ctx, s)
-                             : merge_t<bf16_t, MmaShape, 64>(d, pr, a, ctx, s);
-  return d.head_dim == 128 ? merge_t<float, SimtShape, 128>(d, pr, a, ctx, s)
-                           : merge_t<float, SimtShape, 64>(d, pr, a, ctx, s);
+  if (bf) return d.head_dim == 128 ? merge_t<bf16_t, 128>(a, s) : merge_t<bf16_t, 64>(a, s);
+  return d.head_dim == 128 ? merge_t<float, 128>(a, s) : merge_t<float, 64>(a, s);
 }
 
 }  // namespace skv

@@ -11,14 +11,23 @@
 // whatever the lengths: a prompt of one sequence, a ragged batch and single tokens over long
 // caches are all divided evenly, and the host needs to know no length. An item that a piece's
 // border cuts is computed in parts: each block leaves its rows' (m, l, acc) in the workspace
-// (a block has at most two such parts, its first and its last), and a merge kernel, whose
-// blocks are the borders, joins them. Every block finds its own piece from the lengths: one
-// pass over the batch's offsets, a scan, and closed forms inside the sequence.
+// (a block has at most two such parts, its first and its last) and notes where its piece begins
+// (BorderNote), from which a merge kernel, whose blocks are the borders, joins the parts. Every
+// block finds its own piece from the lengths: one pass over the batch's offsets, a scan, and
+// closed forms inside the sequence.
 #pragma once
 
 #include "packed_rows.cuh"
 
 namespace skv {
+
+// Where block c's piece of the line begins: the item there (by its first packed row and KV head)
+// and the block's key tiles of it. 0 < kt0 < nk: the border cuts the item, whose part before
+// it is block c - 1's last unless block c - 1 notes the same item with kt0 > 0.
+struct BorderNote {
+  int row0, n_tok, g;
+  int kt0, kt1, nk;
+};
 
 struct PrefillArgs {
   const void* q;
@@ -27,6 +36,7 @@ struct PrefillArgs {
   float* lse;             // [total][Hq], or NULL
   float* part_acc;        // [2 NC][part_rows][D], when NC > 1
   float* part_ml;         // [2 NC][part_rows][2]: m in base 2 (-inf: no keys), l
+  BorderNote* notes;      // [NC]
   float scale_log2;       // sm_scale * log2(e)
   int Hq, G, log_g;
   int NC;                 // blocks the work is divided among
@@ -158,22 +168,18 @@ template <typename S> class ItemWalk {
     }
   }
 
-  // The item that holds the line's place lo: its tiles before that place, and how the block of
-  // any other border cuts it.
-  __device__ __forceinline__ bool first(PrefillItem* it) const {
+  // What a merge has to know of the place where the piece begins.
+  __device__ __forceinline__ BorderNote border() const {
     const int t = tile_ + 1;
-    if (t >= seq_.tiles()) return false;
-    it->b = b_;
-    it->g = g_;
-    it->tile = t;
-    it->nk = seq_.key_tiles(t);
-    it->row0 = seq_.row0 + (t << seq_.tq_log);
-    it->n_tok = seq_.tokens(t);
-    return true;
-  }
-  __device__ __forceinline__ int first_before(int64_t y) const {
-    const int t = tile_ + 1;
-    return tiles_before(y, x_, seq_.key_tiles(t), seq_.unit(t, a_.log_g));
+    BorderNote n{0, 0, 0, 0, 0, 0};
+    if (t >= seq_.tiles()) return n;
+    n.row0 = seq_.row0 + (t << seq_.tq_log);
+    n.n_tok = seq_.tokens(t);
+    n.g = g_;
+    n.nk = seq_.key_tiles(t);
+    n.kt0 = tiles_before(lo_, x_, n.nk, seq_.unit(t, a_.log_g));
+    n.kt1 = tiles_before(hi_, x_, n.nk, seq_.unit(t, a_.log_g));
+    return n;
   }
 
  private:
@@ -226,7 +232,7 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
     if (w < warp) before += sh->sums[w];
     total += sh->sums[w];
   }
-  const int64_t y = total * i / a.NC;
+  const int64_t y = total * i / a.NC;        // < total: some thread holds it, unless all is empty
   if (mine > 0 && y >= before && y < before + mine) {
     int b = b0;
     for (; b < b1 - 1; ++b) {

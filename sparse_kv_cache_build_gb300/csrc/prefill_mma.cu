@@ -176,12 +176,18 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     mbar_init(drained, 1);
     fence_mbar_init();
   }
+  pdl_trigger();
   pdl_wait();
-  pdl_trigger();       // not earlier: the merge reads lengths before it waits for this kernel
   finish_empty<bf16_t, D>(ctx, d, pr, a);
   const LinePlace at = find_place<MmaShape>(ctx, d, pr, a, blockIdx.x, &scratch);
   const int64_t lo = at.total * blockIdx.x / a.NC, hi = at.total * (blockIdx.x + 1) / a.NC;
-  if (lo >= hi) return;
+  if (at.total == 0 || lo >= hi) {                 // nothing, or less than a unit of the line
+    if (tid == 0 && a.notes != nullptr)
+      a.notes[blockIdx.x] =
+          at.total == 0 ? BorderNote{0, 0, 0, 0, 0, 0}
+                        : ItemWalk<MmaShape>(d, pr, a, ctx, lo, hi, at.b, at.before, 0).border();
+    return;
+  }
   if (warp == kMmaWarp) tc::alloc(tmem_slot, kTmemCols);
   tc::fence_before();
   __syncthreads();
@@ -648,6 +654,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       // ---- the block's items, one ahead of their rows, and after the last an item without key
       // tiles; a warpgroup's rows are loaded as soon as the item before is done with them
       ItemWalk<MmaShape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
+      if (lane == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
       bool ok = true;
       int loaded[2] = {0, 0};
       PrefillItem it, next;

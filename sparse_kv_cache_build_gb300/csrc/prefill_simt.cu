@@ -49,13 +49,17 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
   float* sq = sm;
   float* sk = sq + R * LD;
   float* sv = sk + KT * LD;
+  pdl_trigger();
   pdl_wait();
-  pdl_trigger();       // not earlier: the merge reads lengths before it waits for this kernel
   finish_empty<float, D>(ctx, d, pr, a);
   const LinePlace at = find_place<SimtShape>(ctx, d, pr, a, blockIdx.x, &scratch);
   const int64_t lo = at.total * blockIdx.x / a.NC, hi = at.total * (blockIdx.x + 1) / a.NC;
-  if (lo >= hi) return;
+  if (at.total == 0) {
+    if (threadIdx.x == 0 && a.notes != nullptr) a.notes[blockIdx.x] = BorderNote{0, 0, 0, 0, 0, 0};
+    return;
+  }
   ItemWalk<SimtShape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
+  if (threadIdx.x == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int Hkv = d.num_kv_heads, PS = d.page_size;
   const float* q = static_cast<const float*>(a.q);

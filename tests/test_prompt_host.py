@@ -91,7 +91,7 @@ def test_workspace_size_formula(lib):
     r256 = lambda x: (x + 255) // 256 * 256  # noqa: E731
     for T, S in ((5, 2), (100, 7)):               # tiles of 256 rows, four heads to a token
         rows = 2 * S * min(256, T * 4)
-        want = r256(rows * 128 * 4) + r256(rows * 8)
+        want = r256(rows * 128 * 4) + r256(rows * 8) + r256(24 * S)
         assert lib.kv_prefill_attn_workspace_size(ctypes.byref(d), 8, T, S) == want
         assert lib.kv_workspace_size(4, ctypes.byref(d), 8, T, S) == want
     assert lib.kv_prefill_attn_workspace_size(ctypes.byref(d), 8, 100, 1) == 0
