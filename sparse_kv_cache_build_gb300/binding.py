@@ -162,6 +162,12 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(kv, stream):
+    """The stream's handle as a number; the current stream of the cache's device by default."""
+    return (torch._C._cuda_getCurrentRawStream(kv.index) if stream is None
+            else stream.cuda_stream)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -203,6 +209,11 @@ class PagedKV:
             self.k_pool.data_ptr(), self.v_pool.data_ptr(), _DT[self.k_pool.dtype], NP, Hkv,
             PS, D, self.page_table.shape[0], self.page_table.data_ptr(),
             self.page_table.shape[1], self.seq_lens.data_ptr())
+        # what the packed calls check on every step, as plain values
+        self.index, self.elem = self.k_pool.get_device(), self.k_pool.dtype
+        self.pages, self.groups, self.cols = NP, Hkv, D
+        self.sequences = self.page_table.shape[0]
+        self._ref = ctypes.byref(self.desc)
 
     @classmethod
     def from_cache(cls, cache) -> "PagedKV":
@@ -233,7 +244,7 @@ class PagedKV:
         return self.page_table.shape[1]
 
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
 
 # -------------------------------------------------------------------------------- calls
@@ -303,35 +314,45 @@ def kv_append_token(kv: PagedKV, k_new, v_new, stats, stream=None):
     return stats
 
 
-def _rows(kv: PagedKV, t, name, heads=None):
+def _rows(kv: PagedKV, t, name, heads):
     """Checks packed rows [T][heads][D] and returns their stride between tokens: the last two
     dimensions are contiguous, tokens may lie apart (a column range of a fused projection)."""
-    if t.device != kv.k_pool.device:
+    T, H, D = t.shape if t.dim() == 3 else (0, 0, 0)
+    step, head, col = t.stride() if D else (0, 0, 0)
+    if (t.get_device() == kv.index and t.dtype is kv.elem and H == heads and D == kv.cols
+            and col == 1 and (head == D or H == 1)):
+        return step if T > 1 else H * D
+    if t.get_device() != kv.index:
         raise ValueError(f"{name} must be on the cache's device {kv.k_pool.device}")
-    if t.dtype != kv.dtype:
-        raise ValueError(f"{name} must be {kv.dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != kv.head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have shape [tokens][{heads or 'heads'}][{kv.head_dim}], "
+    if t.dtype is not kv.elem:
+        raise ValueError(f"{name} must be {kv.elem}, got {t.dtype}")
+    if H != heads or D != kv.cols:
+        raise ValueError(f"{name} must have shape [tokens][{heads}][{kv.cols}], "
                          f"got {tuple(t.shape)}")
-    T, H, D = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"{name} must be contiguous within a token")
-    return t.stride(0) if T > 1 else H * D
+    raise ValueError(f"{name} must be contiguous within a token")
 
 
 def _on_device(kv: PagedKV, t, name, dtype, shape):
-    _need(t, name, dtype, shape)
-    if t.device != kv.k_pool.device:
+    if t.get_device() != kv.index:
         raise ValueError(f"{name} must be on the cache's device {kv.k_pool.device}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, name, dtype, shape)
 
 
 def _packed(kv: PagedKV, q, cu_tokens):
-    if kv.k_pool.device.index != torch.cuda.current_device():
+    """Row count, query heads and row stride of packed queries, and the offsets' pointer."""
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape [tokens][heads][{kv.cols}], got {tuple(q.shape)}")
+    T, Hq, _ = q.shape
+    stride = _rows(kv, q, "q", Hq)
+    if kv.index != torch.cuda.current_device():
         raise ValueError(f"the cache is on {kv.k_pool.device}, which is not the current device")
-    if cu_tokens is not None:
-        _on_device(kv, cu_tokens, "cu_tokens", torch.int32, (kv.batch + 1,))
-    elif q.shape[0] != kv.batch:
-        raise ValueError("without cu_tokens there is one row per sequence")
+    if cu_tokens is None:
+        if T != kv.sequences:
+            raise ValueError("without cu_tokens there is one row per sequence")
+        return T, Hq, stride, None
+    _on_device(kv, cu_tokens, "cu_tokens", torch.int32, (kv.sequences + 1,))
+    return T, Hq, stride, cu_tokens.data_ptr()
 
 
 def kv_rope_turns(inv_freq, device=None):
@@ -351,13 +372,12 @@ def kv_append_rope(kv: PagedKV, q, k_new, v_new, stats, turns=None, cu_tokens=No
     sequence), rotating queries and keys over the first 2 * len(turns) columns (turns=None: no
     rotation); pools and stats are updated in place. Returns the rotated queries (q_out, which
     may be q)."""
-    _packed(kv, q, cu_tokens)
-    T, Hq, D = q.shape
-    qs = _rows(kv, q, "q")
-    ks, vs = (_rows(kv, t, n, kv.num_kv_heads) for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    T, Hq, qs, cu = _packed(kv, q, cu_tokens)
+    Hkv, D = kv.groups, kv.cols
+    ks, vs = _rows(kv, k_new, "k_new", Hkv), _rows(kv, v_new, "v_new", Hkv)
     if k_new.shape[0] != T or v_new.shape[0] != T:
         raise ValueError("q, k_new and v_new must have the same number of rows")
-    _on_device(kv, stats, "stats", kv.dtype, (kv.k_pool.shape[0], kv.num_kv_heads, 2, D))
+    _on_device(kv, stats, "stats", kv.elem, (kv.pages, Hkv, 2, D))
     rot = 0
     if turns is not None:
         rot = 2 * turns.numel()
@@ -365,15 +385,20 @@ def kv_append_rope(kv: PagedKV, q, k_new, v_new, stats, turns=None, cu_tokens=No
     if positions is not None:
         _on_device(kv, positions, "positions", torch.int32, (T,))
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    os_ = _rows(kv, q_out, "q_out", Hq)
-    if q_out.shape[0] != T:
-        raise ValueError("q_out must have q's shape")
+        q_out = torch.empty((T, Hq, D), dtype=kv.elem, device=q.device)
+        os_ = Hq * D
+    else:
+        os_ = _rows(kv, q_out, "q_out", Hq)
+        if q_out.shape[0] != T:
+            raise ValueError("q_out must have q's shape")
     if T > 0:
-        _check("kv_append_rope", lib().kv_append_rope(
-            kv.ref(), _ptr(q), qs, Hq, _ptr(k_new), ks, _ptr(v_new), vs, _ptr(cu_tokens), T,
-            _ptr(positions), _ptr(turns), rot, int(interleaved), _ptr(q_out), os_, _ptr(stats),
-            _stream(stream)))
+        status = lib().kv_append_rope(
+            kv.ref(), q.data_ptr(), qs, Hq, k_new.data_ptr(), ks, v_new.data_ptr(), vs, cu, T,
+            None if positions is None else positions.data_ptr(),
+            None if turns is None else turns.data_ptr(), rot, interleaved, q_out.data_ptr(), os_,
+            stats.data_ptr(), _raw_stream(kv, stream))
+        if status != KV_OK:
+            raise KVError("kv_append_rope", status)
     return q_out
 
 
@@ -387,23 +412,29 @@ def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares:
                     out=None, lse=None, workspace=None, stream=None):
     """Causal attention of packed query rows [T][Hq][D] over the cache, which holds the rows'
     own keys and values already: (out of the cache's dtype, lse float32)."""
-    _packed(kv, q, cu_tokens)
-    T, Hq, D = q.shape
-    qs = _rows(kv, q, "q")
+    T, Hq, qs, cu = _packed(kv, q, cu_tokens)
+    D = kv.cols
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out = torch.empty((T, Hq, D), dtype=kv.elem, device=q.device)
+    else:
+        _on_device(kv, out, "out", kv.elem, (T, Hq, D))
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    _on_device(kv, out, "out", kv.dtype, (T, Hq, D))
-    _on_device(kv, lse, "lse", torch.float32, (T, Hq))
+    else:
+        _on_device(kv, lse, "lse", torch.float32, (T, Hq))
     if T == 0:
         return out, lse
     if workspace is None:
         nbytes = kv_prefill_attn_workspace_size(kv, Hq, T, num_shares)
         workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
-    _check("kv_prefill_attn", lib().kv_prefill_attn(
-        kv.ref(), _ptr(q), qs, Hq, _ptr(cu_tokens), T, float(sm_scale), int(num_shares),
-        _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    elif workspace.get_device() != kv.index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {kv.k_pool.device}")
+    status = lib().kv_prefill_attn(
+        kv.ref(), q.data_ptr(), qs, Hq, cu, T, sm_scale, num_shares, out.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _raw_stream(kv, stream))
+    if status != KV_OK:
+        raise KVError("kv_prefill_attn", status)
     return out, lse
 
 
