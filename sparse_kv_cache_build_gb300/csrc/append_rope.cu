@@ -42,15 +42,6 @@ struct RopeArgs {
 // Sixteen columns of a row as floats: two chunks of eight.
 struct Cols { float a[8], b[8]; };
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float* f);
-template <> __device__ __forceinline__ void load8<bf16_t>(const bf16_t* p, float* f) {
-  chunk_to_f32<bf16_t>(*reinterpret_cast<const uint4*>(p), f);
-}
-template <> __device__ __forceinline__ void load8<float>(const float* p, float* f) {
-  chunk_to_f32<float>(*reinterpret_cast<const uint4*>(p), f);
-  chunk_to_f32<float>(*reinterpret_cast<const uint4*>(p + 4), f + 4);
-}
-
 // Rounds to the storage type (to nearest even) and leaves the rounded values in f.
 template <typename T> __device__ __forceinline__ void store8(T* p, float* f);
 template <> __device__ __forceinline__ void store8<bf16_t>(bf16_t* p, float* f) {
@@ -102,11 +93,34 @@ __device__ __forceinline__ void rotate(Cols* r, const Angle& x) {
   }
 }
 
+// A lane's sixteen columns as they lie in memory: loads of several rows are issued before the
+// first is unpacked.
+template <typename T> struct Raw {
+  static constexpr int N = 8 * sizeof(T) / 16;       // 16-byte loads per chunk
+  uint4 a[N], b[N];
+};
 template <typename T>
-__device__ __forceinline__ void load_cols(const void* base, int64_t at, int ca, int cb, Cols* r) {
+__device__ __forceinline__ void load_raw(const void* base, int64_t at, int ca, int cb,
+                                         Raw<T>* r) {
   const T* p = static_cast<const T*>(base) + at;
-  load8<T>(p + ca, r->a);
-  load8<T>(p + cb, r->b);
+#pragma unroll
+  for (int i = 0; i < Raw<T>::N; ++i) {
+    r->a[i] = reinterpret_cast<const uint4*>(p + ca)[i];
+    r->b[i] = reinterpret_cast<const uint4*>(p + cb)[i];
+  }
+}
+template <typename T> __device__ __forceinline__ void unpack(const Raw<T>& r, Cols* c) {
+#pragma unroll
+  for (int i = 0; i < Raw<T>::N; ++i) {
+    chunk_to_f32<T>(r.a[i], c->a + 8 / Raw<T>::N * i);
+    chunk_to_f32<T>(r.b[i], c->b + 8 / Raw<T>::N * i);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load_cols(const void* base, int64_t at, int ca, int cb, Cols* c) {
+  Raw<T> r;
+  load_raw<T>(base, at, ca, cb, &r);
+  unpack<T>(r, c);
 }
 template <typename T>
 __device__ __forceinline__ void store_cols(void* base, int64_t at, int ca, int cb, Cols* r) {
@@ -134,6 +148,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
   constexpr int LPR = D / 16;            // lanes per row
   constexpr int RPW = 32 / LPR;          // rows per warp step
+  constexpr int HEADS = sizeof(T) == 2 ? 4 : 2;      // query rows in flight per lane
   __shared__ float sh_mn[kRopeWarps][D], sh_mx[kRopeWarps][D];
   pdl_trigger();
   pdl_wait();
@@ -170,15 +185,20 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
   }
   for (int t = t0 + warp * RPW + r; t < t1; t += kRopeWarps * RPW) {
     const int64_t row = sr.row0 + (t - start);
-    Cols k, v;
-    load_cols<T>(a.k, row * a.k_stride + (int64_t)g * D, ca, cb, &k);
-    load_cols<T>(a.v, row * a.v_stride + (int64_t)g * D, ca, cb, &v);
+    Raw<T> rk, rv, rq[HEADS];
+    load_raw<T>(a.k, row * a.k_stride + (int64_t)g * D, ca, cb, &rk);
+    load_raw<T>(a.v, row * a.v_stride + (int64_t)g * D, ca, cb, &rv);
+    const int64_t q_row = row * a.q_stride + (int64_t)g * G * D;
+#pragma unroll
+    for (int h = 0; h < HEADS; ++h)
+      if (h < G) load_raw<T>(a.q, q_row + h * D, ca, cb, &rq[h]);
     Angle x;
-    if (turns) {
-      angles_at(f, a.positions != nullptr ? a.positions[row] : t, &x);
-      rotate<INTER>(&k, x);
-    }
+    if (turns) angles_at(f, a.positions != nullptr ? a.positions[row] : t, &x);
     if (mapped) {
+      Cols k, v;
+      unpack<T>(rk, &k);
+      unpack<T>(rv, &v);
+      if (turns) rotate<INTER>(&k, x);
       const int64_t slot = (((int64_t)P * Hkv + g) * PS + (t - page * PS)) * D;
       store_cols<T>(kp, slot, ca, cb, &k);
       store_cols<T>(vp, slot, ca, cb, &v);
@@ -190,11 +210,17 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
         mx.b[e] = upper(mx.b[e], k.b[e]);
       }
     }
-    for (int h = g * G; h < (g + 1) * G; ++h) {
-      Cols q;
-      load_cols<T>(a.q, row * a.q_stride + (int64_t)h * D, ca, cb, &q);
-      if (turns) rotate<INTER>(&q, x);
-      store_cols<T>(a.q_out, row * a.q_out_stride + (int64_t)h * D, ca, cb, &q);
+    for (int h0 = 0; h0 < G; h0 += HEADS) {
+#pragma unroll
+      for (int h = 0; h < HEADS; ++h) {
+        if (h0 + h >= G) break;
+        Cols q;
+        unpack<T>(rq[h], &q);
+        if (h0 + HEADS + h < G)
+          load_raw<T>(a.q, q_row + (int64_t)(h0 + HEADS + h) * D, ca, cb, &rq[h]);
+        if (turns) rotate<INTER>(&q, x);
+        store_cols<T>(a.q_out, row * a.q_out_stride + (int64_t)(g * G + h0 + h) * D, ca, cb, &q);
+      }
     }
   }
   if (!mapped) return;
