@@ -1,110 +1,133 @@
 // Causal prompt attention: the choice of kernel, and the join of the items its blocks shared.
+#include <type_traits>
+
 #include "prefill.cuh"
 
 namespace skv {
 namespace {
 
 constexpr int kMergeWarps = 8;
-constexpr int kMergeRowGroups = 8;       // blocks per border, each with a share of the rows
+constexpr int kMergeUnits = 4;           // (row, strip) units per warp at most
 
-template <typename T> __device__ __forceinline__ void store2(T* p, float a, float b);
-template <> __device__ __forceinline__ void store2<bf16_t>(bf16_t* p, float a, float b) {
-  uint32_t w;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
-  *reinterpret_cast<uint32_t*>(p) = w;
+// V consecutive floats, read as one word.
+template <int V> union Strip {
+  using Raw = typename std::conditional<V == 4, float4,
+                                        typename std::conditional<V == 2, float2, float>::type>::type;
+  Raw raw;
+  float f[V];
+  __device__ __forceinline__ Strip() {}
+};
+
+template <typename T> __device__ __forceinline__ void store1(T* p, float v);
+template <> __device__ __forceinline__ void store1<bf16_t>(bf16_t* p, float v) {
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(p->bits) : "f"(v));
 }
-template <> __device__ __forceinline__ void store2<float>(float* p, float a, float b) {
-  *reinterpret_cast<float2*>(p) = make_float2(a, b);
-}
+template <> __device__ __forceinline__ void store1<float>(float* p, float v) { *p = v; }
 
 // Border number c = blockIdx.x + 1 between blocks c - 1 and c: if it cuts an item, and is the
 // first that does, joins the item's parts row by row:
 //   out = sum_p acc_p 2^(m_p - M) / L,  M = max_p m_p,  L = sum_p l_p 2^(m_p - M).
 // The parts are those of blocks c - 1, c, ... up to the one that reaches the item's end. One
-// warp per row, lanes over the parts for (m, l) and over the columns for the accumulators,
-// whose loads are independent of one another. A part without keys for a row (m = -inf) has no
-// accumulator to read.
-template <typename T, int D>
+// warp takes 32 V columns of a row; notes, then (m, l) and accumulators together, are the only
+// dependent reads, with several parts in flight. Few rows (single tokens: many parts each) take
+// V = 1, so that four warps share a row (one token over 32K: 4.6 us from the last part to the
+// output, against 7 us); tiles of rows take V = D / 32 (8192 tokens 429 us a call, against 464 us
+// with V = 1, whose warps are four times as many). A part without keys for a row (m = -inf) has
+// no accumulator: what lies there is read and not used.
+template <typename T, int D, int V>
 __global__ void __launch_bounds__(kMergeWarps * 32)
 prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
-  constexpr int PAIRS = D / 64;            // column pairs per lane
+  constexpr int STRIPS = D / (32 * V), BATCH = V == 4 ? 8 : 16;
   pdl_trigger();
   pdl_wait();
   const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const BorderNote it = a.notes[c], before = a.notes[c - 1];
-  auto continues = [&](const BorderNote& n) {
-    return n.row0 == it.row0 && n.g == it.g && n.kt0 > 0 && n.kt0 < n.nk;
+  // lane i: the note of block c - 1 + i
+  const BorderNote none{0, 0, 0, 0, 0, 0};
+  BorderNote n = c - 1 + lane < a.NC ? a.notes[c - 1 + lane] : none;
+  const int row0 = __shfl_sync(0xffffffffu, n.row0, 1), g = __shfl_sync(0xffffffffu, n.g, 1);
+  const int n_tok = __shfl_sync(0xffffffffu, n.n_tok, 1);
+  auto continues = [&](const BorderNote& x) {
+    return x.row0 == row0 && x.g == g && x.kt0 > 0 && x.kt0 < x.nk;
   };
-  if (!continues(it) || continues(before)) return;
-  const int rows = it.n_tok << a.log_g;
-  for (int row = blockIdx.y * kMergeWarps + warp; row < rows;
-       row += kMergeRowGroups * kMergeWarps) {
-    float M = -INFINITY, L = 0.f;
-    float2 acc[PAIRS];
+  const uint32_t first = __ballot_sync(0xffffffffu, continues(n));
+  if ((first & 3u) != 2u) return;
+  const int units = (n_tok << a.log_g) * STRIPS;
+  for (int unit = blockIdx.y * kMergeWarps + warp; unit < units;
+       unit += gridDim.y * kMergeWarps) {
+    const int row = unit / STRIPS, col = ((unit % STRIPS) * 32 + lane) * V;
+    float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-    for (int p = 0; p < PAIRS; ++p) acc[p] = make_float2(0.f, 0.f);
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
     bool more = true;
     for (int j0 = c - 1; more; j0 += 32) {
-      // block c - 1 ends with this item, the others begin with it
       const int j = j0 + lane;
-      BorderNote n = it;
-      if (j >= c && j < a.NC) n = a.notes[j];
-      const bool part = j == c - 1 || (j < a.NC && continues(n));
-      const int parts = __popc(__ballot_sync(0xffffffffu, part));       // the first lanes
+      BorderNote x = n;
+      if (j0 > c - 1) x = j < a.NC ? a.notes[j] : none;
+      const bool head = j == c - 1, part = head || continues(x);
+      const uint32_t run = __ballot_sync(0xffffffffu, part);
+      const int parts = run == 0xffffffffu ? 32 : __ffs(~run) - 1;       // the lanes before a gap
       more = parts == 32;
-      const int64_t mine = (int64_t)(j == c - 1 ? 2 * j + 1 : 2 * j) * a.part_rows + row;
+      // block c - 1 ends with this item, the others begin with it
+      const int64_t mine = (int64_t)(head ? 2 * j + 1 : 2 * j) * a.part_rows + row;
       float m = -INFINITY, l = 0.f;
-      if (part && (j == c - 1 || n.kt1 > n.kt0)) {
+      if (lane < parts && (head || x.kt1 > x.kt0)) {
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + mine);
         m = ml.x;
         l = ml.y;
       }
-      float now = fmaxf(M, m);
+      for (int e0 = 0; e0 < parts; e0 += BATCH) {
+        Strip<V> v[BATCH];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-      if (now == -INFINITY) continue;
-      const float keep = exp2f(M - now), w = exp2f(m - now);
-      M = now;
-      float sum = l * w;
+        for (int e = 0; e < BATCH; ++e) {
+          const int64_t from = __shfl_sync(0xffffffffu, mine, (e0 + e) & 31);
+          if (e0 + e < parts)
+            v[e].raw = __ldcg(reinterpret_cast<const typename Strip<V>::Raw*>(a.part_acc + from * D + col));
+        }
+        if (e0 == 0) {
+          float now = fmaxf(M, m);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      L = fmaf(L, keep, sum);
+          for (int o = 16; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+          const float ref = now == -INFINITY ? 0.f : now;
+          const float keep = exp2f(M - ref);
+          M = now;
+          m = exp2f(m - ref);                      // now the part's weight
+          float sum = l * m;
 #pragma unroll
-      for (int p = 0; p < PAIRS; ++p) {
-        acc[p].x *= keep;
-        acc[p].y *= keep;
-      }
-#pragma unroll 8
-      for (int e = 0; e < parts; ++e) {
-        const float we = __shfl_sync(0xffffffffu, w, e);
-        const int64_t from = __shfl_sync(0xffffffffu, mine, e);
-        float2 v[PAIRS];
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          L = fmaf(L, keep, sum);
 #pragma unroll
-        for (int p = 0; p < PAIRS; ++p)          // no keys, or nothing left of them: not read
-          v[p] = we == 0.f ? make_float2(0.f, 0.f)
-                           : __ldcg(reinterpret_cast<const float2*>(a.part_acc + from * D) + lane +
-                                    32 * p);
+          for (int i = 0; i < V; ++i) acc[i] *= keep;
+        }
 #pragma unroll
-        for (int p = 0; p < PAIRS; ++p) {
-          acc[p].x = fmaf(v[p].x, we, acc[p].x);
-          acc[p].y = fmaf(v[p].y, we, acc[p].y);
+        for (int e = 0; e < BATCH; ++e) {
+          const float w = __shfl_sync(0xffffffffu, m, (e0 + e) & 31);
+          if (e0 + e < parts && w != 0.f)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = fmaf(v[e].f[i], w, acc[i]);
         }
       }
     }
-    const int64_t out_row = (int64_t)(it.row0 + (row >> a.log_g)) * a.Hq + it.g * a.G +
+    const int64_t out_row = (int64_t)(row0 + (row >> a.log_g)) * a.Hq + g * a.G +
                             (row & (a.G - 1));
-    const float inv = 1.f / L;                     // every row sees its own token: L > 0
-    T* dst = static_cast<T*>(a.out) + out_row * D + 2 * lane;
+    T* dst = static_cast<T*>(a.out) + out_row * D + col;
 #pragma unroll
-    for (int p = 0; p < PAIRS; ++p) store2<T>(dst + 64 * p, acc[p].x * inv, acc[p].y * inv);
-    if (lane == 0 && a.lse != nullptr) a.lse[out_row] = (M + log2f(L)) * kLn2;
+    for (int i = 0; i < V; ++i) store1<T>(dst + i, acc[i] / L);        // L > 0: its own token
+    if (col == 0 && a.lse != nullptr) a.lse[out_row] = (M + log2f(L)) * kLn2;
   }
 }
 
+constexpr int kMergeFewRows = 64;
+
+template <typename T, int D, int V>
+cudaError_t merge_v(const PrefillArgs& a, cudaStream_t s) {
+  const int units = a.part_rows * (D / (32 * V));
+  return launch_pdl(prefill_merge_kernel<T, D, V>,
+                    dim3(a.NC - 1, ceil_div(units, kMergeWarps * kMergeUnits)),
+                    dim3(kMergeWarps * 32), 0, s, a);
+}
 template <typename T, int D>
 cudaError_t merge_t(const PrefillArgs& a, cudaStream_t s) {
-  return launch_pdl(prefill_merge_kernel<T, D>, dim3(a.NC - 1, kMergeRowGroups),
-                    dim3(kMergeWarps * 32), 0, s, a);
+  return a.part_rows < kMergeFewRows ? merge_v<T, D, 1>(a, s) : merge_v<T, D, D / 32>(a, s);
 }
 
 }  // namespace

@@ -103,10 +103,17 @@ struct PrefillItem {
   int part;             // workspace part, or -1: the block has the whole item
 };
 
+// a / b for a >= 0, b > 0, in 32 bits where they fit: a 64-bit division is a quarter of a
+// microsecond of dependent instructions, and a block's start has several.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Key tiles of an item before border `y` of the line; the item starts at x and costs `unit`
 // per key tile. Borders that would leave a few tiles on one side move to the item's end.
 __device__ __forceinline__ int tiles_before(int64_t y, int64_t x, int nk, int unit) {
-  const int64_t k = (y - x - kItemCost + unit - 1) / unit;
+  const int64_t k = (y - x - kItemCost + unit - 1) >> (unit - 1);       // unit is 1 or 2
   if (k >= nk) return nk;
   return k < kMinPart ? 0 : nk - k < kMinPart ? nk : (int)k;
 }
@@ -123,7 +130,7 @@ template <typename S> class ItemWalk {
     // the last item that starts at or before lo
     const int64_t head = seq_.cost(seq_.tiles(), a.log_g);
     if (head > 0) {
-      g_ = (int)((lo - x_) / head);
+      g_ = (int)divide(lo - x_, head);
       x_ += g_ * head;
       int t = 0, end = seq_.tiles();
       while (end - t > 1) {
@@ -203,7 +210,11 @@ struct LineScratch {
   int64_t total, before;
   int b;
 };
-struct LinePlace { int64_t total, before; int b; };
+struct LinePlace {
+  int64_t total, before;
+  int b;
+  int64_t lo, hi;         // block i's piece: floor(total i / NC) up to the next block's
+};
 
 template <typename S>
 __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cache_desc& d,
@@ -232,7 +243,11 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
     if (w < warp) before += sh->sums[w];
     total += sh->sums[w];
   }
-  const int64_t y = total * i / a.NC;        // < total: some thread holds it, unless all is empty
+  const int64_t each = divide(total, a.NC);
+  const int rest = (int)(total - each * a.NC);
+  const int64_t lo = each * i + rest * i / a.NC;       // rest * i < 2^20
+  const int64_t hi = each * (i + 1) + rest * (i + 1) / a.NC;
+  const int64_t y = lo;                      // < total: some thread holds it, unless all is empty
   if (mine > 0 && y >= before && y < before + mine) {
     int b = b0;
     for (; b < b1 - 1; ++b) {
@@ -244,7 +259,7 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
     sh->before = before;
   }
   __syncthreads();
-  return LinePlace{total, sh->before, sh->b};
+  return LinePlace{total, sh->before, sh->b, lo, hi};
 }
 
 // Launchers.

@@ -180,7 +180,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   pdl_wait();
   finish_empty<bf16_t, D>(ctx, d, pr, a);
   const LinePlace at = find_place<MmaShape>(ctx, d, pr, a, blockIdx.x, &scratch);
-  const int64_t lo = at.total * blockIdx.x / a.NC, hi = at.total * (blockIdx.x + 1) / a.NC;
+  const int64_t lo = at.lo, hi = at.hi;
   if (at.total == 0 || lo >= hi) {                 // nothing, or less than a unit of the line
     if (tid == 0 && a.notes != nullptr)
       a.notes[blockIdx.x] =

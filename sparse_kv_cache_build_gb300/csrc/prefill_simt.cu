@@ -53,7 +53,7 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
   pdl_wait();
   finish_empty<float, D>(ctx, d, pr, a);
   const LinePlace at = find_place<SimtShape>(ctx, d, pr, a, blockIdx.x, &scratch);
-  const int64_t lo = at.total * blockIdx.x / a.NC, hi = at.total * (blockIdx.x + 1) / a.NC;
+  const int64_t lo = at.lo, hi = at.hi;
   if (at.total == 0) {
     if (threadIdx.x == 0 && a.notes != nullptr) a.notes[blockIdx.x] = BorderNote{0, 0, 0, 0, 0, 0};
     return;
