@@ -220,10 +220,8 @@ kv_status check_packed(const kv_cache_desc* d, const int32_t* cu_tokens, int32_t
 
 constexpr int kPrefillMaxShares = 1024;
 
-// Blocks the prompt attention divides a batch among: as many as are resident at once.
-int prefill_shares(const kv_cache_desc* d, int asked, const DeviceState* st) {
-  return asked > 0 ? asked : st->sms * prefill_blocks_per_sm(d->dtype);
-}
+// Blocks the prompt attention divides a batch among: as many as are resident at once, one per SM.
+int prefill_shares(int asked, const DeviceState* st) { return asked > 0 ? asked : st->sms; }
 
 // Two parts per block, of a tile's rows or all the rows there are.
 struct PrefillLayout { int rows; size_t ml, notes, total; };
@@ -379,7 +377,7 @@ size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_
   if (G != 1 && G != 2 && G != 4 && G != 8) return 0;
   DeviceState* st = nullptr;
   if (num_shares == 0 && device_state(&st) != KV_OK) return 0;
-  return prefill_layout(cache, G, total_tokens, prefill_shares(cache, num_shares, st)).total;
+  return prefill_layout(cache, G, total_tokens, prefill_shares(num_shares, st)).total;
 }
 
 kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
@@ -411,7 +409,7 @@ kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_s
   a.Hq = num_q_heads;
   a.G = num_q_heads / cache->num_kv_heads;
   while (1 << a.log_g < a.G) ++a.log_g;
-  a.NC = prefill_shares(cache, num_shares, st);
+  a.NC = prefill_shares(num_shares, st);
   const PrefillLayout L = prefill_layout(cache, a.G, total_tokens, a.NC);
   if (L.total > 0) {
     if (workspace == nullptr || workspace_bytes < L.total ||

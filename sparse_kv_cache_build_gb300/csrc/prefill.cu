@@ -133,7 +133,6 @@ cudaError_t merge_t(const PrefillArgs& a, cudaStream_t s) {
 }  // namespace
 
 int prefill_tile_rows(int dtype) { return dtype == KV_BF16 ? MmaShape::rows : SimtShape::rows; }
-int prefill_blocks_per_sm(int dtype) { return dtype == KV_BF16 ? 1 : 2; }
 
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {

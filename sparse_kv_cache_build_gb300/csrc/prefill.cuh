@@ -264,9 +264,8 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
 
 // Launchers.
 using MmaShape = TileShape<256, 128, 128>;       // bf16, tensor cores
-using SimtShape = TileShape<64, 64, 0>;          // fp32, CUDA cores
+using SimtShape = TileShape<128, 64, 0>;         // fp32, CUDA cores
 int prefill_tile_rows(int dtype);
-int prefill_blocks_per_sm(int dtype);
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
 cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,

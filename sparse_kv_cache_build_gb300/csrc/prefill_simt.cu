@@ -1,140 +1,164 @@
 // Causal prompt attention for fp32 caches, on the CUDA cores.
 //
-// One block takes 64 rows and walks their keys 64 at a time, with the running maximum and sum
-// of the softmax per row. 256 threads hold 4 x 4 of the 64 x 64 scores and 4 x D/16 of the
-// output each; the operands come from shared memory as 16-byte reads (rows padded by four
-// floats, so that the sixteen keys of a warp's read fall into different banks), the
-// probabilities go through the key tile's buffer once its scores are done.
+// A block takes 128 rows of an item and walks their keys 64 at a time, with the running maximum
+// and sum of the softmax per row; it walks its share of the batch's items (prefill.cuh).
+//
+// What bounds it is the float32 multiply-add rate (two tiles of 128 x 64 x D products a step),
+// so everything else is kept off the issue slots. 256 threads hold 8 x 4 of the 128 x 64 scores
+// and 8 x D/16 of the output each, so that twelve 16-byte reads of shared memory feed 128
+// multiply-adds, issued as packed pairs. Scores pair the even and odd columns of the head (two
+// partial sums, joined at the end), the output pairs neighbouring columns. Rows are padded by
+// four floats so that the sixteen keys of a warp's read fall into different banks. The
+// probabilities take the place of the key tile just used; the next tiles arrive by asynchronous
+// copies meanwhile. Tensor cores would need six bf16 products (or three tf32 ones, and twice the
+// shared memory there is at D = 128) for each float32 product to keep its precision.
 #include "prefill.cuh"
+#include "tcgen05.cuh"
 
 namespace skv {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int R = SimtShape::rows, KT = SimtShape::keys;
+constexpr int RPT = R / 16, KPT = KT / 16;           // rows and keys of a thread
 
 template <int D> struct SimtCfg {
   static constexpr int LD = D + 4;                   // padded row, floats
-  static constexpr int PLD = KT + 4;
-  static constexpr size_t SMEM = sizeof(float) * 3 * R * LD;
-  static_assert(R * PLD <= KT * LD, "the probabilities fit the key buffer");
+  static constexpr size_t SMEM = sizeof(float) * ((R + 4 * KT) * LD + (D == 64 ? R * KT : 0));
+  static_assert(D == 64 || R * KT <= KT * LD, "the probabilities fit the key tile");
 };
 
-// Copies R rows of D elements into padded shared rows; row(i) gives the source of row i, or NULL
-// for zeros.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               ::"r"(smem_addr(dst)), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+// Copies `rows` rows of D elements into padded shared rows; row(i) gives the source of row i, or
+// NULL for zeros.
 template <int D, typename F>
-__device__ __forceinline__ void stage_rows(float* dst, F row) {
+__device__ __forceinline__ void stage_rows(float* dst, int rows, const float* any, F row) {
   constexpr int CPR = D / 4;                         // 16-byte chunks of a row
-  for (int i = threadIdx.x; i < R * CPR; i += kThreads) {
+  for (int i = threadIdx.x; i < rows * CPR; i += kThreads) {
     const int r = i / CPR, c = (i % CPR) * 4;
     const float* src = row(r);
-    *reinterpret_cast<float4*>(dst + r * SimtCfg<D>::LD + c) =
-        src != nullptr ? *reinterpret_cast<const float4*>(src + c)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    copy16(dst + r * SimtCfg<D>::LD + c, src != nullptr ? src + c : any, src != nullptr);
   }
 }
 
-__device__ __forceinline__ void store4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
+__device__ __forceinline__ float2 lo(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi(float4 v) { return make_float2(v.z, v.w); }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
 prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ PackedRows pr,
                     const __grid_constant__ PrefillArgs a, const __grid_constant__ DevCtx ctx) {
-  using C = SimtCfg<D>;
-  constexpr int LD = C::LD, PLD = C::PLD, NC = D / 64;
+  constexpr int LD = SimtCfg<D>::LD, NC = D / 64;
   extern __shared__ __align__(16) float sm[];
   __shared__ LineScratch scratch;
   float* sq = sm;
-  float* sk = sq + R * LD;
-  float* sv = sk + KT * LD;
+  float* ring = sq + R * LD;                 // K, V, K, V
+  float* own_p = ring + 4 * KT * LD;         // at D = 64; over the K tile at D = 128
   pdl_trigger();
   pdl_wait();
   finish_empty<float, D>(ctx, d, pr, a);
   const LinePlace at = find_place<SimtShape>(ctx, d, pr, a, blockIdx.x, &scratch);
-  const int64_t lo = at.lo, hi = at.hi;
+  const int64_t lo_place = at.lo, hi_place = at.hi;
   if (at.total == 0) {
     if (threadIdx.x == 0 && a.notes != nullptr) a.notes[blockIdx.x] = BorderNote{0, 0, 0, 0, 0, 0};
     return;
   }
-  ItemWalk<SimtShape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
+  ItemWalk<SimtShape> walk(d, pr, a, ctx, lo_place, hi_place, at.b, at.before, blockIdx.x);
   if (threadIdx.x == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int Hkv = d.num_kv_heads, PS = d.page_size;
   const float* q = static_cast<const float*>(a.q);
   const float* kp = static_cast<const float*>(d.k_pool);
   const float* vp = static_cast<const float*>(d.v_pool);
+  const int turn = 16 * (ty & 1);            // the two rows of a warp's read in different banks
 
   PrefillItem it;
   while (walk.next(&it)) {
     const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
     const int rows = it.n_tok << a.log_g, keys = it.pos0 + it.n_tok;
-    __syncthreads();                         // the item before has read its rows
-    stage_rows<D>(sq, [&](int r) -> const float* {
+    // keys past the item's last are zeros: whatever their slots hold stays out of the sums
+    auto stage_tile = [&](int kt, int buf) {
+      const int u0 = kt * KT;
+      float* dst = ring + 2 * buf * KT * LD;
+      for (int which = 0; which < 2; ++which) {
+        const float* pool = which == 0 ? kp : vp;
+        stage_rows<D>(dst + which * KT * LD, KT, pool, [&](int i) -> const float* {
+          if (i >= keys - u0) return nullptr;
+          const int u = u0 + i;
+          const int P = table[u / PS];
+          if (P < 0 || P >= d.num_phys_pages) {
+            flag(ctx, KV_DEVERR_BAD_PAGE);
+            return nullptr;
+          }
+          return pool + (((int64_t)P * Hkv + it.g) * PS + u % PS) * D;
+        });
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    stage_rows<D>(sq, R, q, [&](int r) -> const float* {
       return r < rows ? q + (it.row0 + (r >> a.log_g)) * a.q_stride +
                             (int64_t)(it.g * a.G + (r & (a.G - 1))) * D
                       : nullptr;
     });
-    float m[4], l[4], o[4][4 * NC];
+    stage_tile(it.kt0, 0);
+    float m[RPT], l[RPT];
+    float2 o[RPT][2 * NC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4 * NC; ++j) o[i][j] = 0.f;
+      for (int j = 0; j < 2 * NC; ++j) o[i][j] = make_float2(0.f, 0.f);
     }
 
     for (int kt = it.kt0; kt < it.kt1; ++kt) {
-      const int u0 = kt * KT;
-      // keys past the item's last are zeros: whatever their slots hold stays out of the sums
-      auto row_of = [&](const float* pool, int i) -> const float* {
-        if (i >= keys - u0) return nullptr;
-        const int u = u0 + i;
-        const int P = table[u / PS];
-        if (P < 0 || P >= d.num_phys_pages) {
-          flag(ctx, KV_DEVERR_BAD_PAGE);
-          return nullptr;
-        }
-        return pool + (((int64_t)P * Hkv + it.g) * PS + u % PS) * D;
-      };
+      const int buf = (kt - it.kt0) & 1, u0 = kt * KT;
+      if (kt + 1 < it.kt1) {
+        stage_tile(kt + 1, buf ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
       __syncthreads();
-      stage_rows<D>(sk, [&](int i) { return row_of(kp, i); });
-      stage_rows<D>(sv, [&](int i) { return row_of(vp, i); });
-      __syncthreads();
-      float s[4][4];
+      const float* sk = ring + 2 * buf * KT * LD;
+      const float* sv = sk + KT * LD;
+      float* sp = D == 128 ? ring + 2 * buf * KT * LD : own_p;
+      float2 s2[RPT][KPT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+        for (int j = 0; j < KPT; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
       for (int c = 0; c < D; c += 4) {
-        float4 x[4], y[4];
+        float4 y[KPT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = *reinterpret_cast<const float4*>(sq + (ty * 4 + i) * LD + c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < KPT; ++j)
           y[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(sq + (ty * RPT + i) * LD + c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
-            s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
-            s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
-            s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+          for (int j = 0; j < KPT; ++j) {
+            s2[i][j] = tc::fma2(lo(x), lo(y[j]), s2[i][j]);
+            s2[i][j] = tc::fma2(hi(x), hi(y[j]), s2[i][j]);
           }
+        }
       }
-      __syncthreads();                     // the key buffer takes the probabilities
+      if (D == 128) __syncthreads();         // the key tile's buffer takes the probabilities
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int last = it.pos0 + ((ty * 4 + i) >> a.log_g);      // the row's last key
-        float top = -INFINITY;
+      for (int i = 0; i < RPT; ++i) {
+        const int row = ty * RPT + i;
+        const int last = it.pos0 + (row >> a.log_g);        // the row's last key
+        float s[KPT], top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = tx + 16 * j <= last - u0 ? s[i][j] * a.scale_log2 : -INFINITY;
-          top = fmaxf(top, s[i][j]);
+        for (int j = 0; j < KPT; ++j) {
+          s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
+          if (tx + 16 * j > last - u0) s[j] = -INFINITY;
+          top = fmaxf(top, s[j]);
         }
 #pragma unroll
         for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
@@ -144,65 +168,75 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
         m[i] = now;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p = exp2f(s[i][j] - ref);
+        for (int j = 0; j < KPT; ++j) {
+          const float p = exp2f(s[j] - ref);
           sum += p;
-          sk[(ty * 4 + i) * PLD + tx + 16 * j] = p;
+          sp[row * KT + ((tx + 16 * j + turn) & (KT - 1))] = p;
         }
+        l[i] = fmaf(l[i], keep, sum);        // this thread's keys only: joined at the end
 #pragma unroll
-        for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        l[i] = fmaf(l[i], keep, sum);
-#pragma unroll
-        for (int j = 0; j < 4 * NC; ++j) o[i][j] *= keep;
+        for (int j = 0; j < 2 * NC; ++j) {
+          o[i][j].x *= keep;
+          o[i][j].y *= keep;
+        }
       }
-      __syncwarp();                        // a row's sixteen writers are one half warp
-#pragma unroll 4
+      __syncwarp();                          // a row's sixteen writers are one half warp
+#pragma unroll 2
       for (int u = 0; u < KT; u += 4) {
-        float4 p[4];
+        float4 p[RPT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[i] = *reinterpret_cast<const float4*>(sk + (ty * 4 + i) * PLD + u);
+        for (int i = 0; i < RPT; ++i)
+          p[i] = *reinterpret_cast<const float4*>(sp + (ty * RPT + i) * KT + ((u + turn) & (KT - 1)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          float4 v[NC];
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float4 v = *reinterpret_cast<const float4*>(sv + (u + e) * LD + 64 * c + 4 * tx);
+          for (int c = 0; c < NC; ++c)
+            v[c] = *reinterpret_cast<const float4*>(sv + (u + e) * LD + 64 * c + 4 * tx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-              o[i][4 * c] = fmaf(w, v.x, o[i][4 * c]);
-              o[i][4 * c + 1] = fmaf(w, v.y, o[i][4 * c + 1]);
-              o[i][4 * c + 2] = fmaf(w, v.z, o[i][4 * c + 2]);
-              o[i][4 * c + 3] = fmaf(w, v.w, o[i][4 * c + 3]);
+          for (int i = 0; i < RPT; ++i) {
+            const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+            const float2 ww = make_float2(w, w);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              o[i][2 * c] = tc::fma2(ww, lo(v[c]), o[i][2 * c]);
+              o[i][2 * c + 1] = tc::fma2(ww, hi(v[c]), o[i][2 * c + 1]);
             }
           }
         }
       }
+      __syncthreads();                       // this tile's buffers may be filled again
     }
 
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty * 4 + i;
+    for (int i = 0; i < RPT; ++i) {
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+      const int r = ty * RPT + i;
       if (r >= rows) continue;
       if (it.part >= 0) {
         const int64_t at_part = (int64_t)it.part * a.part_rows + r;
         float* acc = a.part_acc + at_part * D;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) store4(acc + 64 * c + 4 * tx, o[i] + 4 * c);
+        for (int c = 0; c < NC; ++c)
+          *reinterpret_cast<float4*>(acc + 64 * c + 4 * tx) =
+              make_float4(o[i][2 * c].x, o[i][2 * c].y, o[i][2 * c + 1].x, o[i][2 * c + 1].y);
         if (tx == 0) {
           a.part_ml[2 * at_part] = m[i];
           a.part_ml[2 * at_part + 1] = l[i];
         }
         continue;
       }
-      const int64_t row = (int64_t)(it.row0 + (r >> a.log_g)) * a.Hq + it.g * a.G + (r & (a.G - 1));
+      const int64_t out_row = (int64_t)(it.row0 + (r >> a.log_g)) * a.Hq + it.g * a.G +
+                              (r & (a.G - 1));
       const float inv = 1.f / l[i];                 // every row sees its own token: l > 0
+      float* dst = static_cast<float*>(a.out) + out_row * D;
 #pragma unroll
-      for (int j = 0; j < 4 * NC; ++j) o[i][j] *= inv;
-      float* dst = static_cast<float*>(a.out) + row * D;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) store4(dst + 64 * c + 4 * tx, o[i] + 4 * c);
-      if (tx == 0 && a.lse != nullptr) a.lse[row] = (m[i] + log2f(l[i])) * kLn2;
+      for (int c = 0; c < NC; ++c)
+        *reinterpret_cast<float4*>(dst + 64 * c + 4 * tx) =
+            make_float4(o[i][2 * c].x * inv, o[i][2 * c].y * inv, o[i][2 * c + 1].x * inv,
+                        o[i][2 * c + 1].y * inv);
+      if (tx == 0 && a.lse != nullptr) a.lse[out_row] = (m[i] + log2f(l[i])) * kLn2;
     }
   }
 }
