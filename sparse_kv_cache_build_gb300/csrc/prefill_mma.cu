@@ -43,7 +43,7 @@ constexpr int kMmaWarp = 8, kLoadWarp = 9, kItemWarp = 10, kReadyWarp = 11;
 constexpr int kItems = 4;              // items known ahead
 constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;     // (2 * 208 + 88) * 128 = 384 * 168
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;     // (2 * 216 + 72) * 128 = 384 * 168
 constexpr float kLazy = 8.f;           // log2 of the growth that forces a rescale
 
 template <int D> struct Cfg {
@@ -214,15 +214,23 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     for (int j = 0;; ++j) {
       ok = item_ready(j);
       if (!ok) break;
-      const PrefillItem it = items[j % kItems];
-      if (it.kt0 >= it.kt1) break;
-      const Plan plan(it, log_g);
-      const int n = plan.tiles(w), rows = it.n_tok << log_g;
-      const int row = plan.wide ? w * 128 + r : r;
-      const int last = it.pos0 + (row >> log_g);                  // the row's last key
-      const int warp_row = row - lane;
-      const bool idle = warp_row >= rows;                         // no row in this warp
-      const int warp_first = it.pos0 + (warp_row >> log_g);       // its first row's last key
+      // What the tiles need of the item; it is read again for the output (its registers are
+      // short while a row's 128 scores are held).
+      int n, row, seen, warp_seen, step;
+      bool idle;
+      {
+        const PrefillItem it = items[j % kItems];
+        if (it.kt0 >= it.kt1) break;
+        const Plan plan(it, log_g);
+        n = plan.tiles(w);
+        row = plan.wide ? w * 128 + r : r;
+        idle = row - lane >= it.n_tok << log_g;                   // no row in this warp
+        // the last key that the row sees, and the warp's first row, from the first tile's first
+        const int u0 = (it.kt0 + plan.tile(w, 0)) * kKeys;
+        seen = it.pos0 + (row >> log_g) - u0;
+        warp_seen = it.pos0 + ((row - lane) >> log_g) - u0;
+        step = plan.wide ? kKeys : 2 * kKeys;
+      }
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
         ok = mbar_wait_bounded(s_full + w, tiles_seen & 1, ctx.wait_ns);
@@ -232,18 +240,21 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         uint32_t s[128];
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, ref2;
         if (!idle) {
-          const int u0 = (it.kt0 + plan.tile(w, i)) * kKeys;
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, s + 32 * c);
           tc::wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::after_wait(s + 32 * c);
-          if (warp_first - u0 < kKeys - 1) {                      // on the border
-            const int seen = last - u0;
+          if (warp_seen < kKeys - 1) {                            // on the border
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > seen) s[c] = 0xff800000u;
+            for (int q = 0; q < 4; ++q)
+              if (warp_seen < 32 * q + 31)
+#pragma unroll
+                for (int c = 32 * q; c < 32 * q + 32; ++c)
+                  if (c > seen) s[c] = 0xff800000u;
           }
+          seen -= step;
+          warp_seen -= step;
           float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -302,6 +313,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       }
       if (!ok) break;
       // ---- output
+      const PrefillItem it = items[j % kItems];
+      const Plan plan(it, log_g);
+      const int rows = it.n_tok << log_g, warp_row = row - lane;
       const bool join = !plan.wide && plan.n1 > 0;
       if (n > 0) ok = mbar_wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
       if (!ok) break;
