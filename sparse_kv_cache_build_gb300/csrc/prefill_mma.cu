@@ -278,6 +278,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                 uint32_t o[16];
                 tc::ld16(to + c, o);
                 tc::wait_ld();
+                tc::after_wait16(o);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                 tc::st16(to + c, o);
@@ -360,11 +361,13 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           uint32_t raw[32];
           tc::ld32(to + c, raw);
           tc::wait_ld();
+          tc::after_wait(raw);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]) * f0;
           if (join) {
             tc::ld32(to + D + c, raw);
             tc::wait_ld();
+            tc::after_wait(raw);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(raw[e]), f1, o[e]);
           }
@@ -373,16 +376,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) =
               make_uint4(x, y, z, u);
         };
-        auto flush = [&](uint8_t* base, int64_t row_bytes, bool packed) {
+        auto flush = [&](uint8_t* base, uint32_t row_bytes, bool packed) {
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int k = 4 * e + (lane >> 3), chunk = lane & 7, out_row = warp_row + k;
             const uint4 v = *reinterpret_cast<const uint4*>(stage + k * 128 +
                                                             ((chunk ^ (k & 7)) << 4));
-            const int64_t index = packed ? (int64_t)(out_row >> log_g) * a.Hq + (out_row & (a.G - 1))
-                                         : out_row;
-            if (out_row < rows) *reinterpret_cast<uint4*>(base + index * row_bytes + chunk * 16) = v;
+            const uint32_t index =
+                packed ? (uint32_t)((out_row >> log_g) * a.Hq + (out_row & (a.G - 1))) : out_row;
+            if (out_row < rows)
+              *reinterpret_cast<uint4*>(base + (uint64_t)index * row_bytes + chunk * 16) = v;
           }
           __syncwarp();
         };
