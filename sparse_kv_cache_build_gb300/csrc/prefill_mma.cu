@@ -114,6 +114,16 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
         "r"(smem_addr(bar)) : "memory");
 }
 
+// The reverse, for 32 rows of the output: from shared memory, one group of copies per call.
+__device__ __forceinline__ void tma_store_rows(const CUtensorMap* map, const void* src, int x,
+                                               int head, int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+      "cp.async.bulk.commit_group;"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(smem_addr(src))
+      : "memory");
+}
+
 // A value that is the same in every lane, said so that the compiler keeps it, and what follows
 // from it, in uniform registers: the products' descriptors come from there.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -123,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
                    const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_out,
                    const __grid_constant__ kv_cache_desc d,
                    const __grid_constant__ PackedRows pr, const __grid_constant__ PrefillArgs a,
                    const __grid_constant__ DevCtx ctx) {
@@ -372,6 +383,8 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(raw[e]), f1, o[e]);
           }
         };
+        // Whole rows of a full warp leave by TMA while the warp goes on.
+        const bool by_tma = it.part < 0 && warp_row + 32 <= rows;
         auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t u) {
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4)) =
               make_uint4(x, y, z, u);
@@ -395,6 +408,8 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
               static_cast<uint16_t*>(a.out) + ((int64_t)it.row0 * a.Hq + it.g * a.G) * D);
 #pragma unroll 1
           for (int c = 0; c < D; c += 64) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();                          // the copy before has read the buffer
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float o[32];
@@ -406,11 +421,20 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                     tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
                     tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
             }
-            flush(out + c * 2, D * 2, true);
+            if (by_tma) {
+              tc::fence_async_smem();
+              __syncwarp();
+              if (lane == 0)
+                tma_store_rows(&map_out, stage, c, it.g * a.G, it.row0 + (warp_row >> log_g));
+            } else {
+              flush(out + c * 2, D * 2, true);
+            }
           }
         } else if (n > 0) {
           uint8_t* out = reinterpret_cast<uint8_t*>(a.part_acc +
                                                     (int64_t)it.part * a.part_rows * D);
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -436,6 +460,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       }
       item_done(j);
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
   } else {
     tc::fewer_regs<kRegsOther>();
@@ -725,9 +750,10 @@ template <int D>
 cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
                      DevCtx ctx, cudaStream_t s) {
   using C = Cfg<D>;
-  CUtensorMap mk, mv, mq;
+  CUtensorMap mk, mv, mq, mo;
   if (!pool_tensor_map(&mk, d.k_pool, d) || !pool_tensor_map(&mv, d.v_pool, d) ||
-      !rows_tensor_map(&mq, a.q, a.q_stride, a.Hq, D, pr.total, a.G, 128 / a.G))
+      !rows_tensor_map(&mq, a.q, a.q_stride, a.Hq, D, pr.total, a.G, 128 / a.G) ||
+      !rows_tensor_map(&mo, a.out, (int64_t)a.Hq * D, a.Hq, D, pr.total, a.G, 32 / a.G))
     return cudaErrorInvalidValue;
   auto kern = prefill_mma_kernel<D>;
   // set once per device; setting it twice from two threads is harmless
@@ -740,7 +766,7 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev].store(1, std::memory_order_release);
   }
-  return launch_pdl(kern, dim3(a.NC), dim3(kThreads), C::SMEM, s, mk, mv, mq, d, pr, a, ctx);
+  return launch_pdl(kern, dim3(a.NC), dim3(kThreads), C::SMEM, s, mk, mv, mq, mo, d, pr, a, ctx);
 }
 
 }  // namespace
