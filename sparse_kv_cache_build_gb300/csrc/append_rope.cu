@@ -162,8 +162,9 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
   const int b = find_sequence(pr, d.batch, PS, 2, item, &base);
   const SeqRows sr = seq_rows(ctx, d, pr, b);
   const int start = sr.len - sr.n;
+  // item < base only where the offsets fall or do not start at zero: that is nobody's number
   const int page = start / PS + (item - base);
-  if (sr.n == 0 || (int64_t)page * PS >= sr.len) return;
+  if (sr.n == 0 || item < base || (int64_t)page * PS >= sr.len) return;
   const int t0 = max(start, page * PS), t1 = min(sr.len - page * PS, PS) + page * PS;
   const int P = d.page_table[(long)b * d.page_table_stride + page];
   const bool mapped = P >= 0 && P < d.num_phys_pages;

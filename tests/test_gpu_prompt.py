@@ -295,6 +295,28 @@ def test_append_flags_bad_data_and_writes_nothing_there():
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("cu", [(48, 54, 60, 60, 60, 60), (60, 60, 60, 60, 60, 60),
+                                (0, 20, 40, 60, 10, 12), (0, 50, 55, 60, 0, 4)])
+def test_append_with_offsets_that_number_no_page(cu):
+    """Offsets that start above zero or fall leave numbers of the grid before the first page of
+    the sequence they are found in: no table entry, slot or statistic belongs to them."""
+    c = Case((12, 12, 12, 12, 12), (40, 0, 3, 20, 16))
+    stats = c.past_stats()
+    skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats,
+                       cu_tokens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    st, flags = skv.kv_check_device_errors()
+    assert st == -5 and flags == 2
+    # what was written is the statistics of what is cached, as far as each page is filled
+    cached = skv.kv_build_page_stats(c.kv, stats=stats.clone())
+    for b, (n, r) in enumerate(zip(np.diff(cu), cu)):
+        if n < 0 or n > c.lens[b]:
+            continue
+        for page in range((c.lens[b] - n) // c.PS, -(-c.lens[b] // c.PS) if n else 0):
+            P = int(c.table[b, page])
+            if page * c.PS >= c.lens[b] - n:
+                assert torch.equal(stats[P], cached[P]), (b, page)
+
+
 # ------------------------------------------------------------------------ attention
 
 ATTN = [
