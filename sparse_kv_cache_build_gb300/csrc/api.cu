@@ -325,13 +325,25 @@ kv_status kv_append_token(const kv_cache_desc* cache, const void* k_new, const v
   return from_cuda(launch_append(*cache, k_new, v_new, stats, ctx, stream));
 }
 
+// f / (2 pi) as a fraction of a turn in units of 2^-64. One double would leave 2^-54 of a turn,
+// which a position multiplies (2^-23 at the largest), so the quotient is kept in two: hi, and lo
+// from hi's remainder, with 2 pi in two doubles. The parts are taken of magnitudes, as
+// x - floor(x) rounds for small negative x.
 kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns) {
+  constexpr double kTurn = 6.283185307179586476925286766559;        // 2 pi rounded, and the rest
+  constexpr double kTurnRest = 2.4492935982947064e-16;
   if (inv_freq == nullptr || turns == nullptr || n <= 0) return KV_ERR_INVALID_ARG;
+  auto fraction = [](double x) {                     // of |x|; below 1, so it fits
+    const double m = fabs(x);
+    const uint64_t u = (uint64_t)ldexp(m - floor(m), 64);
+    return x < 0 ? 0 - u : u;
+  };
   for (int32_t j = 0; j < n; ++j) {
-    if (!isfinite(inv_freq[j])) return KV_ERR_INVALID_ARG;
-    const double t = inv_freq[j] / 6.283185307179586476925286766559;
-    const double frac = t - floor(t);                  // [0, 1]; 1 only by rounding
-    turns[j] = frac >= 1.0 ? 0 : (uint64_t)(frac * 18446744073709551616.0);
+    const double f = inv_freq[j];
+    if (!isfinite(f)) return KV_ERR_INVALID_ARG;
+    const double hi = f / kTurn;
+    const double lo = (fma(-hi, kTurn, f) - hi * kTurnRest) / kTurn;
+    turns[j] = fraction(hi) + fraction(lo);
   }
   return KV_OK;
 }

@@ -2,6 +2,7 @@
 
 import ctypes
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -117,3 +118,17 @@ def test_turns_are_the_fraction_of_a_turn(lib):
     assert lib.kv_rope_turns(NULL, 1, out) == -1
     with pytest.raises(ValueError):
         binding.kv_rope_turns(torch.zeros(2, 2))
+
+
+@pytest.mark.parametrize("freq", [1.0, -1.0, 0.1, 2.0 ** -40, -1e-7, 3.0, 6.283185307179586,
+                                  -6.283185307179586, 1e4, 2.0 ** 30 - 1, 5e-324, 0.0]
+                         + [10000.0 ** (-2 * i / 128) for i in range(64)])
+def test_turns_are_right_to_the_last_places(lib, freq):
+    """Within four units of 2^-64: a position may multiply the error by 2^31. The quotient's two
+    parts are each cut once (two units), the second is off by a relative 2^-50 of at most 2^-53
+    of the angle (under one unit up to 2^27 turns), and the 2 pi used here by 10^-60."""
+    turn = 2 * Fraction(3141592653589793238462643383279502884197169399375105820974944, 10 ** 60)
+    got = binding.kv_rope_turns([freq]).item() % 2 ** 64
+    want = Fraction(freq) / turn % 1 * 2 ** 64
+    err = abs(got - want)
+    assert min(err, 2 ** 64 - err) <= 4
