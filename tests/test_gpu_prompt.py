@@ -295,6 +295,64 @@ def test_append_flags_bad_data_and_writes_nothing_there():
     assert_no_device_error()
 
 
+@pytest.mark.parametrize("dtype,D,G,PS,inter", [("bf16", 128, 4, 16, False),
+                                                ("bf16", 128, 1, 64, True),
+                                                ("bf16", 64, 8, 32, False),
+                                                ("fp32", 128, 2, 64, False),
+                                                ("fp32", 64, 1, 16, True)])
+def test_append_many_rows(dtype, D, G, PS, inter):
+    """From 8192 (token, KV head) pairs on, a warp takes several steps of its page."""
+    c = Case((2501, 0, 1, 1595), (37, 5, 63, 0), dtype, D, G, PS=PS)
+    c.q_in = c.q
+    stats = c.past_stats()
+    before = (c.k_pool.clone(), c.v_pool.clone(), None)
+    q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, skv.kv_rope_turns(freqs(D), device="cuda"),
+                           cu_tokens=c.cu, interleaved=inter)
+    assert_no_device_error()
+    check_append(c, q, stats, before, D, inter)
+    used = pages_of(c, c.lens)
+    assert torch.equal(stats[used], skv.kv_build_page_stats(c.kv)[used])
+
+
+def test_append_to_many_sequences():
+    """More sequences than one round of the search's loads, many without new tokens."""
+    c = Case(tuple(i * i % 4 for i in range(2500)), tuple(7 * i % 40 for i in range(2500)),
+             D=64, G=1)
+    c.q_in = c.q
+    stats = c.past_stats()
+    before = (c.k_pool.clone(), c.v_pool.clone(), None)
+    q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, skv.kv_rope_turns(freqs(64), device="cuda"),
+                           cu_tokens=c.cu)
+    assert_no_device_error()
+    check_append(c, q, stats, before, 64, False)
+    used = pages_of(c, c.lens)
+    assert torch.equal(stats[used], skv.kv_build_page_stats(c.kv)[used])
+
+
+def test_append_past_32_bit_offsets():
+    """Slots and statistics of the last pages of pools of more than 2^31 elements."""
+    NP = 2 ** 31 // (2 * 16 * 128) + 40
+    c = Case((20, 1), (5, 16), extra=0)
+    need = c.k_pool.shape[0]
+    small_k, small_v, table = c.k_pool, c.v_pool, c.table.clone()
+    c.k_pool = torch.empty((NP, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    c.v_pool = torch.empty_like(c.k_pool)
+    c.k_pool[-need:], c.v_pool[-need:] = small_k, small_v
+    c.table = torch.where(table >= 0, table + (NP - need), table).to(torch.int32)
+    c.kv = skv.PagedKV(c.k_pool, c.v_pool, c.table, c.seq_lens)
+    turns = skv.kv_rope_turns(freqs(128), device="cuda")
+    stats = torch.empty((NP, 2, 2, 128), dtype=torch.bfloat16, device="cuda")
+    skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=c.cu)
+    assert_no_device_error()
+    c.k_pool, c.v_pool, c.table = small_k.clone(), small_v.clone(), table
+    big = c.kv
+    c.kv = skv.PagedKV(c.k_pool, c.v_pool, table, c.seq_lens)
+    skv.kv_append_rope(c.kv, c.q, c.k, c.v, c.past_stats(), turns, cu_tokens=c.cu)
+    assert_no_device_error()
+    assert torch.equal(big.k_pool[-need:], c.k_pool)
+    assert torch.equal(big.v_pool[-need:], c.v_pool)
+
+
 @pytest.mark.parametrize("cu", [(48, 54, 60, 60, 60, 60), (60, 60, 60, 60, 60, 60),
                                 (0, 20, 40, 60, 10, 12), (0, 50, 55, 60, 0, 4)])
 def test_append_with_offsets_that_number_no_page(cu):
@@ -442,6 +500,31 @@ def test_prefill_attn_past_32_bit_offsets(dtype):
     seq, pos, phys, slot = c.slots()
     assert torch.equal(c.k_pool[phys, :, slot], c.k)
     c.check_attn(q, out, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shares", [0, 1, 3])
+def test_prefill_attn_of_a_batch_without_new_tokens(dtype, shares):
+    """A padded batch between two requests: rows there are, but no sequence owns one."""
+    c = Case((0, 0, 0), (0, 40, 500), dtype, tail=300)
+    out = torch.full(c.q.shape, -9.0, dtype=c.q.dtype, device="cuda")
+    lse = torch.full(c.q.shape[:2], -9.0, device="cuda")
+    for _ in range(3):
+        skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu, num_shares=shares, out=out,
+                            lse=lse)
+    assert_no_device_error()
+    assert (out == -9.0).all() and (lse == -9.0).all()
+
+
+@pytest.mark.parametrize("dtype,D,G", [("bf16", 128, 4), ("bf16", 64, 1), ("fp32", 64, 2)])
+def test_prefill_attn_of_sequences_that_share_pages(dtype, D, G):
+    """A common prefix mapped by several sequences, and a page mapped twice by one."""
+    c = Case((40, 3, 1, 200), (160, 317, 319, 120), dtype, D, G)
+    c.table[1:, :6] = c.table[0, :6]
+    c.table[3, 7] = c.table[3, 2]
+    out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu)
+    assert_no_device_error()
+    c.check_attn(c.q, out, lse)
 
 
 def test_prefill_attn_flags_bad_data():
