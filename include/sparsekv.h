@@ -239,13 +239,14 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
  * b, at position pos = seq_lens[b] - n_b + i, sees tokens 0 .. pos of its sequence:
  *   x_t = sm_scale * q . k_t,  lse = log sum_t exp(x_t),  out = sum_t exp(x_t - lse) v_t.
  * out: device [total_tokens][num_q_heads][head_dim] of the CACHE dtype (a prompt's rows feed
- * the next matrix product), 16-byte aligned; lse: device [total_tokens][num_q_heads] float32
- * (natural log) or NULL. Scores, softmax and sums are float32; for bf16 caches the
- * probabilities are rounded to bf16 before they meet the values. Rows that belong to no
- * sequence are left as they were; with cu_tokens = NULL the row of an empty sequence gets
- * out = 0 and lse = -inf. Cached tokens must be finite; what lies in a page past its
- * sequence's end has no influence. The same call gives the same bits (no atomics); where a
- * row's keys are cut, and so its last bits, depends on the whole batch unless num_shares = 1.
+ * the next matrix product), 16-byte aligned, overlapping no input; lse: device
+ * [total_tokens][num_q_heads] float32 (natural log) or NULL. Scores, softmax and sums are
+ * float32; for bf16 caches the probabilities are rounded to bf16 before they meet the values.
+ * Rows that belong to no sequence are left as they were; with cu_tokens = NULL the row of an
+ * empty sequence gets out = 0 and lse = -inf. Cached tokens must be finite; what lies in a page
+ * past its sequence's end has no influence. The same call gives the same bits (no atomics);
+ * where a row's keys are cut, and so its last bits, depends on the whole batch unless
+ * num_shares = 1.
  * num_shares: the work (row tiles by their keys, cut inside a row's keys where need be) is
  * divided evenly among this many blocks whatever the lengths; 0 takes as many as the GPU holds
  * at once, 1 .. 1024 asks for that many. workspace: device, 256-byte aligned,

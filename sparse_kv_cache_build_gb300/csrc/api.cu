@@ -368,8 +368,8 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
   if ((r = check_rows(cache, v_new, v_stride, cache->num_kv_heads)) != KV_OK) return r;
   if (!aligned16(stats) || (reinterpret_cast<uintptr_t>(turns) & 7u) != 0)
     return KV_ERR_MISALIGNED;
-  if (work_numbers(cu_tokens, total_tokens, cache->batch, cache->page_size, 2) *
-          cache->num_kv_heads > INT32_MAX)
+  if (cu_tokens != nullptr &&
+      page_numbers(total_tokens, cache->batch, cache->page_size) * cache->num_kv_heads > INT32_MAX)
     return KV_ERR_UNSUPPORTED;
   if (total_tokens == 0) return KV_OK;
   DevCtx ctx;

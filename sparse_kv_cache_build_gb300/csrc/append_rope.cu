@@ -159,7 +159,7 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
   const int PS = d.page_size, Hkv = d.num_kv_heads;
   const int g = blockIdx.x % Hkv, item = blockIdx.x / Hkv;
   int base;
-  const int b = find_sequence(pr, d.batch, PS, 2, item, &base);
+  const int b = find_sequence(pr, d.batch, PS, item, &base);
   const SeqRows sr = seq_rows(ctx, d, pr, b);
   const int start = sr.len - sr.n;
   // item < base only where the offsets fall or do not start at zero: that is nobody's number
@@ -339,8 +339,7 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const RopeArg
     return launch_pdl(append_rope_single_kernel<T, D, INTER>, grid, dim3(kRopeThreads), 0, s, d,
                       a, ctx);
   }
-  const dim3 grid(
-      (unsigned)(work_numbers(pr.cu, pr.total, d.batch, d.page_size, 2) * d.num_kv_heads));
+  const dim3 grid((unsigned)(page_numbers(pr.total, d.batch, d.page_size) * d.num_kv_heads));
   // With many rows a warp takes four steps of its page, so that finding the page is paid for by
   // more rows (pages of 16 at D = 128 are one warp's: 8192 tokens of 32/8 heads 43.7 us, against
   // 48.1 us with a warp per step). With few, a warp per step makes the call shorter (128 and 512

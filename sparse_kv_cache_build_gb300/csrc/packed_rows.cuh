@@ -51,26 +51,21 @@ __device__ __forceinline__ void check_packed_rows(const DevCtx& c, const kv_cach
   if (threadIdx.x == 0 && pr.cu[0] != 0) flag(c, KV_DEVERR_BAD_LEN);
 }
 
-// Work is numbered over the whole batch without knowing the lengths: sequence b owns the
-// numbers from base(b) = floor(cu[b] / unit) + spare * b up to base(b + 1). Cutting n rows
-// into pieces of `unit` takes at most floor(n / unit) + 1 pieces (spare = 1), or one more
-// when the cuts lie at multiples of `unit` of the positions (spare = 2), so each sequence's
-// range holds its pieces, and floor(total / unit) + spare * batch numbers hold them all.
+// Pages to append to are numbered over the whole batch without knowing the lengths: sequence b
+// owns the numbers from base(b) = floor(cu[b] / PS) + 2 b up to base(b + 1). n new tokens lie in
+// at most floor(n / PS) + 2 pages (the first and the last may be partial), so each sequence's
+// range holds its pages, and floor(total / PS) + 2 batch numbers hold them all.
 //
 // The sequence whose range holds `item`, found by one warp, 32 offsets at a time: one round of
 // loads for batches up to 32, two up to 1024. Sets *base to the range's first number.
-__device__ __forceinline__ int find_sequence(const PackedRows& pr, int batch, int unit,
-                                             int spare, int item, int* base) {
-  if (pr.cu == nullptr) {       // one row each: sequence b owns the number b
-    *base = item;
-    return item;
-  }
+__device__ __forceinline__ int find_sequence(const PackedRows& pr, int batch, int page_size,
+                                             int item, int* base) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = batch, at = 0;
   for (;;) {
     const int step = (hi - lo + 31) >> 5;
     const int b = lo + lane * step;
-    const int first = b < hi ? pr.cu[b] / unit + spare * b : INT32_MAX;
+    const int first = b < hi ? pr.cu[b] / page_size + 2 * b : INT32_MAX;
     int cnt = __popc(__ballot_sync(0xffffffffu, first <= item));
     cnt = cnt < 1 ? 1 : cnt;
     at = __shfl_sync(0xffffffffu, first, cnt - 1);
@@ -82,9 +77,8 @@ __device__ __forceinline__ int find_sequence(const PackedRows& pr, int batch, in
   return lo;
 }
 
-__host__ __device__ __forceinline__ long work_numbers(const int32_t* cu, int total, int batch,
-                                                      int unit, int spare) {
-  return cu == nullptr ? (long)batch : (long)(total / unit) + (long)spare * batch;
+inline long page_numbers(int total, int batch, int page_size) {
+  return (long)(total / page_size) + 2l * batch;
 }
 
 }  // namespace skv

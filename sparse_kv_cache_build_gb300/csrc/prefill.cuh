@@ -95,11 +95,11 @@ template <typename S> struct SeqItems {
 };
 
 // An item, or this block's part of it: rows of `n_tok` tokens from packed row `row0` on, of KV
-// head g; row r is token r / G and sees keys up to pos0 + r / G; key tiles [kt0, kt1) of nk.
+// head g; row r is token r / G and sees keys up to pos0 + r / G; key tiles [kt0, kt1).
 struct PrefillItem {
-  int b, g, tile;
+  int b, g;
   int row0, n_tok, pos0;
-  int nk, kt0, kt1;
+  int kt0, kt1;
   int part;             // workspace part, or -1: the block has the whole item
 };
 
@@ -164,8 +164,6 @@ template <typename S> class ItemWalk {
       if (it->kt0 >= it->kt1) continue;
       it->b = b_;
       it->g = g_;
-      it->tile = tile_;
-      it->nk = nk;
       const int t0 = tile_ << seq_.tq_log;
       it->row0 = seq_.row0 + t0;
       it->n_tok = seq_.tokens(tile_);

@@ -179,15 +179,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   memcpy(&o, &r, 8);
   return o;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t x, y, r;
-  memcpy(&x, &a, 8);
-  memcpy(&y, &b, 8);
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  float2 o;
-  memcpy(&o, &r, 8);
-  return o;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
