@@ -8,12 +8,12 @@
 //   O += P V     128 x D x 128,   P from TMEM, V from shared memory, O in TMEM
 // One warp issues the products, the two warpgroups' in turn:
 //   ... P0 V(j), Q0 K(j+1) | P1 V(j), Q1 K(j+1) | P0 V(j+1), Q0 K(j+2) | ...
-// so that one warpgroup's softmax runs under the other's products. A tile's round trip (scores,
-// softmax, P V) bounds the rate, not the products alone; P is handed over in two halves, so
-// that half of P V runs under the softmax of the other half. Measured and dropped: one S for
-// both warpgroups and P beside it, scores a tile ahead (the hand-over of S then bounds it).
-// One warp feeds K and V tiles through a ring by TMA, page by page (a page of one KV head is
-// PS dense rows of the pool).
+// so that one warpgroup's softmax runs under the other's products. P is handed over in two
+// halves, so that half of P V runs under the softmax of the other half. A second warp waits for
+// what the products need beside P (their K and V tiles, rows, O), so that the issuing warp waits
+// once per half. One warp feeds K and V tiles through a ring by TMA, page by page (a page of one
+// KV head is PS dense rows of the pool); one works out the items and loads their rows. Whole
+// rows of the output leave by TMA.
 //
 // An item with at most 128 rows (single tokens, drafts, a prompt's tail) gives both warpgroups
 // the same rows and alternating key tiles instead, and joins their (m, l, O) at the end: the
@@ -21,6 +21,22 @@
 //
 // A block walks its share of the batch's items (prefill.cuh) without stopping between them:
 // loads and products run ahead into the next item while a warpgroup writes its output.
+//
+// What bounds it. Long prompts: a tile's round trip. The two tiles of a key tile cost 2048
+// cycles of products at D = 128 and take 2700; a warpgroup's own chain (scores, about 1400
+// cycles of softmax, half of P V) is as long, so neither side waits for the other alone.
+// Measured, 64 query over 8 KV heads, D = 128: a prompt of 16384 tokens 2.81 ms, 1.56 PFLOP/s, 81%
+// of the measured library product's rate; 8192 tokens of 32/8 heads 0.42 ms, 67% (151 blocks
+// have less than three items each, whose starts and ends do not overlap everything). At D = 64
+// the products are half as long and the chain is not: 440 TFLOP/s over prompts of 1 to 4096
+// tokens of 16 heads without sharing. A single token over 32768: 38 us, of which the keys and values stream in 18 at the
+// measured copy rate; the start of the blocks (8), their last output (4) and the merge (5)
+// remain.
+//
+// Measured and dropped, at 16384 tokens unless said: one S for both warpgroups and P beside it,
+// scores a tile ahead (the hand-over of S bounds it); two threads per row, 640 threads (3.5 ms);
+// the maximum beside the first half's exponentials (3.07 ms); polling without suspension in the
+// issuing warp (8192 tokens 0.60 ms against 0.42).
 //
 // The running maximum is lazy: O and l are rescaled only when a row's maximum grows by more
 // than 2^8, so that almost no tile pays for it; P stays below 2^8 and every sum is float32.
@@ -366,7 +382,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         }
         // Through 4 KB of the warp's own shared memory, 128 bytes of each of its 32 rows at a
         // time, so that eight lanes write one row's 128 bytes: a lane per row would touch 32
-        // lines with every store (6000 cycles an item against 1500).
+        // lines with every store (6000 cycles an item; this way 1500).
         uint8_t* stage = sm + C::OFF_OUT + warp * 4096;
         auto columns = [&](int c, float* o) {      // 32 columns from c on, scaled and joined
           uint32_t raw[32];

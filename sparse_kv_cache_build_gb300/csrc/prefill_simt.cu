@@ -10,8 +10,14 @@
 // partial sums, joined at the end), the output pairs neighbouring columns. Rows are padded by
 // four floats so that the sixteen keys of a warp's read fall into different banks. The
 // probabilities take the place of the key tile just used; the next tiles arrive by asynchronous
-// copies meanwhile. Tensor cores would need six bf16 products (or three tf32 ones, and twice the
-// shared memory there is at D = 128) for each float32 product to keep its precision.
+// copies meanwhile.
+//
+// Measured: 4096 tokens of 8 query over 2 KV heads, D = 64: 497 us, 34.6 TFLOP/s (the causal
+// multiply-adds alone would take 230 at one per lane and clock). Reads of shared memory keep
+// their pipe 70% busy and the multiply-adds theirs 55%; 512 threads with 8 x 2 scores each, for
+// more warps to hide the one under the other, took 515. Tensor cores would need six bf16
+// products (or three tf32 ones, and twice the shared memory there is at D = 128) for each
+// float32 product to keep its precision.
 #include "prefill.cuh"
 #include "tcgen05.cuh"
 
