@@ -29,9 +29,9 @@
 // of the measured library product's rate; 8192 tokens of 32/8 heads 0.42 ms, 67% (151 blocks
 // have less than three items each, whose starts and ends do not overlap everything). At D = 64
 // the products are half as long and the chain is not: 440 TFLOP/s over prompts of 1 to 4096
-// tokens of 16 heads without sharing. A single token over 32768: 38 us, of which the keys and values stream in 18 at the
-// measured copy rate; the start of the blocks (8), their last output (4) and the merge (5)
-// remain.
+// tokens of 16 heads without sharing. A single token over 32768: 38 us, of which the keys and
+// values stream in 18 at the measured copy rate; the start of the blocks (8), their last output
+// (4) and the merge (5) remain.
 //
 // Measured and dropped, at 16384 tokens unless said: one S for both warpgroups and P beside it,
 // scores a tile ahead (the hand-over of S bounds it); two threads per row, 640 threads (3.5 ms);
