@@ -35,7 +35,9 @@
 //
 // Measured and dropped, at 16384 tokens unless said: one S for both warpgroups and P beside it,
 // scores a tile ahead (the hand-over of S bounds it); two threads per row, 640 threads (3.5 ms);
-// the maximum beside the first half's exponentials (3.07 ms); polling without suspension in the
+// the maximum beside the first half's exponentials (3.07 ms); P handed over at 96 of 128 keys,
+// or at 64 with the wait for its store put off by 16 or 32 keys (2.69 to 2.71 ms against 2.70,
+// D = 64 slower by up to 4%); polling without suspension in the
 // issuing warp (8192 tokens 0.60 ms against 0.42); at D = 64 P beside each warpgroup's own S and
 // scores a tile ahead (the four prompts above 145 us against 109: with one more hand-over per
 // tile the issuing warp, 1600 cycles a tile among the softmax's instructions, is the bound).
@@ -317,27 +319,34 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           const float ref = m == -INFINITY ? 0.f : m;             // no key of this row yet
           ref2 = make_float2(-ref, -ref);
         }
+        uint32_t p[64];
+        auto exps = [&](int first, int last) {                    // P of keys [first, last)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!idle) {
-            uint32_t p[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float2 x = make_float2(__uint_as_float(s[64 * h + 2 * e]),
-                                     __uint_as_float(s[64 * h + 2 * e + 1]));
-              x = tc::fma2(x, scale2, ref2);
-              x.x = tc::exp2_approx(x.x);
-              x.y = tc::exp2_approx(x.y);
-              sum[e & 1] = tc::add2(sum[e & 1], x);
-              p[e] = tc::pack_bf16(x.x, x.y);
-            }
-            tc::st32(ts + 32 * h, p);
-            tc::wait_st();
+          for (int e = first / 2; e < last / 2; ++e) {
+            float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+            x = tc::fma2(x, scale2, ref2);
+            x.x = tc::exp2_approx(x.x);
+            x.y = tc::exp2_approx(x.y);
+            sum[e & 1] = tc::add2(sum[e & 1], x);
+            p[e] = tc::pack_bf16(x.x, x.y);
           }
+        };
+        auto hand_over = [&](uint64_t* to_whom) {
+          if (!idle) tc::wait_st();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) arrive((h == 0 ? p_half : p_full) + w);
+          if (lane == 0) arrive(to_whom + w);
+        };
+        if (!idle) {
+          exps(0, 64);
+          tc::st32(ts, p);
         }
+        hand_over(p_half);
+        if (!idle) {
+          exps(64, 128);
+          tc::st32(ts + 32, p + 32);
+        }
+        hand_over(p_full);
         sum[0] = tc::add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
       }
