@@ -124,6 +124,17 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// mbar_wait_bounded in fewer instructions: this kernel has thirty waits.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
+                                             unsigned long long limit_ns) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    const uint64_t t = global_timer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > limit_ns) return false;
+  }
+  return true;
+}
 // 64 columns of a tile's rows: G heads of 128 / G tokens of the query tensor [T][Hq][D].
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head,
                                          int token, uint64_t* bar) {
@@ -226,7 +237,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   const uint32_t tmem = uniform(*tmem_slot);
   // Item number j of the block, for the warp that asks; the last one has no key tiles.
   auto item_ready = [&](int j) {
-    return mbar_wait_bounded(item_full + j % kItems, (j / kItems) & 1, ctx.wait_ns);
+    return wait_bounded(item_full + j % kItems, (j / kItems) & 1, ctx.wait_ns);
   };
   auto item_done = [&](int j) {
     __syncwarp();
@@ -264,7 +275,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       }
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n; ++i) {
-        ok = mbar_wait_bounded(s_full + w, tiles_seen & 1, ctx.wait_ns);
+        ok = wait_bounded(s_full + w, tiles_seen & 1, ctx.wait_ns);
         if (!ok) break;
         ++tiles_seen;
         tc::fence_after();
@@ -279,10 +290,13 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           if (warp_seen < kKeys - 1) {                            // on the border
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              if (warp_seen < 32 * q + 31)
+              if (warp_seen < 32 * q + 31) {
+                const int last = seen - 32 * q;
+                const uint32_t keep = last >= 31 ? ~0u : last < 0 ? 0u : (2u << last) - 1u;
 #pragma unroll
-                for (int c = 32 * q; c < 32 * q + 32; ++c)
-                  if (c > seen) s[c] = 0xff800000u;
+                for (int c = 0; c < 32; ++c)
+                  if ((keep >> c & 1u) == 0u) s[32 * q + c] = 0xff800000u;
+              }
           }
           seen -= step;
           warp_seen -= step;
@@ -356,7 +370,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       const Plan plan(it, log_g);
       const int rows = it.n_tok << log_g, warp_row = row - lane;
       const bool join = !plan.wide && plan.n1 > 0;
-      if (n > 0) ok = mbar_wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
+      if (n > 0) ok = wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
       if (!ok) break;
       if (join && w == 1) {
         box[r] = m;
@@ -367,7 +381,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (n > 0) ++items_seen;
       if (join && w == 0) {
         // the other warpgroup's last product: it has one for each of this one's joins
-        ok = mbar_wait_bounded(joined, joins_seen & 1, ctx.wait_ns);
+        ok = wait_bounded(joined, joins_seen & 1, ctx.wait_ns);
         if (!ok) break;
         ++joins_seen;
       }
@@ -430,47 +444,42 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           }
           __syncwarp();
         };
-        if (n > 0 && whole) {
-          uint8_t* out = reinterpret_cast<uint8_t*>(
-              static_cast<uint16_t*>(a.out) + ((int64_t)it.row0 * a.Hq + it.g * a.G) * D);
-#pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            __syncwarp();                          // the copy before has read the buffer
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float o[32];
-              columns(c + 32 * h, o);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                put(4 * h + e, tc::pack_bf16(o[8 * e], o[8 * e + 1]),
-                    tc::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                    tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
-                    tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-            }
-            if (by_tma) {
-              tc::fence_async_smem();
-              __syncwarp();
-              if (lane == 0)
-                tma_store_rows(&map_out, stage, c, it.g * a.G, it.row0 + (warp_row >> log_g));
-            } else {
-              flush(out + c * 2, D * 2, true);
-            }
-          }
-        } else if (n > 0) {
-          uint8_t* out = reinterpret_cast<uint8_t*>(a.part_acc +
-                                                    (int64_t)it.part * a.part_rows * D);
+        if (n > 0) {
+          uint8_t* out = whole ? reinterpret_cast<uint8_t*>(
+              static_cast<uint16_t*>(a.out) + ((int64_t)it.row0 * a.Hq + it.g * a.G) * D)
+                               : reinterpret_cast<uint8_t*>(
+              a.part_acc + (int64_t)it.part * a.part_rows * D);
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
+          __syncwarp();                            // the copy before has read the buffer
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
             columns(c, o);
+            if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              put(e, __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                  __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
-            flush(out + c * 4, D * 4, false);
+              for (int e = 0; e < 8; ++e)
+                put(e, __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                    __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                put((c >> 3 & 4) + e, tc::pack_bf16(o[8 * e], o[8 * e + 1]),
+                    tc::pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                    tc::pack_bf16(o[8 * e + 4], o[8 * e + 5]),
+                    tc::pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+              if ((c & 32) == 0) continue;         // 128 bytes of a row are 64 columns
+            }
+            if (!by_tma) {
+              flush(whole ? out + (c - 32) * 2 : out + c * 4, whole ? D * 2 : D * 4, whole);
+              continue;
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_rows(&map_out, stage, c - 32, it.g * a.G, it.row0 + (warp_row >> log_g));
+              if (c + 32 < D) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            __syncwarp();
           }
         }
         if (mine && whole && a.lse != nullptr) a.lse[at_row] = (m + log2f(l)) * kLn2;
@@ -491,37 +500,32 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
   } else {
     tc::fewer_regs<kRegsOther>();
-    if (warp == kMmaWarp || warp == kReadyWarp) {
-      // ---- products, and what they need beside P. The time between two batches of products is
-      // lost to the tensor core, so the warp that issues them waits for as little as it can: a
-      // second warp walks the same batches a little ahead, waits for their V and K tiles, rows
-      // and O, and adds its arrival to the softmax warps' at p_half and p_full.
-      const bool issues = warp == kMmaWarp;
+    auto uniform_plan = [&](int j) {
+      Plan plan(items[j % kItems], log_g);
+      plan.wide = uniform(plan.wide);
+      plan.n = uniform(plan.n);
+      plan.n0 = uniform(plan.n0);
+      plan.n1 = uniform(plan.n1);
+      return plan;
+    };
+    // The next item's first scores can be issued with the last of this one's products.
+    auto runs_on = [](const Plan& plan, const Plan& next) {
+      return plan.wide && plan.n0 == plan.n1 && next.wide && next.n0 > 0;
+    };
+    if (warp == kMmaWarp) {
+      // ---- products. The time between two batches of them is lost to the tensor core, so this
+      // warp waits for as little as it can: for P, whose barriers the ready warp joins.
       bool ok = true;
       int base = 0;                                  // ring slots of the items before
       int items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0;           // for the barriers' phases
+      // The first try stands alone: inside the loop of the slow path it costs 4% of a long prompt.
       auto wait = [&](uint64_t* x, int parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(x, parity))) return;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(x, parity, ctx.wait_ns)) && ok;
-      };
-      auto wait_slot = [&](int slot) {
-        wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
-      };
-      auto say = [&](uint64_t* x) {
-        __syncwarp();
-        if (lane == 0) arrive(x);
+        ok = __all_sync(0xffffffffu, wait_bounded(x, parity, ctx.wait_ns)) && ok;
       };
       const uint64_t q_desc = tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q)), 16);
       const uint64_t k_desc = tc::smem_desc(uniform(smem_addr(ring)), 16);
       const uint64_t v_desc = tc::smem_desc(uniform(smem_addr(ring)), 16384);
-      auto uniform_plan = [&](int j) {
-        Plan plan(items[j % kItems], log_g);
-        plan.wide = uniform(plan.wide);
-        plan.n = uniform(plan.n);
-        plan.n0 = uniform(plan.n0);
-        plan.n1 = uniform(plan.n1);
-        return plan;
-      };
       // Scores of warpgroup w's tile in ring slot `slot`; `done`: w is its last reader; `last`:
       // of the item.
       auto scores = [&](int w, int slot, bool done, bool last) {
@@ -541,15 +545,16 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       bool early = false;          // this item's first scores were issued with the last's end
       ok = __all_sync(0xffffffffu, item_ready(0));
       Plan plan = uniform_plan(0), next = plan;
+#pragma unroll 1
       for (int j = 0; ok && plan.n > 0; ++j) {
         const int most = max(plan.n0, plan.n1);
-        if (!early && issues) {
-#pragma unroll
+        if (!early) {
+#pragma unroll 1
           for (int w = 0; w < 2; ++w) {
             if (!ok || plan.tiles(w) == 0) continue;
             const int slot = base + plan.k_slot(plan.tile(w, 0));
             wait(q_full + w, (w == 0 ? items0 : items1) & 1);
-            wait_slot(slot);
+            wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
             if (!ok) continue;
             tc::fence_after();
             if (tc::elect()) scores(w, slot, !plan.wide || w == 1, plan.tiles(w) == 1);
@@ -557,36 +562,22 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           }
         }
         early = false;
+#pragma unroll 1
         for (int i = 0; ok && i < most; ++i) {
           if (i == most - 1) {                         // what follows
             ok = __all_sync(0xffffffffu, item_ready(j + 1));
             if (!ok) break;
             next = uniform_plan(j + 1);
-            early = plan.wide && plan.n0 == plan.n1 && next.wide && next.n0 > 0;
+            early = runs_on(plan, next);
           }
+          // written out for both warpgroups: as a loop it costs a long prompt 4%
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || i >= plan.tiles(w)) continue;
             const int slot = base + plan.v_slot(plan.tile(w, i));
-            const int tiles = w == 0 ? tiles0++ : tiles1++, before = w == 0 ? items0 : items1;
+            const int tiles = w == 0 ? tiles0++ : tiles1++;
             const bool more = i + 1 < plan.tiles(w), go_on = more || early;
             const int k_slot = more ? base + plan.k_slot(plan.tile(w, i + 1)) : base + 2 * plan.n;
-            if (!issues) {
-              // The tile's scores are there: so is every tile before, whose barriers' phases
-              // (of two kinds) could otherwise be taken for those waited for here.
-              wait(s_full + w, tiles & 1);
-              wait_slot(slot);
-              if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);   // it has been read
-              if (!ok) continue;
-              say(p_half + w);
-              if (go_on) {
-                if (!more) wait(q_full + w, (before + 1) & 1);
-                wait_slot(k_slot);
-                if (!ok) continue;
-              }
-              say(p_full + w);
-              continue;
-            }
             const bool done = !plan.wide || w == 1;
             const bool last = more ? i + 2 == plan.tiles(w) : next.tiles(w) == 1;
             constexpr uint32_t id = tc::idesc(D, true);
@@ -624,10 +615,68 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok) {
         if (tc::elect()) {
           flag(ctx, KV_DEVERR_TIMEOUT);
-          if (issues) tc::commit(drained);
+          tc::commit(drained);
         }
-        if (issues) (void)mbar_wait_bounded(drained, 0, ctx.wait_ns);
+        (void)wait_bounded(drained, 0, ctx.wait_ns);
       }
+    } else if (warp == kReadyWarp) {
+      // ---- what the products need beside P: this warp walks the same batches a little ahead,
+      // waits for their V and K tiles, rows and O, and adds its arrival to the softmax warps'
+      // at p_half and p_full.
+      bool ok = true;
+      int base = 0, items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0;
+      auto wait = [&](uint64_t* x, int parity) {
+        ok = __all_sync(0xffffffffu, wait_bounded(x, parity, ctx.wait_ns)) && ok;
+      };
+      auto wait_slot = [&](int slot) {
+        wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
+      };
+      auto say = [&](uint64_t* x) {
+        __syncwarp();
+        if (lane == 0) arrive(x);
+      };
+      ok = __all_sync(0xffffffffu, item_ready(0));
+      Plan plan = uniform_plan(0), next = plan;
+#pragma unroll 1
+      for (int j = 0; ok && plan.n > 0; ++j) {
+        const int most = max(plan.n0, plan.n1);
+        bool early = false;
+#pragma unroll 1
+        for (int i = 0; ok && i < most; ++i) {
+          if (i == most - 1) {
+            ok = __all_sync(0xffffffffu, item_ready(j + 1));
+            if (!ok) break;
+            next = uniform_plan(j + 1);
+            early = runs_on(plan, next);
+          }
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || i >= plan.tiles(w)) continue;
+            const int tiles = w == 0 ? tiles0++ : tiles1++, before = w == 0 ? items0 : items1;
+            const bool more = i + 1 < plan.tiles(w);
+            // The tile's scores are there: so is every tile before, whose barriers' phases (of
+            // two kinds) could otherwise be taken for those waited for here.
+            wait(s_full + w, tiles & 1);
+            wait_slot(base + plan.v_slot(plan.tile(w, i)));
+            if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);     // it has been read
+            if (!ok) continue;
+            say(p_half + w);
+            if (more || early) {
+              if (!more) wait(q_full + w, (before + 1) & 1);
+              wait_slot(more ? base + plan.k_slot(plan.tile(w, i + 1)) : base + 2 * plan.n);
+              if (!ok) continue;
+            }
+            say(p_full + w);
+          }
+        }
+        item_done(j);
+        items0 += plan.n0 > 0;
+        items1 += plan.n1 > 0;
+        base += 2 * plan.n;
+        plan = next;
+      }
+      __syncwarp();
+      if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
     } else if (warp == kLoadWarp) {
       // ---- loads: one page half (64 columns) per lane
       const int PS = d.page_size, per_tile = kKeys / PS;
@@ -636,7 +685,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       const uint32_t box_bytes = (uint32_t)PS * 128;
       const uint32_t dst = smem_addr(ring) + half * 16384 + page * box_bytes;
       bool ok = true;
-      int base = 0, used = 0, tails = 0;
+      int used = 0, tails = 0;                         // slots filled
       for (int j = 0;; ++j) {
         ok = __all_sync(0xffffffffu, ok && item_ready(j));
         if (!ok) break;
@@ -663,7 +712,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         };
         int chunk = it.kt0 * per_tile / 32;
         int e0 = -1, e1 = entries(chunk), e2 = entries(chunk + 1);
-        auto load = [&](const CUtensorMap* map, int t, bool values) {
+        auto load = [&](bool values, int t) {
           if (!ok) return;
           const int first = (it.kt0 + t) * per_tile;
           if (first / 32 > chunk) {
@@ -673,10 +722,10 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           }
           int P = __shfl_sync(0xffffffffu, first / 32 == chunk ? e1 : e0, (first + page) & 31);
           if (lane >= copies) P = -1;
-          const int slot = base + (values ? plan.v_slot(t) : plan.k_slot(t));
+          const int slot = used;
           const int stage = slot % C::STAGES;
           if (slot >= C::STAGES)
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(
+            ok = __all_sync(0xffffffffu, wait_bounded(
                 empty + stage, (slot / C::STAGES - 1) & 1, ctx.wait_ns));
           if (!ok) return;
           // the item's last key lies inside this tile: the V rows after it become zeros
@@ -687,11 +736,11 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           if (lane == 0) mbar_arrive_expect_tx(land, boxes * box_bytes);
           __syncwarp();
           if (P >= 0)
-            tma_page(dst + stage * C::TILE_BYTES, map, half * 64,
+            tma_page(dst + stage * C::TILE_BYTES, values ? &map_v : &map_k, half * 64,
                      (P * d.num_kv_heads + it.g) * PS, land);
-          used = slot + 1;
+          ++used;
           if (!tail) return;
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(v_land, tails & 1, ctx.wait_ns));
+          ok = __all_sync(0xffffffffu, wait_bounded(v_land, tails & 1, ctx.wait_ns));
           ++tails;
           uint8_t* tile = ring + stage * C::TILE_BYTES;
           for (int i = valid * 8 + lane; i < kKeys * 8; i += 32)
@@ -703,23 +752,23 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           if (lane == 0) arrive(full + stage);
         };
         if (plan.wide) {
+#pragma unroll 1
           for (int t = 0; t < plan.n; ++t) {
-            load(&map_k, t, false);
-            load(&map_v, t, true);
+            load(false, t);
+            load(true, t);
           }
         } else {
-          for (int t = 0; t < min(2, plan.n); ++t) load(&map_k, t, false);
-          for (int t = 0; t < plan.n; ++t) {
-            load(&map_v, t, true);
-            if (t + 2 < plan.n) load(&map_k, t + 2, false);
+#pragma unroll 1
+          for (int t = -2; t < plan.n; ++t) {
+            if (t >= 0) load(true, t);
+            if (t + 2 < plan.n) load(false, t + 2);
           }
         }
-        base += 2 * plan.n;
       }
       if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
       // no copy may be in flight when the block's shared memory goes
       for (int slot = max(0, used - C::STAGES); slot < used; ++slot)
-        (void)mbar_wait_bounded(full + slot % C::STAGES, (slot / C::STAGES) & 1, ctx.wait_ns);
+        (void)wait_bounded(full + slot % C::STAGES, (slot / C::STAGES) & 1, ctx.wait_ns);
     } else if (warp == kItemWarp) {
       // ---- the block's items, one ahead of their rows, and after the last an item without key
       // tiles; a warpgroup's rows are loaded as soon as the item before is done with them
@@ -727,28 +776,29 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (lane == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
       bool ok = true;
       int loaded[2] = {0, 0};
-      PrefillItem it, next;
+      PrefillItem it, next{};
       auto publish = [&](int j) {
         if (!walk.next(&next)) next.kt0 = next.kt1 = 0;
         if (j >= kItems)
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(item_free + j % kItems,
-                                                         (j / kItems - 1) & 1, ctx.wait_ns));
+          ok = __all_sync(0xffffffffu, wait_bounded(item_free + j % kItems,
+                                                    (j / kItems - 1) & 1, ctx.wait_ns));
         if (ok && lane == 0) {
           items[j % kItems] = next;
           arrive(item_full + j % kItems);
         }
       };
-      publish(0);
-      for (int j = 0; ok && next.kt0 < next.kt1; ++j) {
+#pragma unroll 1
+      for (int j = -1;; ++j) {
         it = next;
         publish(j + 1);
+        if (!ok) break;
         const Plan plan(it, log_g);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || plan.tiles(w) == 0) continue;
           if (loaded[w] > 0)
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_free + w, (loaded[w] - 1) & 1,
-                                                           ctx.wait_ns));
+            ok = __all_sync(0xffffffffu, wait_bounded(q_free + w, (loaded[w] - 1) & 1,
+                                                      ctx.wait_ns));
           if (!ok) continue;
           if (lane == 0) {
             mbar_arrive_expect_tx(q_full + w, C::TILE_BYTES);
@@ -760,11 +810,12 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           __syncwarp();
           ++loaded[w];
         }
+        if (next.kt0 >= next.kt1) break;
       }
       if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        if (loaded[w] > 0) (void)mbar_wait_bounded(q_full + w, (loaded[w] - 1) & 1, ctx.wait_ns);
+        if (loaded[w] > 0) (void)wait_bounded(q_full + w, (loaded[w] - 1) & 1, ctx.wait_ns);
     }
     __syncwarp();
   }
