@@ -23,24 +23,32 @@
 // loads and products run ahead into the next item while a warpgroup writes its output.
 //
 // What bounds it. Long prompts: a tile's round trip. The two tiles of a key tile cost 2048
-// cycles of products at D = 128 and take 2700; a warpgroup's own chain (scores, about 1400
-// cycles of softmax, half of P V) is as long, so neither side waits for the other alone.
-// Measured, 64 query over 8 KV heads, D = 128: a prompt of 16384 tokens 2.81 ms, 1.56 PFLOP/s, 81%
-// of the measured library product's rate; 8192 tokens of 32/8 heads 0.42 ms, 67% (151 blocks
-// have less than three items each, whose starts and ends do not overlap everything). At D = 64
-// the products are half as long and the chain is not: 440 TFLOP/s over prompts of 1 to 4096
-// tokens of 16 heads without sharing. A single token over 32768: 38 us, of which the keys and
-// values stream in 18 at the measured copy rate; the start of the blocks (8), their last output
-// (4) and the merge (5) remain.
+// cycles of products at D = 128 and take about 2600; a warpgroup's own chain (scores, about 1400
+// cycles of softmax, half of P V) is as long, so neither side waits for the other alone. With
+// pages of 16 tokens a K or V tile is sixteen copies of 2 KB, whose issue then bounds the rate:
+// a prompt of 8192 tokens of 32/8 heads takes 0.41 ms with pages of 16, 0.33 with 32, 0.35 with
+// 64. Short items: instruction fetches, as what lies between items is long code that few warps
+// run (32 prompts of 400 tokens: a stall of 4.2 per instruction issued, 0.2 on a long prompt);
+// hence the rolled loops there, which took them from 127 us to 111.
+// Measured, D = 128: a prompt of 16384 tokens, 64/8 heads, pages of 64: 2.69 ms, 1.64 PFLOP/s,
+// 84% of the measured library product's rate; 8192 tokens, 32/8 heads, pages of 16: 0.42 ms,
+// 67%. At D = 64 the products are half as long and the chain is not: 465 TFLOP/s over prompts of
+// 1 to 4096 tokens of 16 heads without sharing. A single token over 32768: 37 us, of which the
+// keys and values stream in 18 at the measured copy rate; the start of the blocks (8), their
+// last output (4) and the merge (5) remain.
 //
 // Measured and dropped, at 16384 tokens unless said: one S for both warpgroups and P beside it,
 // scores a tile ahead (the hand-over of S bounds it); two threads per row, 640 threads (3.5 ms);
 // the maximum beside the first half's exponentials (3.07 ms); P handed over at 96 of 128 keys,
 // or at 64 with the wait for its store put off by 16 or 32 keys (2.69 to 2.71 ms against 2.70,
-// D = 64 slower by up to 4%); polling without suspension in the
-// issuing warp (8192 tokens 0.60 ms against 0.42); at D = 64 P beside each warpgroup's own S and
-// scores a tile ahead (the four prompts above 145 us against 109: with one more hand-over per
-// tile the issuing warp, 1600 cycles a tile among the softmax's instructions, is the bound).
+// D = 64 slower by up to 4%); polling without suspension in the issuing warp (8192 tokens 0.60
+// ms against 0.42); at D = 64 P beside each warpgroup's own S and scores a tile ahead (145 us
+// against 109: with one more hand-over per tile the issuing warp, 1600 cycles a tile among the
+// softmax's instructions, is the bound); the copies of a tile's pages issued by one thread, page
+// after page (0.55 ms for 8192 tokens) or written out (0.38 against 0.41, but pages of 32 and 64
+// and ragged batches 10 to 18% slower); both products' warpgroups in one loop (short items 9%
+// faster, long prompts 4% slower); V tiles zeroed behind the sequence's end only (8192 tokens 1%
+// slower).
 //
 // The running maximum is lazy: O and l are rescaled only when a row's maximum grows by more
 // than 2^8, so that almost no tile pays for it; P stays below 2^8 and every sum is float32.
