@@ -12,7 +12,7 @@
 // probabilities take the place of the key tile just used; the next tiles arrive by asynchronous
 // copies meanwhile.
 //
-// Measured: 4096 tokens of 8 query over 2 KV heads, D = 64: 497 us, 34.6 TFLOP/s (the causal
+// Measured: 4096 tokens of 8 query over 2 KV heads, D = 64: 491 us, 35 TFLOP/s (the causal
 // multiply-adds alone would take 230 at one per lane and clock). Reads of shared memory keep
 // their pipe 70% busy and the multiply-adds theirs 55%; 512 threads with 8 x 2 scores each, for
 // more warps to hide the one under the other, took 515. Tensor cores would need six bf16
