@@ -132,17 +132,27 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// mbar_wait_bounded in fewer instructions: this kernel has thirty waits.
+// A whole warp's bounded wait, with one answer for all its lanes: each lane reads the timer for
+// itself, and where some gave up while others went on, the rest of the warp's code (TMEM loads,
+// votes) would run without them. mbar_wait_bounded in fewer instructions: this kernel has thirty
+// waits.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
                                              unsigned long long limit_ns) {
+  bool ok = true;
   uint64_t t0 = 0;
   while (!mbar_try_wait(bar, parity)) {
     const uint64_t t = global_timer_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > limit_ns) return false;
+    if (t - t0 > limit_ns) {
+      ok = false;
+      break;
+    }
   }
-  return true;
+  return __all_sync(0xffffffffu, ok);
 }
+// Products and copies in flight end by themselves, within microseconds; the block must outlive
+// them whatever limit the caller set for its waits.
+constexpr unsigned long long kDrainNs = 4000000000ull;
 // 64 columns of a tile's rows: G heads of 128 / G tokens of the query tensor [T][Hq][D].
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head,
                                          int token, uint64_t* bar) {
@@ -194,7 +204,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* o_free = q_free + 2;                 // [2] its O has been read
   uint64_t* joined = o_free + 2;                 // the second warpgroup's (m, l) are written
   uint64_t* v_land = joined + 1;                 // the last V tile, before its tail is zeroed
-  uint64_t* drained = v_land + 1;                // after a timeout: no product in flight
+  uint64_t* drained = v_land + 1;                // no product in flight
   uint64_t* item_full = drained + 1;             // [kItems] an item is in shared memory
   uint64_t* item_free = item_full + kItems;      // [kItems] every warp is done with it
   PrefillItem* items = reinterpret_cast<PrefillItem*>(sm + C::OFF_ITEMS);
@@ -529,7 +539,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       // The first try stands alone: inside the loop of the slow path it costs 4% of a long prompt.
       auto wait = [&](uint64_t* x, int parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(x, parity))) return;
-        ok = __all_sync(0xffffffffu, wait_bounded(x, parity, ctx.wait_ns)) && ok;
+        ok = wait_bounded(x, parity, ctx.wait_ns) && ok;
       };
       const uint64_t q_desc = tc::smem_desc(uniform(smem_addr(sm + C::OFF_Q)), 16);
       const uint64_t k_desc = tc::smem_desc(uniform(smem_addr(ring)), 16);
@@ -551,8 +561,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         if (done) tc::commit(empty + stage);
       };
       bool early = false;          // this item's first scores were issued with the last's end
-      ok = __all_sync(0xffffffffu, item_ready(0));
+      ok = item_ready(0);
       Plan plan = uniform_plan(0), next = plan;
+      const bool any = ok && plan.n > 0;
 #pragma unroll 1
       for (int j = 0; ok && plan.n > 0; ++j) {
         const int most = max(plan.n0, plan.n1);
@@ -573,7 +584,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll 1
         for (int i = 0; ok && i < most; ++i) {
           if (i == most - 1) {                         // what follows
-            ok = __all_sync(0xffffffffu, item_ready(j + 1));
+            ok = item_ready(j + 1);
             if (!ok) break;
             next = uniform_plan(j + 1);
             early = runs_on(plan, next);
@@ -619,14 +630,15 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         base += 2 * plan.n;
         plan = next;
       }
+      // No product may be in flight when the TMEM goes: this warp may have ended well while a
+      // softmax warp, which waits for the last ones, gave up.
       __syncwarp();
-      if (!ok) {
-        if (tc::elect()) {
-          flag(ctx, KV_DEVERR_TIMEOUT);
-          tc::commit(drained);
-        }
-        (void)wait_bounded(drained, 0, ctx.wait_ns);
+      if (any) {
+        if (tc::elect()) tc::commit(drained);
+        __syncwarp();
+        (void)wait_bounded(drained, 0, kDrainNs);
       }
+      if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
     } else if (warp == kReadyWarp) {
       // ---- what the products need beside P: this warp walks the same batches a little ahead,
       // waits for their V and K tiles, rows and O, and adds its arrival to the softmax warps'
@@ -634,7 +646,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       bool ok = true;
       int base = 0, items0 = 0, items1 = 0, tiles0 = 0, tiles1 = 0;
       auto wait = [&](uint64_t* x, int parity) {
-        ok = __all_sync(0xffffffffu, wait_bounded(x, parity, ctx.wait_ns)) && ok;
+        ok = wait_bounded(x, parity, ctx.wait_ns) && ok;
       };
       auto wait_slot = [&](int slot) {
         wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
@@ -643,7 +655,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         __syncwarp();
         if (lane == 0) arrive(x);
       };
-      ok = __all_sync(0xffffffffu, item_ready(0));
+      ok = item_ready(0);
       Plan plan = uniform_plan(0), next = plan;
 #pragma unroll 1
       for (int j = 0; ok && plan.n > 0; ++j) {
@@ -652,7 +664,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll 1
         for (int i = 0; ok && i < most; ++i) {
           if (i == most - 1) {
-            ok = __all_sync(0xffffffffu, item_ready(j + 1));
+            ok = item_ready(j + 1);
             if (!ok) break;
             next = uniform_plan(j + 1);
             early = runs_on(plan, next);
@@ -695,7 +707,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       bool ok = true;
       int used = 0, tails = 0;                         // slots filled
       for (int j = 0;; ++j) {
-        ok = __all_sync(0xffffffffu, ok && item_ready(j));
+        ok = ok && item_ready(j);
         if (!ok) break;
         const PrefillItem it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
@@ -733,8 +745,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           const int slot = used;
           const int stage = slot % C::STAGES;
           if (slot >= C::STAGES)
-            ok = __all_sync(0xffffffffu, wait_bounded(
-                empty + stage, (slot / C::STAGES - 1) & 1, ctx.wait_ns));
+            ok = wait_bounded(empty + stage, (slot / C::STAGES - 1) & 1, ctx.wait_ns);
           if (!ok) return;
           // the item's last key lies inside this tile: the V rows after it become zeros
           const int valid = min(kKeys, keys - (it.kt0 + t) * kKeys);
@@ -748,7 +759,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                      (P * d.num_kv_heads + it.g) * PS, land);
           ++used;
           if (!tail) return;
-          ok = __all_sync(0xffffffffu, wait_bounded(v_land, tails & 1, ctx.wait_ns));
+          ok = wait_bounded(v_land, tails & 1, ctx.wait_ns);
+          // given up: what follows is for nobody, but the copy must not outlive the block
+          if (!ok) (void)wait_bounded(v_land, tails & 1, kDrainNs);
           ++tails;
           uint8_t* tile = ring + stage * C::TILE_BYTES;
           for (int i = valid * 8 + lane; i < kKeys * 8; i += 32)
@@ -776,7 +789,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
       // no copy may be in flight when the block's shared memory goes
       for (int slot = max(0, used - C::STAGES); slot < used; ++slot)
-        (void)wait_bounded(full + slot % C::STAGES, (slot / C::STAGES) & 1, ctx.wait_ns);
+        (void)wait_bounded(full + slot % C::STAGES, (slot / C::STAGES) & 1, kDrainNs);
     } else if (warp == kItemWarp) {
       // ---- the block's items, one ahead of their rows, and after the last an item without key
       // tiles; a warpgroup's rows are loaded as soon as the item before is done with them
@@ -788,8 +801,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       auto publish = [&](int j) {
         if (!walk.next(&next)) next.kt0 = next.kt1 = 0;
         if (j >= kItems)
-          ok = __all_sync(0xffffffffu, wait_bounded(item_free + j % kItems,
-                                                    (j / kItems - 1) & 1, ctx.wait_ns));
+          ok = wait_bounded(item_free + j % kItems, (j / kItems - 1) & 1, ctx.wait_ns);
         if (ok && lane == 0) {
           items[j % kItems] = next;
           arrive(item_full + j % kItems);
@@ -805,8 +817,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         for (int w = 0; w < 2; ++w) {
           if (!ok || plan.tiles(w) == 0) continue;
           if (loaded[w] > 0)
-            ok = __all_sync(0xffffffffu, wait_bounded(q_free + w, (loaded[w] - 1) & 1,
-                                                      ctx.wait_ns));
+            ok = wait_bounded(q_free + w, (loaded[w] - 1) & 1, ctx.wait_ns);
           if (!ok) continue;
           if (lane == 0) {
             mbar_arrive_expect_tx(q_full + w, C::TILE_BYTES);
@@ -823,7 +834,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
 #pragma unroll
       for (int w = 0; w < 2; ++w)
-        if (loaded[w] > 0) (void)wait_bounded(q_full + w, (loaded[w] - 1) & 1, ctx.wait_ns);
+        if (loaded[w] > 0) (void)wait_bounded(q_full + w, (loaded[w] - 1) & 1, kDrainNs);
     }
     __syncwarp();
   }
