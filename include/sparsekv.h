@@ -680,7 +680,10 @@ kv_status kv_check_device_errors(cudaStream_t stream, int32_t* flags);
 /*
  * kv_set_wait_limit_ns -- host: limit, in nanoseconds of the GPU's global timer, of every
  * device-side wait on an asynchronous copy (default 2e9). After it runs out the kernel
- * flags KV_DEVERR_TIMEOUT, drains its own copies (again bounded) and returns.
+ * flags KV_DEVERR_TIMEOUT, drains its own copies (again bounded, by a time of its own where the
+ * limit is short) and returns. The GPU looks at the time only once or twice in some microseconds,
+ * so a wait may last longer than a short limit. Where kv_prefill_attn waits for its own products
+ * over a row tile's keys, the limit counts once for every 128 keys.
  */
 kv_status kv_set_wait_limit_ns(uint64_t limit_ns);
 

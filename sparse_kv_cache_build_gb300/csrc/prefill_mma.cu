@@ -793,15 +793,27 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
     } else if (warp == kItemWarp) {
       // ---- the block's items, one ahead of their rows, and after the last an item without key
       // tiles; a warpgroup's rows are loaded as soon as the item before is done with them
+      // Its waits are for work, not for copies: an item takes as long as it has keys (11 ms over
+      // 2^20), so the limit counts per key tile of the items not known to be done.
       ItemWalk<MmaShape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
       if (lane == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
       bool ok = true;
       int loaded[2] = {0, 0};
       PrefillItem it, next{};
+      int open[kItems] = {};                         // key tiles of the last items published
+      auto patience = [&]() {
+        unsigned long long tiles = 1;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) tiles += open[i];
+        return ctx.wait_ns <= ~0ull / tiles ? ctx.wait_ns * tiles : ~0ull;
+      };
       auto publish = [&](int j) {
         if (!walk.next(&next)) next.kt0 = next.kt1 = 0;
         if (j >= kItems)
-          ok = wait_bounded(item_free + j % kItems, (j / kItems - 1) & 1, ctx.wait_ns);
+          ok = wait_bounded(item_free + j % kItems, (j / kItems - 1) & 1, patience());
+#pragma unroll
+        for (int i = 0; i + 1 < kItems; ++i) open[i] = open[i + 1];
+        open[kItems - 1] = next.kt1 - next.kt0;
         if (ok && lane == 0) {
           items[j % kItems] = next;
           arrive(item_full + j % kItems);
@@ -817,7 +829,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         for (int w = 0; w < 2; ++w) {
           if (!ok || plan.tiles(w) == 0) continue;
           if (loaded[w] > 0)
-            ok = wait_bounded(q_free + w, (loaded[w] - 1) & 1, ctx.wait_ns);
+            ok = wait_bounded(q_free + w, (loaded[w] - 1) & 1, patience());
           if (!ok) continue;
           if (lane == 0) {
             mbar_arrive_expect_tx(q_full + w, C::TILE_BYTES);

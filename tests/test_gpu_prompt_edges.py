@@ -56,6 +56,21 @@ def test_waits_that_run_out_are_flagged_and_end_the_call(wait_limit, D):
         assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
 
 
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("limit", [50_000, 2 ** 64 - 1])
+def test_long_items_do_not_run_out_of_a_copy_s_limit(wait_limit, limit, D):
+    """The limit is for copies: 2^22 keys keep a block busy for 40 ms, each copy for microseconds.
+    The largest limit there is does not wrap round."""
+    c = long_items(D, 1 << 22)
+    ref, ref_lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, num_shares=1)
+    assert_no_device_error()
+    wait_limit(limit)
+    out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, num_shares=1)
+    wait_limit(2_000_000_000)
+    assert_no_device_error()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
 @pytest.mark.parametrize("new,past,D,G,PS,shares", [
     ((700, 1, 129, 64), (0, 2000, 90, 33), 128, 4, 16, 0),
     ((700, 1, 129, 64), (0, 2000, 90, 33), 64, 8, 32, 1),
