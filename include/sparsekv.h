@@ -219,8 +219,8 @@ kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * elements from one token to the next (so the three may be column ranges of one fused
  * projection): at least heads * head_dim, a multiple of 16 bytes; all bases 16-byte aligned
  * (KV_ERR_MISALIGNED). A page that two sequences of the batch share must not be written by
- * both. Rows that belong to no sequence are left alone. A sequence shorter than its new tokens
- * (KV_DEVERR_BAD_LEN: it is left out), bad offsets (KV_DEVERR_BAD_LEN: which other sequences
+ * both. Rows that belong to no sequence are left alone. A sequence shorter than its new tokens or
+ * longer than its page-table row (KV_DEVERR_BAD_LEN: it is left out), bad offsets (KV_DEVERR_BAD_LEN: which other sequences
  * are then left out is unspecified) and an unmapped page (KV_DEVERR_BAD_PAGE: its keys and
  * values are left out) are flagged on the device.
  */

@@ -294,7 +294,7 @@ append_rope_single_kernel(kv_cache_desc d, RopeArgs a, DevCtx ctx) {
   load_cols<T>(is_q ? a.q : is_v ? a.v : a.k,
                b * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + (int64_t)head * D,
                ca, cb, &x);
-  const int len = checked_len(ctx, d, b);
+  const int len = packed_len(ctx, d, b);
   if (len == 0) return;                                    // nothing to append
   if (turns && !is_v) {
     uint64_t f[8];

@@ -21,12 +21,21 @@ struct SeqRows {
   int len;    // sequence length, the new tokens included
 };
 
+// Length of sequence b; one that is negative or longer than its page-table row is flagged and 0:
+// where its new tokens belong is not known, and clamped they would fall on cached ones.
+__device__ __forceinline__ int packed_len(const DevCtx& c, const kv_cache_desc& d, int b) {
+  const int len = d.seq_lens[b];
+  if (len >= 0 && len <= d.page_table_stride * d.page_size) return len;
+  flag(c, KV_DEVERR_BAD_LEN);
+  return 0;
+}
+
 // Offsets must rise from 0 and stay inside [0, total], and a sequence holds at least its new
 // tokens; anything else is flagged and the sequence is left out.
 __device__ __forceinline__ SeqRows seq_rows(const DevCtx& c, const kv_cache_desc& d,
                                             const PackedRows& pr, int b) {
   SeqRows s;
-  s.len = checked_len(c, d, b);
+  s.len = packed_len(c, d, b);
   if (pr.cu == nullptr) {
     s.row0 = b;
     s.n = s.len > 0 ? 1 : 0;

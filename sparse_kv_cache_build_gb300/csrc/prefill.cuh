@@ -284,7 +284,7 @@ __device__ __forceinline__ void finish_empty(const DevCtx& ctx, const kv_cache_d
     return;
   }
   for (int b = blockIdx.x; b < d.batch; b += gridDim.x) {
-    if (d.seq_lens[b] > 0) continue;
+    if (d.seq_lens[b] != 0) continue;                // of a bad length: left out
     T* out = static_cast<T*>(a.out) + (int64_t)b * a.Hq * D;
     for (int i = threadIdx.x; i < a.Hq * D; i += blockDim.x) out[i] = T{};
     if (a.lse != nullptr)

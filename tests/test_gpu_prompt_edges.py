@@ -27,6 +27,63 @@ def wait_limit():
     binding.lib().kv_set_wait_limit_ns(2_000_000_000)
 
 
+# ---------------------------------------------------------------- lengths out of range
+
+@pytest.mark.parametrize("over", [1, 7, 2 ** 31 - 1, -1])
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp32", 64)])
+def test_append_leaves_out_a_sequence_longer_than_its_table(dtype, D, packed, over):
+    """Its new tokens have no place: cached tokens, statistics and q_out stay as they were, and
+    the other sequences are appended."""
+    new = (3, 9, 1) if packed else (1, 1, 1)
+    c = Case(new, (13, 23, 31), dtype, D, PS=16)       # two pages of 16 each: the second is full
+    stats = c.past_stats()
+    want_q = torch.full(c.q.shape, -9.0, dtype=c.q.dtype, device="cuda")
+    q_out = want_q.clone()
+    k0, v0, s0 = c.k_pool.clone(), c.v_pool.clone(), stats.clone()
+    lens = list(c.lens)
+    turns = skv.kv_rope_turns([1.0] * (D // 2), device="cuda")
+    cu = c.cu if packed else None
+    skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=cu, q_out=want_q)
+    assert_no_device_error()
+    k1, v1, s1 = c.k_pool.clone(), c.v_pool.clone(), stats.clone()
+    c.k_pool.copy_(k0)
+    c.v_pool.copy_(v0)
+    stats.copy_(s0)
+    lens[1] = over if over in (-1, 2 ** 31 - 1) else 2 * 16 + over
+    c.set_len(lens)
+    skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=cu, q_out=q_out)
+    assert skv.kv_check_device_errors() == (-5, 2)
+    mid, rest = c.table[1, :2].long(), c.table[[0, 2]].flatten().long()
+    rest = rest[rest >= 0]
+    for got, old, full in ((c.k_pool, k0, k1), (c.v_pool, v0, v1), (stats, s0, s1)):
+        assert torch.equal(got[mid], old[mid]) and torch.equal(got[rest], full[rest])
+    rows = slice(int(c.cu_h[1]), int(c.cu_h[2]))
+    assert (q_out[rows] == -9.0).all()
+    for r in (slice(0, rows.start), slice(rows.stop, None)):
+        assert torch.equal(q_out[r], want_q[r])
+
+
+@pytest.mark.parametrize("over", [1, 7, 2 ** 31 - 1, -1])
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("dtype,shares", [("bf16", 1), ("bf16", 3), ("fp32", 0)])
+def test_attention_leaves_out_a_sequence_longer_than_its_table(dtype, shares, packed, over):
+    c = Case((3, 9, 1) if packed else (1, 1, 1), (13, 23, 31), dtype, 128, PS=16)
+    want, _, tol, _ = c.attn_bounds(c.q)
+    lens = list(c.lens)
+    lens[1] = over if over in (-1, 2 ** 31 - 1) else 2 * 16 + over
+    c.set_len(lens)
+    out = torch.full(c.q.shape, -9.0, dtype=c.q.dtype, device="cuda")
+    lse = torch.full(c.q.shape[:2], -9.0, device="cuda")
+    skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu if packed else None,
+                        num_shares=shares, out=out, lse=lse)
+    assert skv.kv_check_device_errors() == (-5, 2)
+    rows = slice(int(c.cu_h[1]), int(c.cu_h[2]))
+    assert (out[rows] == -9.0).all() and (lse[rows] == -9.0).all()
+    for r in (slice(0, rows.start), slice(rows.stop, None)):
+        assert (np.abs(f64(out[r]) - want[r]) <= tol[r]).all()
+
+
 # ------------------------------------------------------------------ waits that run out
 
 def long_items(D, tokens):
