@@ -222,7 +222,8 @@ kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * both. Rows that belong to no sequence are left alone. A sequence shorter than its new tokens or
  * longer than its page-table row (KV_DEVERR_BAD_LEN: it is left out), bad offsets (KV_DEVERR_BAD_LEN: which other sequences
  * are then left out is unspecified) and an unmapped page (KV_DEVERR_BAD_PAGE: its keys and
- * values are left out) are flagged on the device.
+ * values are left out) are flagged on the device. KV_ERR_UNSUPPORTED for page-table rows of
+ * 2^31 - 256 tokens (page_table_stride * page_size) or more.
  */
 kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_stride,
                          int32_t num_q_heads, const void* k_new, int64_t k_stride,
@@ -256,7 +257,7 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
  * on the device and the sequence left out; an unmapped page is flagged and not read, and its
  * sequence's rows are unspecified.
  * KV_ERR_UNSUPPORTED for bf16 pools of 2^31 rows (num_phys_pages * num_kv_heads * page_size)
- * or more.
+ * or more, and for page-table rows of 2^31 - 256 tokens or more.
  */
 size_t kv_prefill_attn_workspace_size(const kv_cache_desc* cache, int32_t num_q_heads,
                                       int32_t total_tokens, int32_t num_shares);

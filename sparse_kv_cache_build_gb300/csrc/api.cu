@@ -211,8 +211,10 @@ kv_status check_rows(const kv_cache_desc* d, const void* p, int64_t stride, int 
   return KV_OK;
 }
 
-// Offsets and row count of a packed batch.
+// Offsets and row count of a packed batch. The kernels count positions in 32 bits and look up to
+// a tile of 256 rows past a sequence's end, so the table's last tokens must leave room for one.
 kv_status check_packed(const kv_cache_desc* d, const int32_t* cu_tokens, int32_t total_tokens) {
+  if ((int64_t)d->page_table_stride * d->page_size > INT32_MAX - 256) return KV_ERR_UNSUPPORTED;
   if (total_tokens < 0 || (cu_tokens == nullptr && total_tokens != d->batch))
     return KV_ERR_INVALID_ARG;
   return KV_OK;

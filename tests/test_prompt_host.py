@@ -61,6 +61,17 @@ def test_append_refusals(lib, kw, status):
     assert append(lib, **kw) == status
 
 
+@pytest.mark.parametrize("page_size", [16, 32, 64])
+def test_tables_whose_positions_pass_32_bits_are_refused(lib, page_size):
+    """2^31 - 256 tokens to a table row and more: the rows of a tile may lie past the last."""
+    last = (2 ** 31 - 1 - 256) // page_size
+    most = (2 ** 31 - 1) // page_size
+    for stride, status in ((last, 0), (last + 1, -2), (most, -2)):
+        d = desc(page_size=page_size, page_table_stride=stride)
+        assert append(lib, d, total=0) == status
+        assert attn(lib, d, total=0) == status
+
+
 def test_append_refuses_bad_caches_and_accepts_nothing_to_do(lib):
     assert append(lib, desc(head_dim=96)) == -2
     assert append(lib, desc(k_pool=NULL)) == -1
