@@ -168,6 +168,20 @@ def _raw_stream(kv, stream):
             else stream.cuda_stream)
 
 
+def _new(shape, dtype, device, stream, zero=False):
+    """A buffer that a call makes for itself and uses on `stream` (None: the current one). It is
+    allocated there, so that its memory neither has work of another stream pending nor goes to
+    one while the call still runs; the current stream may read it (after waiting for the call)
+    and drop it."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -385,7 +399,7 @@ def kv_append_rope(kv: PagedKV, q, k_new, v_new, stats, turns=None, cu_tokens=No
     if positions is not None:
         _on_device(kv, positions, "positions", torch.int32, (T,))
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=kv.elem, device=q.device)
+        q_out = _new((T, Hq, D), kv.elem, q.device, stream)
         os_ = Hq * D
     else:
         os_ = _rows(kv, q_out, "q_out", Hq)
@@ -415,18 +429,18 @@ def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares:
     T, Hq, qs, cu = _packed(kv, q, cu_tokens)
     D = kv.cols
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=kv.elem, device=q.device)
+        out = _new((T, Hq, D), kv.elem, q.device, stream)
     else:
         _on_device(kv, out, "out", kv.elem, (T, Hq, D))
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((T, Hq), torch.float32, q.device, stream)
     else:
         _on_device(kv, lse, "lse", torch.float32, (T, Hq))
     if T == 0:
         return out, lse
     if workspace is None:
         nbytes = kv_prefill_attn_workspace_size(kv, Hq, T, num_shares)
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+        workspace = _new((nbytes,), torch.uint8, q.device, stream)
     elif workspace.get_device() != kv.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {kv.k_pool.device}")
     status = lib().kv_prefill_attn(

@@ -84,6 +84,58 @@ def test_attention_leaves_out_a_sequence_longer_than_its_table(dtype, shares, pa
         assert (np.abs(f64(out[r]) - want[r]) <= tol[r]).all()
 
 
+# ---------------------------------------------------------------------- streams by argument
+
+def busy(stream):
+    """Work of some milliseconds on a stream, so that what follows there runs after the host's."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(10_000_000)
+
+
+def test_attention_on_streams_given_by_argument():
+    """Buffers that the call makes for itself belong to its stream: the current stream's later
+    allocations and writes do not touch them, nor do two calls on two streams share one."""
+    c = Case((200, 31, 1), (100, 900, 4000), "bf16", 128, 4)
+    ref, ref_lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu)
+    nbytes = skv.kv_prefill_attn_workspace_size(c.kv, c.Hq, c.T)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for s in streams:
+            busy(s)
+        for s in streams:
+            got.append(skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu, stream=s))
+        for n in (nbytes, ref.numel() * 2, ref_lse.numel() * 4):
+            for _ in range(3):                # what the allocator would hand out again
+                torch.empty((n,), dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert_no_device_error()
+        for out, lse in got:
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+def test_append_on_a_stream_given_by_argument():
+    """The rotated queries' buffer is the stream's: not one that the current stream still uses."""
+    c = Case((40, 3), (9, 30), "bf16", 128, 4, PS=16)
+    turns = skv.kv_rope_turns([0.5] * 64, device="cuda")
+    stats = c.past_stats()
+    ref = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=c.cu)
+    k1, s1 = c.k_pool.clone(), stats.clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        old = torch.empty_like(ref)           # freed with a write of this stream still to come
+        torch.cuda._sleep(10_000_000)
+        old.fill_(7.0)
+        del old
+        q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=c.cu, stream=s)
+        torch.cuda.synchronize()
+        assert_no_device_error()
+        assert torch.equal(q, ref) and torch.equal(c.k_pool, k1) and torch.equal(stats, s1)
+        del q
+
+
 # ------------------------------------------------------------------ waits that run out
 
 def long_items(D, tokens):
