@@ -168,18 +168,19 @@ def _raw_stream(kv, stream):
             else stream.cuda_stream)
 
 
-def _new(shape, dtype, device, stream, zero=False):
+def _new(shape, dtype, device, stream, fill=None):
     """A buffer that a call makes for itself and uses on `stream` (None: the current one). It is
     allocated there, so that its memory neither has work of another stream pending nor goes to
     one while the call still runs; the current stream may read it (after waiting for the call)
     and drop it."""
-    make = torch.zeros if zero else torch.empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = make(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            t = _new(shape, dtype, device, None, fill)
+        t.record_stream(torch.cuda.current_stream(t.device))
+        return t
+    if fill is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.full(shape, fill, dtype=dtype, device=device)
 
 
 def _ptr(t):
@@ -272,7 +273,7 @@ def kv_build_page_stats(kv: PagedKV, stats=None, phys_pages=None, stream=None):
     tensor of physical page indices) of the mapped pages in that subset only."""
     NP, Hkv, PS, D = kv.k_pool.shape
     if stats is None:
-        stats = torch.empty((NP, Hkv, 2, D), dtype=kv.dtype, device=kv.k_pool.device)
+        stats = _new((NP, Hkv, 2, D), kv.dtype, kv.k_pool.device, stream)
     _need(stats, "stats", kv.dtype, (NP, Hkv, 2, D))
     n_phys = 0
     if phys_pages is not None:
@@ -291,9 +292,9 @@ def kv_build_page_stats_fp8(kv: PagedKV, stats=None, stats_exp=None, stream=None
     NP, Hkv, D = kv.k_pool.shape[0], kv.num_kv_heads, kv.head_dim
     dev = kv.k_pool.device
     if stats is None:
-        stats = torch.zeros((NP, Hkv, 2, D), dtype=torch.uint8, device=dev)
+        stats = _new((NP, Hkv, 2, D), torch.uint8, dev, stream, fill=0)
     if stats_exp is None:
-        stats_exp = torch.zeros((NP, Hkv), dtype=torch.int8, device=dev)
+        stats_exp = _new((NP, Hkv), torch.int8, dev, stream, fill=0)
     _need(stats, "stats", torch.uint8, (NP, Hkv, 2, D))
     _need(stats_exp, "stats_exp", torch.int8, (NP, Hkv))
     _check("kv_build_page_stats_fp8", lib().kv_build_page_stats_fp8(
@@ -307,8 +308,7 @@ def kv_score_pages_fp8(kv: PagedKV, q, stats, stats_exp, scores=None, stream=Non
     _need(stats_exp, "stats_exp", torch.int8)
     B, Hq, _ = q.shape
     if scores is None:
-        scores = torch.empty((B, kv.num_kv_heads, kv.stride), dtype=torch.float32,
-                             device=q.device)
+        scores = _new((B, kv.num_kv_heads, kv.stride), torch.float32, q.device, stream)
     _need(scores, "scores", torch.float32)
     _check("kv_score_pages_fp8", lib().kv_score_pages_fp8(
         kv.ref(), _ptr(q), Hq, _ptr(stats), _ptr(stats_exp), _ptr(scores), scores.shape[-1],
@@ -456,8 +456,7 @@ def kv_score_pages(kv: PagedKV, q, stats, scores=None, stream=None):
     _need(q, "q", kv.dtype)
     Hq = q.shape[1]
     if scores is None:
-        scores = torch.empty((kv.batch, kv.num_kv_heads, kv.stride), dtype=torch.float32,
-                             device=q.device)
+        scores = _new((kv.batch, kv.num_kv_heads, kv.stride), torch.float32, q.device, stream)
     _need(scores, "scores", torch.float32)
     _check("kv_score_pages", lib().kv_score_pages(kv.ref(), _ptr(q), Hq, _ptr(stats), _ptr(scores),
                                                   scores.shape[-1], _stream(stream)))
@@ -482,9 +481,9 @@ def kv_select_topk(scores, seq_lens, page_size: int, keep=None, keep_ratio: floa
     if k_max is None:
         k_max = stride if keep is not None else max_keep_pages(stride, keep_ratio, budget_pages)
     if sel_idx is None:
-        sel_idx = torch.empty((B, Hkv, k_max), dtype=torch.int32, device=scores.device)
+        sel_idx = _new((B, Hkv, k_max), torch.int32, scores.device, stream)
     if sel_cnt is None:
-        sel_cnt = torch.empty((B, Hkv), dtype=torch.int32, device=scores.device)
+        sel_cnt = _new((B, Hkv), torch.int32, scores.device, stream)
     _need(sel_idx, "sel_idx", torch.int32, (B, Hkv, k_max))
     _need(sel_cnt, "sel_cnt", torch.int32, (B, Hkv))
     if keep is not None:
@@ -509,9 +508,9 @@ def kv_select_structured(scores, seq_lens, page_size: int, batch: int, num_kv_he
         k_max = min(stride, max_keep_pages(stride, keep_ratio if keep_ratio else None,
                                            budget_pages or None) + sink_pages + local_pages)
     if sel_idx is None:
-        sel_idx = torch.empty((batch, num_kv_heads, k_max), dtype=torch.int32, device=dev)
+        sel_idx = _new((batch, num_kv_heads, k_max), torch.int32, dev, stream)
     if sel_cnt is None:
-        sel_cnt = torch.empty((batch, num_kv_heads), dtype=torch.int32, device=dev)
+        sel_cnt = _new((batch, num_kv_heads), torch.int32, dev, stream)
     _need(sel_idx, "sel_idx", torch.int32, (batch, num_kv_heads, k_max))
     _need(sel_cnt, "sel_cnt", torch.int32, (batch, num_kv_heads))
     if keep is not None:
@@ -540,9 +539,9 @@ def kv_sparse_decode_attn(kv: PagedKV, q, sm_scale: float, sel_idx=None, sel_cnt
         num_splits = kv_auto_num_splits(kv, Hq, bound)
     S = int(num_splits)
     if part_acc is None:
-        part_acc = torch.empty((B, Hq, S, D), dtype=torch.float32, device=q.device)
+        part_acc = _new((B, Hq, S, D), torch.float32, q.device, stream)
     if part_ml is None:
-        part_ml = torch.empty((B, Hq, S, 2), dtype=torch.float32, device=q.device)
+        part_ml = _new((B, Hq, S, 2), torch.float32, q.device, stream)
     _need(part_acc, "part_acc", torch.float32, (B, Hq, S, D))
     _need(part_ml, "part_ml", torch.float32, (B, Hq, S, 2))
     sel_stride = 0
@@ -574,16 +573,16 @@ def kv_select_decode_attn(kv: PagedKV, q, sm_scale: float, scores=None, keep_rat
     S = int(num_splits)
     dev = q.device
     if part_acc is None:
-        part_acc = torch.empty((B, Hq, S, D), dtype=torch.float32, device=dev)
+        part_acc = _new((B, Hq, S, D), torch.float32, dev, stream)
     if part_ml is None:
-        part_ml = torch.empty((B, Hq, S, 2), dtype=torch.float32, device=dev)
+        part_ml = _new((B, Hq, S, 2), torch.float32, dev, stream)
     if merge:
         if counters is None:
-            counters = torch.zeros((B, Hkv), dtype=torch.int32, device=dev)
+            counters = _new((B, Hkv), torch.int32, dev, stream, fill=0)
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+            out = _new((B, Hq, D), torch.float32, dev, stream)
         if lse is None:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+            lse = _new((B, Hq), torch.float32, dev, stream)
         _need(counters, "counters", torch.int32, (B, Hkv))
     else:
         counters = out = lse = None
@@ -610,13 +609,13 @@ def kv_score_select(kv: PagedKV, q, stats, keep_ratio: float = 0.0, budget_pages
     if k_max is None:
         k_max = max_keep_pages(stride, keep_ratio, budget_pages)
     if scores is None:
-        scores = torch.empty((B, Hkv, stride), dtype=torch.float32, device=dev)
+        scores = _new((B, Hkv, stride), torch.float32, dev, stream)
     if counters is None:
-        counters = torch.zeros((B, Hkv), dtype=torch.int32, device=dev)
+        counters = _new((B, Hkv), torch.int32, dev, stream, fill=0)
     if sel_idx is None:
-        sel_idx = torch.empty((B, Hkv, k_max), dtype=torch.int32, device=dev)
+        sel_idx = _new((B, Hkv, k_max), torch.int32, dev, stream)
     if sel_cnt is None:
-        sel_cnt = torch.empty((B, Hkv), dtype=torch.int32, device=dev)
+        sel_cnt = _new((B, Hkv), torch.int32, dev, stream)
     _need(scores, "scores", torch.float32)
     _need(counters, "counters", torch.int32, (B, Hkv))
     _need(sel_idx, "sel_idx", torch.int32, (B, Hkv, k_max))
@@ -641,15 +640,15 @@ def kv_decode_attn_merge(kv: PagedKV, q, sm_scale: float, sel_idx=None, sel_cnt=
         num_splits = kv_auto_num_splits(kv, Hq, bound)
     S = int(num_splits)
     if part_acc is None:
-        part_acc = torch.empty((B, Hq, S, D), dtype=torch.float32, device=dev)
+        part_acc = _new((B, Hq, S, D), torch.float32, dev, stream)
     if part_ml is None:
-        part_ml = torch.empty((B, Hq, S, 2), dtype=torch.float32, device=dev)
+        part_ml = _new((B, Hq, S, 2), torch.float32, dev, stream)
     if counters is None:
-        counters = torch.zeros((B, kv.num_kv_heads), dtype=torch.int32, device=dev)
+        counters = _new((B, kv.num_kv_heads), torch.int32, dev, stream, fill=0)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=dev)
+        out = _new((B, Hq, D), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        lse = _new((B, Hq), torch.float32, dev, stream)
     _need(part_acc, "part_acc", torch.float32, (B, Hq, S, D))
     _need(part_ml, "part_ml", torch.float32, (B, Hq, S, 2))
     _need(counters, "counters", torch.int32, (B, kv.num_kv_heads))
@@ -669,9 +668,9 @@ def kv_merge_splits(part_acc, part_ml, out=None, lse=None, stream=None):
     B, Hq, S, D = part_acc.shape
     _need(part_ml, "part_ml", torch.float32, (B, Hq, S, 2))
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=part_acc.device)
+        out = _new((B, Hq, D), torch.float32, part_acc.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=part_acc.device)
+        lse = _new((B, Hq), torch.float32, part_acc.device, stream)
     _need(out, "out", torch.float32, (B, Hq, D))
     _check("kv_merge_splits", lib().kv_merge_splits(
         _ptr(part_acc), _ptr(part_ml), B, Hq, S, D, _ptr(out), _ptr(lse), _stream(stream)))
@@ -689,10 +688,10 @@ def kv_dropped_mass(kv: PagedKV, q, sm_scale: float, sel_idx, sel_cnt, delta=Non
     _need(sel_idx, "sel_idx", torch.int32)
     _need(sel_cnt, "sel_cnt", torch.int32)
     if delta is None:
-        delta = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        delta = _new((B, Hq), torch.float32, q.device, stream)
     nbytes = kv_dropped_mass_workspace_size(kv, Hq)
     if workspace is None:
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+        workspace = _new((nbytes,), torch.uint8, q.device, stream)
     _check("kv_dropped_mass", lib().kv_dropped_mass(
         kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(sel_idx), _ptr(sel_cnt),
         sel_idx.shape[-1], _ptr(delta), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -723,12 +722,12 @@ def kv_decode_step(kv: PagedKV, q, sm_scale: float, stats=None, keep_ratio: floa
     if k_max is None:
         k_max = max_keep_pages(kv.stride, keep_ratio, budget_pages)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _new((B, Hq, D), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = kv_decode_step_workspace_size(kv, Hq, k_max, max(num_splits, 0))
-        workspace = torch.zeros((nbytes,), dtype=torch.uint8, device=q.device)
+        workspace = _new((nbytes,), torch.uint8, q.device, stream, fill=0)
     _check("kv_decode_step", lib().kv_decode_step(
         kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(stats), float(keep_ratio),
         int(budget_pages), int(k_max), int(num_splits), _ptr(out), _ptr(lse),
@@ -818,12 +817,12 @@ def kv_decode_step_fp8(kv: PagedKV, q, sm_scale: float, stats=None, stats_exp=No
     if k_max is None:
         k_max = max_keep_pages(kv.stride, keep_ratio, budget_pages)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _new((B, Hq, D), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq), torch.float32, q.device, stream)
     if workspace is None:
         nbytes = kv_decode_step_workspace_size(kv, Hq, k_max, max(num_splits, 0))
-        workspace = torch.zeros((nbytes,), dtype=torch.uint8, device=q.device)
+        workspace = _new((nbytes,), torch.uint8, q.device, stream, fill=0)
     _check("kv_decode_step_fp8", lib().kv_decode_step_fp8(
         kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(stats), _ptr(stats_exp),
         float(keep_ratio), int(budget_pages), int(k_max), int(num_splits), _ptr(out), _ptr(lse),
@@ -836,8 +835,8 @@ def kv_entmax_page_moments(kv: PagedKV, q, stats, sm_scale: float, stream=None):
     of z = sm_scale * q.k / 2."""
     _need(q, "q", kv.dtype)
     B, Hq, _ = q.shape
-    zb, cz, vz = (torch.full((B, Hq, kv.stride), float("nan"), dtype=torch.float32,
-                             device=q.device) for _ in range(3))
+    zb, cz, vz = (_new((B, Hq, kv.stride), torch.float32, q.device, stream, fill=float("nan"))
+                  for _ in range(3))
     _check("kv_entmax_page_moments", lib().kv_entmax_page_moments(
         kv.ref(), _ptr(q), Hq, _ptr(stats), float(sm_scale), _ptr(zb), _ptr(cz), _ptr(vz),
         kv.stride, _stream(stream)))
@@ -853,9 +852,9 @@ def kv_entmax_select(zb, cz, vz, seq_lens, page_size: int, num_kv_heads: int,
     if k_max is None:
         k_max = stride
     dev = zb.device
-    sel = torch.empty((B, num_kv_heads, k_max), dtype=torch.int32, device=dev)
-    cnt = torch.empty((B, num_kv_heads), dtype=torch.int32, device=dev)
-    tau = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    sel = _new((B, num_kv_heads, k_max), torch.int32, dev, stream)
+    cnt = _new((B, num_kv_heads), torch.int32, dev, stream)
+    tau = _new((B, Hq), torch.float32, dev, stream)
     _check("kv_entmax_select", lib().kv_entmax_select(
         _ptr(zb), _ptr(cz), _ptr(vz), stride, _ptr(seq_lens), int(page_size), B, Hq,
         int(num_kv_heads), int(k_max), _ptr(sel), _ptr(cnt), _ptr(tau), _stream(stream)))
@@ -869,12 +868,12 @@ def kv_entmax_decode_attn(kv: PagedKV, q, sm_scale: float, sel_idx=None, sel_cnt
     B, Hq, D = q.shape
     sel_stride = sel_idx.shape[-1] if sel_idx is not None else 0
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _new((B, Hq, D), torch.float32, q.device, stream)
     if tau is None:
-        tau = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        tau = _new((B, Hq), torch.float32, q.device, stream)
     if workspace is None:
         n = int(lib().kv_entmax_attn_workspace_size(kv.ref(), Hq, sel_stride))
-        workspace = torch.empty((n,), dtype=torch.uint8, device=q.device)
+        workspace = _new((n,), torch.uint8, q.device, stream)
     _check("kv_entmax_decode_attn", lib().kv_entmax_decode_attn(
         kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(sel_idx), _ptr(sel_cnt), sel_stride,
         _ptr(out), _ptr(tau), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -894,12 +893,12 @@ def kv_entmax_decode_step(kv: PagedKV, q, sm_scale: float, stats, k_max: int | N
     if k_max is None:
         k_max = kv.stride
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _new((B, Hq, D), torch.float32, q.device, stream)
     if tau is None:
-        tau = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        tau = _new((B, Hq), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = torch.empty((kv_entmax_decode_step_workspace_size(kv, Hq, k_max),),
-                                dtype=torch.uint8, device=q.device)
+        nbytes = kv_entmax_decode_step_workspace_size(kv, Hq, k_max)
+        workspace = _new((nbytes,), torch.uint8, q.device, stream)
     _check("kv_entmax_decode_step", lib().kv_entmax_decode_step(
         kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(stats), int(k_max), _ptr(out), _ptr(tau),
         _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -937,9 +936,9 @@ def kv_decode_step_static(kv: PagedKV, q, sm_scale: float, stats=None, keep_rati
     if k_max is None:
         k_max = max_keep_pages(kv.stride, keep_ratio, budget_pages)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        out = _new((B, Hq, D), torch.float32, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq), torch.float32, q.device, stream)
     st = lib().kv_decode_step_static(
         kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(stats), float(keep_ratio),
         int(budget_pages), int(k_max), int(num_splits), _ptr(out), _ptr(lse), _stream(stream))
