@@ -767,6 +767,9 @@ class DecodeStepGraph:
         # the buffers must outlive the graph: keep them referenced
         self._keep = (kv, q, stats, workspace, q_host, out_host)
         handle = ctypes.c_void_p()
+        # the library runs the step once, on a stream of its own: the zeros of the workspace and
+        # what the caller has still to write here come first
+        torch.cuda.current_stream(q.device).synchronize()
         _check("kv_decode_step_graph_create", lib().kv_decode_step_graph_create(
             kv.ref(), _ptr(q), Hq, float(sm_scale), _ptr(stats), float(keep_ratio),
             int(budget_pages), int(k_max), int(num_splits), _ptr(self.out), _ptr(self.lse),

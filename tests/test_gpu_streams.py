@@ -116,6 +116,27 @@ def test_a_call_s_own_buffers_are_its_stream_s(cache, name):
             assert torch.equal(a, b)
 
 
+def test_a_step_graph_is_made_after_the_current_stream_s_writes():
+    """Creation runs the step once: on the lengths that the current stream was about to write."""
+    w = workload(num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16, dtype="bf16", seed=6,
+                 seq_lens=(500, 300))
+    c = inputs.make_cache(w, "cuda")
+    kv = skv.PagedKV.from_cache(c)
+    stats = skv.kv_build_page_stats(kv)
+    want, _ = skv.kv_decode_step(kv, c.q, w.sm_scale, stats, budget_pages=8)
+    lens = c.seq_lens.clone()
+    for _ in range(3):
+        c.seq_lens.fill_(-5)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        c.seq_lens.copy_(lens)
+        g = skv.DecodeStepGraph(kv, c.q, w.sm_scale, stats, budget_pages=8)
+        out, _ = g.launch()
+        assert_no_device_error()
+        assert torch.equal(out, want)
+        g.close()
+
+
 def test_a_call_on_the_capturing_stream_given_by_argument(cache):
     q, scale, kv = cache["c"].q, cache["scale"], cache["kv"]
     want = skv.kv_decode_step(kv, q, scale)
