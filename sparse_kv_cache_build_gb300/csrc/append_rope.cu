@@ -192,6 +192,10 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
     mn.a[e] = mn.b[e] = INFINITY;
     mx.a[e] = mx.b[e] = -INFINITY;
   }
+  // Columns of the page's first key that are NaN: the full build begins with that key, so they
+  // stay NaN, where those of later keys do not count. (Beginning with the key here instead of
+  // with infinities costs 1 us of 39 and 87.)
+  uint32_t nan = 0;
   const int warps = blockDim.x >> 5;
   for (int t = t0 + warp * RPW + r; t < t1; t += warps * RPW) {
     const int64_t row = sr.row0 + (t - start);
@@ -218,6 +222,11 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
         mn.b[e] = lower(mn.b[e], k.b[e]);
         mx.a[e] = upper(mx.a[e], k.a[e]);
         mx.b[e] = upper(mx.b[e], k.b[e]);
+      }
+      if (t == page * PS) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          nan |= (isnan(k.a[e]) ? 1u << e : 0u) | (isnan(k.b[e]) ? 256u << e : 0u);
       }
     }
     for (int h0 = 0; h0 < G; h0 += HEADS) {
@@ -251,6 +260,13 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
       sh_mn[warp][cb + e] = mn.b[e];
       sh_mx[warp][ca + e] = mx.a[e];
       sh_mx[warp][cb + e] = mx.b[e];
+    }
+    if (nan != 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (nan >> e & 1u) sh_mn[warp][ca + e] = sh_mx[warp][ca + e] = NAN;
+        if (nan >> e & 256u) sh_mn[warp][cb + e] = sh_mx[warp][cb + e] = NAN;
+      }
     }
   }
   __syncthreads();

@@ -84,6 +84,35 @@ def test_attention_leaves_out_a_sequence_longer_than_its_table(dtype, shares, pa
         assert (np.abs(f64(out[r]) - want[r]) <= tol[r]).all()
 
 
+# ------------------------------------------------------------------- keys that are not numbers
+
+@pytest.mark.parametrize("dtype,D,PS,many", [("bf16", 128, 16, False), ("bf16", 64, 64, False),
+                                             ("fp32", 128, 32, False), ("fp32", 64, 16, False),
+                                             ("bf16", 128, 64, True), ("bf16", 128, 16, True)])
+def test_statistics_of_keys_with_nan_equal_the_full_build_s(dtype, D, PS, many):
+    """A NaN in a page's first key stays, one in a later key does not count, and infinities are
+    extremes: in pages that begin with the call, resume a page or are filled one by one."""
+    new = (2500, 1700, 70) if many else (100, 70, 1)
+    c = Case(new, (0, 5, PS), dtype, D, 2, Hkv=2, PS=PS)
+    k = c.k                                                # a view into the fused rows
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").to(k.dtype)
+    pick = torch.randint(0, 12, k.shape, generator=gen, device="cuda")
+    for i in range(3):
+        k[pick == i] = bad[i]
+    k[:, :, 3] = float("nan")                              # a column without any number
+    k[:, 0, 5] = float("inf")
+    c.k_pool[c.table[1, 0].long(), :, 0, 7] = float("nan")  # held by a page before the call
+    stats = c.past_stats()
+    skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, cu_tokens=c.cu)
+    assert_no_device_error()
+    table = c.table.flatten().long()
+    used = table[table >= 0]
+    rebuilt = skv.kv_build_page_stats(c.kv)
+    np.testing.assert_array_equal(f64(stats[used]), f64(rebuilt[used]))
+    assert torch.isnan(stats[used]).any()
+
+
 # ---------------------------------------------------------------------- streams by argument
 
 def busy(stream):
