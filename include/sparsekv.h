@@ -205,7 +205,7 @@ kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * (j, j + rot_dim/2), or (2j, 2j+1) when interleaved is not 0:
  *   (a, b) -> (a cos x - b sin x, a sin x + b cos x),  x = pos * inv_freq[j],
  * with pos the token's cache position, or positions[row] if positions is not NULL (device
- * int32[total_tokens], any values); the angle is exact to 2^-31 of a turn at every position.
+ * int32[total_tokens], any values); the angle is exact to 2^-27 of a turn at every position.
  * Computed in float32, rounded once to the cache dtype. Columns from rot_dim on, and values,
  * are copied. rot_dim: a multiple of 16 up to head_dim (else KV_ERR_UNSUPPORTED), 0 for no
  * rotation (turns may then be NULL). turns: device uint64[rot_dim/2] of kv_rope_turns.

@@ -9,8 +9,9 @@
 // follow from the stored keys alone, as kv_append_token keeps them for one token.
 //
 // Angles: the frequency is held in turns as a 64-bit fraction, so pos * turns modulo 2^64 is
-// the fraction of a turn exactly, however far the position; only its leading 32 bits become a
-// float, for sincospif. A product in 32-bit floats would be off by 2^-24 of the whole angle
+// the fraction of a turn exactly, however far the position. Its leading 32 bits less the nearest
+// quarter turn become a float for sincospif, off by 2^-28 of a turn (2.3e-8 rad, below half a
+// step of the float sine). A product in 32-bit floats would be off by 2^-24 of the whole angle
 // (0.06 rad at position 10^6).
 //
 // Rounding: the rotation is done in float32 and rounded once to the cache's type; the
@@ -21,8 +22,8 @@
 // between lanes is needed and D/16 lanes cover a row; a warp moves 512/D rows at once. One
 // block per (page, KV head) lets the page's statistics be joined inside the block, without
 // atomics. Measured, bf16, D = 128: ragged prompts of 64/8 heads in pages of 64 tokens (545 MB)
-// 87 us, 6.2 TB/s, 92% of the measured copy rate; a prompt of 8192 tokens of 32/8 heads in pages
-// of 16 (203 MB) 39 us, 5.2 TB/s, as each of the small blocks pays for finding its page. 32
+// 88.6 us, 6.2 TB/s, 91% of the measured copy rate; a prompt of 8192 tokens of 32/8 heads in pages
+// of 16 (203 MB) 40.5 us, 5.0 TB/s, as each of the small blocks pays for finding its page. 32
 // single tokens take 5 us on the device, three dependent reads long; the call costs the host
 // 13 to 15. Bounds of four or five blocks per SM on the registers gave nothing.
 #include "packed_rows.cuh"
@@ -79,9 +80,15 @@ struct Angle { float cos[8], sin[8]; };
 __device__ __forceinline__ void angles_at(const uint64_t* f, int pos, Angle* x) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const uint64_t turn = f[e] * (uint64_t)(int64_t)pos;      // modulo one turn
-    const float half_turns = (float)(int32_t)(turn >> 32) * 0x1p-31f;
-    sincospif(half_turns, &x->sin[e], &x->cos[e]);
+    const uint32_t turn = (uint32_t)((f[e] * (uint64_t)(int64_t)pos) >> 32);   // modulo one turn
+    // the nearest quarter turn, and what is left of it: at most 2^29 of these units, so the
+    // float is off by 2^-28 of a turn (of the whole signed fraction it would be 2^-26)
+    const uint32_t quarter = (turn + (1u << 29)) >> 30;
+    float s, c;
+    sincospif((float)(int32_t)(turn - (quarter << 30)) * 0x1p-31f, &s, &c);
+    const float a = quarter & 1u ? s : c, b = quarter & 1u ? c : s;
+    x->cos[e] = __uint_as_float(__float_as_uint(a) ^ ((quarter + 1u) & 2u) << 30);
+    x->sin[e] = __uint_as_float(__float_as_uint(b) ^ (quarter & 2u) << 30);
   }
 }
 
@@ -194,7 +201,7 @@ append_rope_kernel(kv_cache_desc d, PackedRows pr, RopeArgs a, DevCtx ctx) {
   }
   // Columns of the page's first key that are NaN: the full build begins with that key, so they
   // stay NaN, where those of later keys do not count. (Beginning with the key here instead of
-  // with infinities costs 1 us of 39 and 87.)
+  // with infinities costs 0.9 us of 39 and 87, this mask 0.2.)
   uint32_t nan = 0;
   const int warps = blockDim.x >> 5;
   for (int t = t0 + warp * RPW + r; t < t1; t += warps * RPW) {

@@ -84,6 +84,32 @@ def test_attention_leaves_out_a_sequence_longer_than_its_table(dtype, shares, pa
         assert (np.abs(f64(out[r]) - want[r]) <= tol[r]).all()
 
 
+# ------------------------------------------------------------------------- angles, positions
+
+@pytest.mark.parametrize("packed", [True, False])
+def test_angles_are_right_to_the_header_s_bound(packed):
+    """Pairs (1, 0) become (cos, sin) of the angle, which is off by at most 2^-28 of a turn (the
+    float) and 2^-32 (the fraction's cut); sincospif adds a unit, 2^-23 of the value. (1, 0) makes
+    the products and the sum exact."""
+    T, D = 4096, 64
+    rng = np.random.default_rng(2)
+    pos = np.concatenate([np.arange(1024), rng.integers(-2 ** 31, 2 ** 31, T - 1024)])
+    c = Case((1,) * T if not packed else (T,), (0,) * (1 if packed else T), "fp32", D, 1, Hkv=1)
+    c.q.copy_((torch.arange(D, device="cuda") < D // 2).float().expand_as(c.q))
+    turns = skv.kv_rope_turns([10000.0 ** (-2.0 * i / D) for i in range(D // 2)], device="cuda")
+    stats = c.past_stats()
+    q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=c.cu if packed else None,
+                           positions=torch.tensor(pos, dtype=torch.int32, device="cuda"))
+    assert_no_device_error()
+    frac = np.array([[(t % 2 ** 64) * int(p) % 2 ** 64 / 2.0 ** 64 for t in turns.tolist()]
+                     for p in pos])
+    angle = 2 * np.pi * np.where(frac > 0.5, frac - 1, frac)
+    want = np.concatenate([np.cos(angle), np.sin(angle)], axis=1)
+    bound = 2 * np.pi * (2.0 ** -28 + 2.0 ** -32) + 2.0 ** -23 * np.abs(want)
+    err = np.abs(f64(q)[:, 0] - want)
+    assert (err <= bound).all(), (err / bound).max()
+
+
 # ------------------------------------------------------------------- keys that are not numbers
 
 @pytest.mark.parametrize("dtype,D,PS,many", [("bf16", 128, 16, False), ("bf16", 64, 64, False),
