@@ -242,7 +242,9 @@ kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_st
  * out: device [total_tokens][num_q_heads][head_dim] of the CACHE dtype (a prompt's rows feed
  * the next matrix product), 16-byte aligned, overlapping no input; lse: device
  * [total_tokens][num_q_heads] float32 (natural log) or NULL. Scores, softmax and sums are
- * float32; for bf16 caches the probabilities are rounded to bf16 before they meet the values.
+ * float32. For bf16 caches the probabilities are rounded before they meet the values: to 2^-17 of
+ * themselves where the batch has at most 32 rows (tokens times group heads) to a sequence on
+ * average and num_shares is not 1, and to bf16 otherwise.
  * Rows that belong to no sequence are left as they were; with cu_tokens = NULL the row of an
  * empty sequence gets out = 0 and lse = -inf. Cached tokens must be finite; what lies in a page
  * past its sequence's end has no influence. The same call gives the same bits (no atomics);

@@ -73,9 +73,10 @@ template <typename S> struct SeqItems {
   __device__ __forceinline__ int unit(int tile, int log_g) const {
     return (tokens(tile) << log_g) > S::narrow ? 2 : 1;
   }
-  // Cost of the first x tiles. All but the sequence's last tile are full: two units for each
+  // Cost of the first x tiles. All but the sequence's last tile are full: FULL units for each
   // of ceil((past + (j + 1) TQ) / KT) key tiles.
   __device__ __forceinline__ int64_t cost(int x, int log_g) const {
+    constexpr int FULL = S::rows > S::narrow ? 2 : 1;
     const int nt = tiles();
     int64_t c = (int64_t)kItemCost * x;
     if (x == nt && x > 0) {
@@ -85,14 +86,14 @@ template <typename S> struct SeqItems {
     const int a = len - n + S::keys - 1;            // sum of floor((a + j TQ) / KT), j = 1..x
     if ((1 << tq_log) >= S::keys) {
       const int64_t r = (1 << tq_log) / S::keys;
-      return c + 2 * (x * (int64_t)(a / S::keys) + r * ((int64_t)x * (x + 1) / 2));
+      return c + FULL * (x * (int64_t)(a / S::keys) + r * ((int64_t)x * (x + 1) / 2));
     }
     const int r_log = (__ffs(S::keys) - 1) - tq_log, r = 1 << r_log;
     const int rest = (a & (S::keys - 1)) >> tq_log;
     // floor((rest + j) / r) summed over j = 1..x; below r the terms are zero
     const int64_t y = (int64_t)rest + x + 1, q = y >> r_log;
     const int64_t steps = r * (q * (q - 1) / 2) + q * (y & (r - 1));
-    return c + 2 * (x * (int64_t)(a / S::keys) + steps);
+    return c + FULL * (x * (int64_t)(a / S::keys) + steps);
   }
 };
 
@@ -264,6 +265,7 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
 
 // Launchers.
 using MmaShape = TileShape<256, 128, 128>;       // bf16, tensor cores
+using FewShape = TileShape<128, 128, 128>;       // the same for batches of few rows
 using SimtShape = TileShape<128, 64, 0>;         // fp32, CUDA cores
 int prefill_tile_rows(int dtype);
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,

@@ -57,8 +57,18 @@
 // V tile are zeroed in shared memory (a zero probability times a NaN would not vanish).
 //
 // Rounding: P is rounded to bf16 for the second product (relative 2^-8 each, independent), as
-// the tensor core takes bf16 operands; its sum l is taken over the unrounded values.
+// the tensor core takes bf16 operands; its sum l is taken over the unrounded values. Batches of
+// few rows (FEW: at most 32 to a sequence) multiply V by P in two parts, its rounding and the
+// rounding of what that leaves, 2^-17 together: with one warp of each warpgroup at work the
+// tensor core idles, and the second part fits where S was, beside the first. Up to 32 rows that
+// costs under 1% (16 sequences over 4133 tokens, 4 to 32 rows: 62.5 to 62.8 us against 62.0 to
+// 62.3; one token over 32768: 37.2 against 36.4), from 64 rows on 8% and more (72.9 against 67.1;
+// 128 rows 76.9 against 71.9). The mean is what the host knows: 31 single tokens and a chunk of
+// 128, four heads to a group, have 20 rows to a sequence and pay 9% (125.7 us against 115.3).
+// It is an instance of its own, whose tiles have 128 rows: code for both in one kernel costs
+// prompts 5 to 12% and ragged batches 14 to 40%, in registers and instruction fetches.
 #include <atomic>
+#include <type_traits>
 
 #include "prefill.cuh"
 #include "tcgen05.cuh"
@@ -72,6 +82,7 @@ constexpr int kItems = 4;              // items known ahead
 constexpr int kKeys = MmaShape::keys;
 constexpr int kTmemCols = 512;
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;     // (2 * 216 + 72) * 128 = 384 * 168
+constexpr int kFewRows = 32;           // mean rows per sequence up to which P has two parts
 constexpr float kLazy = 8.f;           // log2 of the growth that forces a rescale
 
 template <int D> struct Cfg {
@@ -98,8 +109,8 @@ struct Plan {
   int n;          // key tiles of the item (or of the block's part of it)
   int n0, n1;     // key tiles of each warpgroup
 
-  __device__ __forceinline__ Plan(const PrefillItem& it, int log_g) {
-    wide = (it.n_tok << log_g) > 128;
+  __device__ __forceinline__ Plan(const PrefillItem& it, int log_g, bool few) {
+    wide = !few && (it.n_tok << log_g) > 128;
     n = it.kt1 - it.kt0;
     if (wide) {
       // the first tile's rows end earlier: its last keys may lie a tile before the item's
@@ -177,7 +188,7 @@ __device__ __forceinline__ void tma_store_rows(const CUtensorMap* map, const voi
 // from it, in uniform registers: the products' descriptors come from there.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v,
@@ -187,6 +198,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ PackedRows pr, const __grid_constant__ PrefillArgs a,
                    const __grid_constant__ DevCtx ctx) {
   using C = Cfg<D>;
+  using Shape = typename std::conditional<FEW, FewShape, MmaShape>::type;
   extern __shared__ uint8_t smem_raw[];
   __shared__ LineScratch scratch;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -239,13 +251,13 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   pdl_trigger();
   pdl_wait();
   finish_empty<bf16_t, D>(ctx, d, pr, a);
-  const LinePlace at = find_place<MmaShape>(ctx, d, pr, a, blockIdx.x, &scratch);
+  const LinePlace at = find_place<Shape>(ctx, d, pr, a, blockIdx.x, &scratch);
   const int64_t lo = at.lo, hi = at.hi;
   if (at.total == 0 || lo >= hi) {                 // nothing, or less than a unit of the line
     if (tid == 0 && a.notes != nullptr)
       a.notes[blockIdx.x] =
           at.total == 0 ? BorderNote{0, 0, 0, 0, 0, 0}
-                        : ItemWalk<MmaShape>(d, pr, a, ctx, lo, hi, at.b, at.before, 0).border();
+                        : ItemWalk<Shape>(d, pr, a, ctx, lo, hi, at.b, at.before, 0).border();
     return;
   }
   if (warp == kMmaWarp) tc::alloc(tmem_slot, kTmemCols);
@@ -281,7 +293,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       {
         const PrefillItem it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
-        const Plan plan(it, log_g);
+        const Plan plan(it, log_g, FEW);
         n = plan.tiles(w);
         row = plan.wide ? w * 128 + r : r;
         idle = row - lane >= it.n_tok << log_g;                   // no row in this warp
@@ -351,16 +363,29 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           const float ref = m == -INFINITY ? 0.f : m;             // no key of this row yet
           ref2 = make_float2(-ref, -ref);
         }
-        uint32_t p[64];
-        auto exps = [&](int first, int last) {                    // P of keys [first, last)
+        constexpr int STEP = FEW ? 16 : 32;
+        uint32_t p[64 / 32 * STEP], low[STEP];
+        auto exps = [&](int first) {                              // P of 64 keys from `first` on
 #pragma unroll
-          for (int e = first / 2; e < last / 2; ++e) {
-            float2 x = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-            x = tc::fma2(x, scale2, ref2);
-            x.x = tc::exp2_approx(x.x);
-            x.y = tc::exp2_approx(x.y);
-            sum[e & 1] = tc::add2(sum[e & 1], x);
-            p[e] = tc::pack_bf16(x.x, x.y);
+          for (int c = first / 2; c < first / 2 + 32; c += STEP) {
+            uint32_t* high = p + c % (64 / 32 * STEP);
+#pragma unroll
+            for (int e = 0; e < STEP; ++e) {
+              const int k = 2 * (c + e);
+              float2 x = make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+              x = tc::fma2(x, scale2, ref2);
+              x.x = tc::exp2_approx(x.x);
+              x.y = tc::exp2_approx(x.y);
+              sum[e & 1] = tc::add2(sum[e & 1], x);
+              high[e] = tc::pack_bf16(x.x, x.y);
+              if (FEW) low[e] = tc::pack_bf16(x.x - bf16_lo(high[e]), x.y - bf16_hi(high[e]));
+            }
+            if constexpr (FEW) {
+              tc::st16(ts + c, high);
+              tc::st16(ts + 64 + c, low);
+            } else {
+              tc::st32(ts + c, high);
+            }
           }
         };
         auto hand_over = [&](uint64_t* to_whom) {
@@ -369,15 +394,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           __syncwarp();
           if (lane == 0) arrive(to_whom + w);
         };
-        if (!idle) {
-          exps(0, 64);
-          tc::st32(ts, p);
-        }
+        if (!idle) exps(0);
         hand_over(p_half);
-        if (!idle) {
-          exps(64, 128);
-          tc::st32(ts + 32, p + 32);
-        }
+        if (!idle) exps(64);
         hand_over(p_full);
         sum[0] = tc::add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
@@ -385,7 +404,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok) break;
       // ---- output
       const PrefillItem it = items[j % kItems];
-      const Plan plan(it, log_g);
+      const Plan plan(it, log_g, FEW);
       const int rows = it.n_tok << log_g, warp_row = row - lane;
       const bool join = !plan.wide && plan.n1 > 0;
       if (n > 0) ok = wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
@@ -519,8 +538,8 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   } else {
     tc::fewer_regs<kRegsOther>();
     auto uniform_plan = [&](int j) {
-      Plan plan(items[j % kItems], log_g);
-      plan.wide = uniform(plan.wide);
+      Plan plan(items[j % kItems], log_g, FEW);
+      if (!FEW) plan.wide = uniform(plan.wide);
       plan.n = uniform(plan.n);
       plan.n0 = uniform(plan.n0);
       plan.n1 = uniform(plan.n1);
@@ -560,6 +579,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         if (last) tc::commit(q_free + w);
         if (done) tc::commit(empty + stage);
       };
+      constexpr int kUnroll = FEW ? 1 : 2;
       bool early = false;          // this item's first scores were issued with the last's end
       ok = item_ready(0);
       Plan plan = uniform_plan(0), next = plan;
@@ -590,7 +610,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             early = runs_on(plan, next);
           }
           // written out for both warpgroups: as a loop it costs a long prompt 4%
-#pragma unroll
+#pragma unroll kUnroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || i >= plan.tiles(w)) continue;
             const int slot = base + plan.v_slot(plan.tile(w, i));
@@ -606,6 +626,12 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
               for (int k = 4 * h; k < 4 * h + 4; ++k)
                 tc::mma_ts(tmem + C::COL_O + w * D, tmem + C::COL_S + w * 128 + k * 8,
                            vd + k * (2048 >> 4), id, i > 0 || k > 0);
+              if constexpr (FEW) {
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k)          // what P's rounding left
+                  tc::mma_ts(tmem + C::COL_O + w * D, tmem + C::COL_S + w * 128 + 64 + k * 8,
+                             vd + k * (2048 >> 4), id, 1);
+              }
             };
             wait(p_half + w, tiles & 1);
             if (!ok) continue;
@@ -712,7 +738,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         const PrefillItem it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
         item_done(j);
-        const Plan plan(it, log_g);
+        const Plan plan(it, log_g, FEW);
         const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
         const int keys = it.pos0 + it.n_tok;         // keys from here on are nobody's
         const int pages = (int)(((int64_t)keys + PS - 1) / PS);
@@ -795,7 +821,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       // tiles; a warpgroup's rows are loaded as soon as the item before is done with them
       // Its waits are for work, not for copies: an item takes as long as it has keys (11 ms over
       // 2^20), so the limit counts per key tile of the items not known to be done.
-      ItemWalk<MmaShape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
+      ItemWalk<Shape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
       if (lane == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
       bool ok = true;
       int loaded[2] = {0, 0};
@@ -824,7 +850,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         it = next;
         publish(j + 1);
         if (!ok) break;
-        const Plan plan(it, log_g);
+        const Plan plan(it, log_g, FEW);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || plan.tiles(w) == 0) continue;
@@ -855,7 +881,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   if (warp == kMmaWarp) tc::dealloc(tmem, kTmemCols);
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const PrefillArgs& a,
                      DevCtx ctx, cudaStream_t s) {
   using C = Cfg<D>;
@@ -864,7 +890,7 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
       !rows_tensor_map(&mq, a.q, a.q_stride, a.Hq, D, pr.total, a.G, 128 / a.G) ||
       !rows_tensor_map(&mo, a.out, (int64_t)a.Hq * D, a.Hq, D, pr.total, a.G, 32 / a.G))
     return cudaErrorInvalidValue;
-  auto kern = prefill_mma_kernel<D>;
+  auto kern = prefill_mma_kernel<D, FEW>;
   // set once per device; setting it twice from two threads is harmless
   static std::atomic<int> ready[64];
   int dev = 0;
@@ -882,7 +908,13 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
 
 cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
-  return d.head_dim == 128 ? launch_t<128>(d, pr, a, ctx, s) : launch_t<64>(d, pr, a, ctx, s);
+  // one share promises a row the same bits whatever the batch, so the batch chooses nothing there
+  const bool few = a.NC > 1 && (int64_t)pr.total * a.G <= (int64_t)kFewRows * d.batch;
+  if (few)
+    return d.head_dim == 128 ? launch_t<128, true>(d, pr, a, ctx, s)
+                             : launch_t<64, true>(d, pr, a, ctx, s);
+  return d.head_dim == 128 ? launch_t<128, false>(d, pr, a, ctx, s)
+                           : launch_t<64, false>(d, pr, a, ctx, s);
 }
 
 }  // namespace skv

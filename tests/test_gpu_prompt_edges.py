@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import sparse_kv_cache_build_gb300 as skv
+from oracle import prompt
 from sparse_kv_cache_build_gb300 import binding
 
 from gpu_helpers import assert_no_device_error, f64, need_gpu
@@ -108,6 +109,58 @@ def test_angles_are_right_to_the_header_s_bound(packed):
     bound = 2 * np.pi * (2.0 ** -28 + 2.0 ** -32) + 2.0 ** -23 * np.abs(want)
     err = np.abs(f64(q)[:, 0] - want)
     assert (err <= bound).all(), (err / bound).max()
+
+
+# ------------------------------------------------------------------------ few rows, exactly
+
+@pytest.mark.parametrize("new,past,D,G,PS,shares", [
+    ((1,), (2047,), 128, 4, 16, 0),
+    ((1, 1, 1, 1, 1, 1), (0, 1, 127, 128, 300, 1200), 128, 8, 16, 2),
+    ((5, 5, 5), (63, 1500, 700), 64, 1, 16, 7),
+    ((4, 4, 4), (63, 1500, 700), 128, 8, 64, 0),
+    ((32, 31), (0, 900), 128, 1, 32, 40),
+    ((8, 7), (0, 500), 64, 4, 64, 3),
+    ((200,) + (1,) * 31, (100,) + (500,) * 31, 128, 4, 16, 0),
+    ((301,) + (1,) * 31, (0,) + (300,) * 31, 64, 2, 32, 5),
+    ((130, 0, 0, 2, 0), (0, 50, 0, 126, 0), 128, 1, 16, 0),
+])
+def test_few_rows_take_p_to_2_17(new, past, D, G, PS, shares):
+    """A batch of at most 32 rows (tokens times group heads) to a sequence multiplies the values
+    with P in two parts. A probability in [2^e, 2^(e+1)) is first off by at most 2^(e-8); what that
+    leaves lies below that power, so its own half step is 2^(e-17) at most: 2^-17 together. Otherwise the bounds of the prompt attention: the row's own and
+    the sum's logits, the exponential, sums over the keys, and the output's rounding."""
+    c = Case(new, past, "bf16", D, G, PS=PS)
+    assert sum(new) * G <= 32 * len(new) and shares != 1
+    c.q.mul_(1.5)
+    out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu, num_shares=shares)
+    assert_no_device_error()
+    ref, ref_lse, mass, logit = prompt.prefill(f64(c.q), f64(c.k_pool), f64(c.v_pool),
+                                               c.table.cpu().numpy(), c.lens, c.cu_h, PS, c.scale)
+    rel = 2 * D * 2.0 ** -23 * logit + 2.0 ** -21 + max(c.lens) * 2.0 ** -23
+    tol = (rel + 2.0 ** -17)[..., None] * mass * 1.01 + 2.0 ** -8 * np.abs(ref) * 1.01 + 1e-30
+    err = np.abs(f64(out) - ref)
+    assert (err <= tol).all(), (err / tol).max()
+    assert (np.abs(f64(lse) - ref_lse) <= rel + 2.0 ** -23 * np.abs(ref_lse)).all()
+
+
+def test_with_one_share_the_bits_do_not_depend_on_the_batch():
+    """num_shares = 1 cuts no row's keys, and the batch's mean of rows chooses nothing there: a
+    sequence alone, among single tokens and beside a prompt gives the same bits."""
+    c = Case((1, 1, 500, 2), (900, 77, 30, 1300), "bf16", 128, 4)
+    out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, cu_tokens=c.cu, num_shares=1)
+    for pick in ([0], [1], [3], [0, 1], [0, 3], [2]):
+        rows = torch.cat([torch.arange(int(c.cu_h[b]), int(c.cu_h[b + 1])) for b in pick]).cuda()
+        kv = skv.PagedKV(c.k_pool, c.v_pool, c.table[pick].contiguous(),
+                         c.seq_lens[pick].contiguous())
+        cu = torch.tensor(np.concatenate([[0], np.cumsum([c.new[b] for b in pick])]),
+                          dtype=torch.int32, device="cuda")
+        got, got_lse = skv.kv_prefill_attn(kv, c.q[rows].contiguous(), c.scale, cu_tokens=cu,
+                                           num_shares=1)
+        assert torch.equal(got, out[rows]) and torch.equal(got_lse, lse[rows])
+        if all(c.new[b] == 1 for b in pick):
+            got, got_lse = skv.kv_prefill_attn(kv, c.q[rows].contiguous(), c.scale, num_shares=1)
+            assert torch.equal(got, out[rows]) and torch.equal(got_lse, lse[rows])
+    assert_no_device_error()
 
 
 # ------------------------------------------------------------------- keys that are not numbers
