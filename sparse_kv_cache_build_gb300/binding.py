@@ -409,7 +409,8 @@ def kv_append_rope(kv: PagedKV, q, k_new, v_new, stats, turns=None, cu_tokens=No
         status = lib().kv_append_rope(
             kv.ref(), q.data_ptr(), qs, Hq, k_new.data_ptr(), ks, v_new.data_ptr(), vs, cu, T,
             None if positions is None else positions.data_ptr(),
-            None if turns is None else turns.data_ptr(), rot, interleaved, q_out.data_ptr(), os_,
+            None if turns is None else turns.data_ptr(), rot, int(bool(interleaved)),
+            q_out.data_ptr(), os_,
             stats.data_ptr(), _raw_stream(kv, stream))
         if status != KV_OK:
             raise KVError("kv_append_rope", status)
@@ -444,7 +445,7 @@ def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares:
     elif workspace.get_device() != kv.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {kv.k_pool.device}")
     status = lib().kv_prefill_attn(
-        kv.ref(), q.data_ptr(), qs, Hq, cu, T, sm_scale, num_shares, out.data_ptr(),
+        kv.ref(), q.data_ptr(), qs, Hq, cu, T, float(sm_scale), int(num_shares), out.data_ptr(),
         lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _raw_stream(kv, stream))
     if status != KV_OK:

@@ -85,6 +85,26 @@ def test_attention_leaves_out_a_sequence_longer_than_its_table(dtype, shares, pa
         assert (np.abs(f64(out[r]) - want[r]) <= tol[r]).all()
 
 
+# ------------------------------------------------------------------- arguments as users have them
+
+def test_scalars_of_other_kinds():
+    """numpy's numbers and one-element tensors, as the older calls take them."""
+    c = Case((7, 1), (20, 40), "bf16", 128, 4)
+    turns = skv.kv_rope_turns([0.5] * 64, device="cuda")
+    stats = c.past_stats()
+    q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=c.cu, interleaved=True)
+    ref = skv.kv_prefill_attn(c.kv, q, 0.125, cu_tokens=c.cu, num_shares=3)
+    for yes in (np.bool_(True), torch.tensor(True), 2):
+        got = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=c.cu,
+                                 interleaved=yes)
+        assert torch.equal(got, q)
+    for scale, shares in ((np.float32(0.125), np.int64(3)), (torch.tensor(0.125), np.int32(3)),
+                          (np.float64(0.125), torch.tensor(3))):
+        got = skv.kv_prefill_attn(c.kv, q, scale, cu_tokens=c.cu, num_shares=shares)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert_no_device_error()
+
+
 # ------------------------------------------------------------------------- angles, positions
 
 @pytest.mark.parametrize("packed", [True, False])
