@@ -10,7 +10,7 @@ from oracle import prompt
 from sparse_kv_cache_build_gb300 import binding
 
 from gpu_helpers import assert_no_device_error, f64, need_gpu
-from test_gpu_prompt import Case
+from test_gpu_prompt import Case, check_append, freqs, pages_of
 
 pytestmark = pytest.mark.gpu
 
@@ -181,6 +181,62 @@ def test_with_one_share_the_bits_do_not_depend_on_the_batch():
             got, got_lse = skv.kv_prefill_attn(kv, c.q[rows].contiguous(), c.scale, num_shares=1)
             assert torch.equal(got, out[rows]) and torch.equal(got_lse, lse[rows])
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("dtype,D,G,PS,rot,inter", [
+    ("bf16", 128, 4, 16, 64, False), ("bf16", 128, 1, 32, 16, True), ("bf16", 64, 8, 64, 48, True),
+    ("fp32", 128, 2, 16, 96, False), ("fp32", 64, 4, 32, 32, True),
+])
+@pytest.mark.parametrize("given", [True, False])
+def test_one_token_with_part_of_the_head_rotated(dtype, D, G, PS, rot, inter, given):
+    """The single-token form with fewer rotated columns than the head has, by the cache's
+    positions and by positions given: the first past 2^31 in magnitude, negative and repeated."""
+    past = (0, 15, 16, 31, 100, 63)
+    c = Case((1,) * len(past), past, dtype, D, G, PS=PS)
+    pos = np.array([2 ** 31 - 1, -2 ** 31, -7, 12345, 12345, 0])
+    stats = c.past_stats()
+    before = (c.k_pool.clone(), c.v_pool.clone(), None)
+    c.q_in = c.q.clone()
+    turns = skv.kv_rope_turns(freqs(rot), device="cuda")
+    where = torch.tensor(pos, dtype=torch.int32, device="cuda") if given else None
+    q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, interleaved=inter, positions=where)
+    assert_no_device_error()
+    check_append(c, q, stats, before, rot, inter, pos_of_row=pos if given else None)
+    mapped = pages_of(c, c.lens)
+    rebuilt = skv.kv_build_page_stats(c.kv)
+    np.testing.assert_array_equal(f64(stats)[mapped], f64(rebuilt)[mapped])
+
+
+@pytest.mark.parametrize("new", [(20, 1, 300), (1, 1, 1)])
+def test_append_statistics_past_32_bit_offsets(new):
+    """Statistics of more than 2^31 elements: those of the last pages are joined with what was
+    there and equal the same call's on a small cache; the first pages stay as they were."""
+    packed = new[0] > 1
+    c = Case(new, (5, 16, 40), "bf16", 128, 4, Hkv=2, PS=16, extra=0)
+    need = c.k_pool.shape[0]
+    NP = 2 ** 31 // (2 * 2 * 128) + need + 8
+    if torch.cuda.mem_get_info()[0] < 90 * 2 ** 30:
+        pytest.skip("needs 74 GB of device memory")
+    turns = skv.kv_rope_turns(freqs(128), device="cuda")
+    stats = c.past_stats()
+    k = torch.empty((NP, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    far = torch.empty((NP, 2, 2, 128), dtype=torch.bfloat16, device="cuda")
+    for big, small in ((k, c.k_pool), (v, c.v_pool), (far, stats)):
+        big[-need:] = small
+        big[:64] = 3.0
+    table = torch.where(c.table >= 0, c.table + (NP - need), c.table).to(torch.int32)
+    cu = c.cu if packed else None
+    q_far = skv.kv_append_rope(skv.PagedKV(k, v, table, c.seq_lens), c.q, c.k, c.v, far, turns,
+                               cu_tokens=cu)
+    q = skv.kv_append_rope(c.kv, c.q, c.k, c.v, stats, turns, cu_tokens=cu)
+    assert_no_device_error()
+    assert torch.equal(q_far, q)
+    used = pages_of(c, c.lens)
+    for big, small in ((k, c.k_pool), (v, c.v_pool), (far, stats)):
+        assert torch.equal(big[-need:][used], small[used])
+        assert (big[:64] == 3.0).all()
+    np.testing.assert_array_equal(f64(stats[used]), f64(skv.kv_build_page_stats(c.kv)[used]))
 
 
 # ------------------------------------------------------------------- keys that are not numbers
