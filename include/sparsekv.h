@@ -40,9 +40,10 @@
  *     KV_ERR_MISALIGNED and launch nothing. A failed launch returns KV_ERR_CUDA.
  *   - Device-detected faults in the DATA (a page-table entry outside [0, num_phys_pages),
  *     a sequence longer than its page-table row, a selected index outside the sequence,
- *     packed-row offsets out of order, a keep count above k_max, an asynchronous copy that did not land in time) never
- *     trap: the kernel skips the bad access, records a flag in a per-device error word
- *     and finishes. kv_check_device_errors() reports and clears that word.
+ *     packed-row offsets out of order, a keep count above k_max, an asynchronous copy that
+ *     did not land in time) never trap: the kernel skips the bad access, records a flag in a
+ *     per-device error word and finishes. kv_check_device_errors() reports and clears that
+ *     word.
  *   - Supported shapes: head_dim 64 or 128; page_size 16, 32 or 64; group size
  *     G = num_q_heads / num_kv_heads in {1, 2, 4, 8}; dtype bf16 or fp32. Anything else
  *     returns KV_ERR_UNSUPPORTED.
@@ -172,7 +173,8 @@ kv_status kv_build_page_stats_fp8(const kv_cache_desc* cache, void* stats_fp8,
  * k_new[b][g][:], v_new[b][g][:] are written to k_pool and v_pool (the descriptor's pool
  * pointers are written through), and the page's statistics become the element-wise min/max
  * of the old ones and the key (a page's first token, slot 0, resets them to the key). The
- * result equals kv_build_page_stats of the grown cache bit for bit.
+ * result equals kv_build_page_stats of the grown cache bit for bit. FP8 statistics are not
+ * kept: kv_build_page_stats_fp8 makes them anew.
  * k_new, v_new: device [batch][num_kv_heads][head_dim] of the cache dtype.
  * stats: device [num_phys_pages][num_kv_heads][2][head_dim] of the cache dtype.
  */
@@ -213,17 +215,19 @@ kv_status kv_rope_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * allowed), keys to k_pool and values to v_pool (written through the descriptor's pointers).
  * Statistics of every page written: the element-wise min/max of the old ones (when the page
  * held tokens of the sequence before) and the new keys as stored, equal to
- * kv_build_page_stats of the grown cache.
+ * kv_build_page_stats of the grown cache (a NaN in a page's first key stays, in a later one it
+ * does not count). FP8 statistics are not kept: kv_build_page_stats_fp8 makes them anew.
  * q [total_tokens][num_q_heads][head_dim], k_new, v_new [total_tokens][num_kv_heads][head_dim]
  * in the cache dtype, head_dim innermost and contiguous, heads side by side, and *_stride
  * elements from one token to the next (so the three may be column ranges of one fused
  * projection): at least heads * head_dim, a multiple of 16 bytes; all bases 16-byte aligned
  * (KV_ERR_MISALIGNED). A page that two sequences of the batch share must not be written by
- * both. Rows that belong to no sequence are left alone. A sequence shorter than its new tokens or
- * longer than its page-table row (KV_DEVERR_BAD_LEN: it is left out), bad offsets (KV_DEVERR_BAD_LEN: which other sequences
- * are then left out is unspecified) and an unmapped page (KV_DEVERR_BAD_PAGE: its keys and
- * values are left out) are flagged on the device. KV_ERR_UNSUPPORTED for page-table rows of
- * 2^31 - 256 tokens (page_table_stride * page_size) or more.
+ * both. Rows that belong to no sequence are left alone. A sequence shorter than its new tokens
+ * or longer than its page-table row (KV_DEVERR_BAD_LEN: it is left out), bad offsets
+ * (KV_DEVERR_BAD_LEN: which other sequences are then left out is unspecified) and an unmapped
+ * page (KV_DEVERR_BAD_PAGE: its keys and values are left out) are flagged on the device.
+ * KV_ERR_UNSUPPORTED for page-table rows of 2^31 - 256 tokens (page_table_stride * page_size)
+ * or more.
  */
 kv_status kv_append_rope(const kv_cache_desc* cache, const void* q, int64_t q_stride,
                          int32_t num_q_heads, const void* k_new, int64_t k_stride,
@@ -660,8 +664,9 @@ kv_status kv_entmax_decode_step(const kv_cache_desc* cache, const void* q, int32
  * kv_entmax_attn_workspace_size(cache, num_q_heads, k_max as sel_stride, 0 = every page);
  * KV_OP_ENTMAX_DECODE_STEP: kv_entmax_decode_step_workspace_size(cache, num_q_heads,
  * k_max); KV_OP_PREFILL_ATTN: kv_prefill_attn_workspace_size(cache, num_q_heads, k_max as
- * total_tokens, num_splits as num_shares)). Arguments a given op does not use are ignored. Every other call of this library
- * takes no workspace. Returns 0 for an unknown op or a bad argument.
+ * total_tokens, num_splits as num_shares)). Arguments a given op does not use are ignored.
+ * Every other call of this library takes no workspace. Returns 0 for an unknown op or a bad
+ * argument.
  */
 typedef enum {
   KV_OP_DECODE_STEP = 0,

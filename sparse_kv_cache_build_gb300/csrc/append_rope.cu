@@ -22,8 +22,8 @@
 // between lanes is needed and D/16 lanes cover a row; a warp moves 512/D rows at once. One
 // block per (page, KV head) lets the page's statistics be joined inside the block, without
 // atomics. Measured, bf16, D = 128: ragged prompts of 64/8 heads in pages of 64 tokens (545 MB)
-// 88.6 us, 6.2 TB/s, 91% of the measured copy rate; a prompt of 8192 tokens of 32/8 heads in pages
-// of 16 (203 MB) 40.5 us, 5.0 TB/s, as each of the small blocks pays for finding its page. 32
+// 88.2 us, 6.2 TB/s, 91% of the measured copy rate; a prompt of 8192 tokens of 32/8 heads in pages
+// of 16 (203 MB) 40.2 us, 5.0 TB/s, as each of the small blocks pays for finding its page. 32
 // single tokens take 5 us on the device, three dependent reads long; the call costs the host
 // 13 to 15. Bounds of four or five blocks per SM on the registers gave nothing.
 #include "packed_rows.cuh"

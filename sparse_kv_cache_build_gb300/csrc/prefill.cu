@@ -11,8 +11,8 @@ constexpr int kMergeUnits = 4;           // (row, strip) units per warp at most
 
 // V consecutive floats, read as one word.
 template <int V> union Strip {
-  using Raw = typename std::conditional<V == 4, float4,
-                                        typename std::conditional<V == 2, float2, float>::type>::type;
+  using Few = typename std::conditional<V == 2, float2, float>::type;
+  using Raw = typename std::conditional<V == 4, float4, Few>::type;
   Raw raw;
   float f[V];
   __device__ __forceinline__ Strip() {}
@@ -81,7 +81,8 @@ prefill_merge_kernel(const __grid_constant__ PrefillArgs a) {
         for (int e = 0; e < BATCH; ++e) {
           const int64_t from = __shfl_sync(0xffffffffu, mine, (e0 + e) & 31);
           if (e0 + e < parts)
-            v[e].raw = __ldcg(reinterpret_cast<const typename Strip<V>::Raw*>(a.part_acc + from * D + col));
+            v[e].raw = __ldcg(reinterpret_cast<const typename Strip<V>::Raw*>(
+                a.part_acc + from * D + col));
         }
         if (e0 == 0) {
           float now = fmaxf(M, m);

@@ -15,9 +15,15 @@
 // Measured: 4096 tokens of 8 query over 2 KV heads, D = 64: 491 us, 35 TFLOP/s (the causal
 // multiply-adds alone would take 230 at one per lane and clock). Reads of shared memory keep
 // their pipe 70% busy and the multiply-adds theirs 55%; 512 threads with 8 x 2 scores each, for
-// more warps to hide the one under the other, took 515. Tensor cores would need six bf16
-// products (or three tf32 ones, and twice the shared memory there is at D = 128) for each
-// float32 product to keep its precision.
+// more warps to hide the one under the other, took 515. Tensor cores would take six bf16
+// products for each float32 product to keep its precision: 53 us of them for that call at the
+// measured rate of the library product, so it is not the arithmetic that speaks against them; such
+// a kernel has not been built.
+//
+// Every item computes 128 rows, however few it has, so single tokens cost as much as rows for 128:
+// 16 single tokens over 4096 each take 131 us at 8/2 heads of 64 and 846 at 32/8 heads of 128
+// (the bytes: 10 and 79), one over 32768 422 (40). kv_decode_step reads them at 18, 99 and 46, and
+// is the call for float32 caches there; a form for few rows has not been built.
 #include "prefill.cuh"
 #include "tcgen05.cuh"
 
@@ -192,7 +198,8 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
         float4 p[RPT];
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
-          p[i] = *reinterpret_cast<const float4*>(sp + (ty * RPT + i) * KT + ((u + turn) & (KT - 1)));
+          p[i] = *reinterpret_cast<const float4*>(sp + (ty * RPT + i) * KT +
+                                                  ((u + turn) & (KT - 1)));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float4 v[NC];

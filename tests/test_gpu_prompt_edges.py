@@ -147,8 +147,9 @@ def test_angles_are_right_to_the_header_s_bound(packed):
 def test_few_rows_take_p_to_2_17(new, past, D, G, PS, shares):
     """A batch of at most 32 rows (tokens times group heads) to a sequence multiplies the values
     with P in two parts. A probability in [2^e, 2^(e+1)) is first off by at most 2^(e-8); what that
-    leaves lies below that power, so its own half step is 2^(e-17) at most: 2^-17 together. Otherwise the bounds of the prompt attention: the row's own and
-    the sum's logits, the exponential, sums over the keys, and the output's rounding."""
+    leaves lies below that power, so its own half step is 2^(e-17) at most: 2^-17 together.
+    Otherwise the bounds of the prompt attention: the row's own and the sum's logits, the
+    exponential, sums over the keys, and the output's rounding."""
     c = Case(new, past, "bf16", D, G, PS=PS)
     assert sum(new) * G <= 32 * len(new) and shares != 1
     c.q.mul_(1.5)

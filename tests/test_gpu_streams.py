@@ -84,7 +84,8 @@ def written(x, name, outs):
             keep.append(t[mapped])
         elif t.dim() == 3 and t.dtype == torch.int32:          # lists: up to their counts
             cnt = next(c for c in outs if c.dim() == 2 and c.dtype == torch.int32).tolist()
-            keep.append(torch.cat([t[b, g, :n] for b, r in enumerate(cnt) for g, n in enumerate(r)]))
+            keep.append(torch.cat([t[b, g, :n] for b, row in enumerate(cnt)
+                                   for g, n in enumerate(row)]))
         elif t.dim() == 3:                                     # a value per page
             keep.append(torch.cat([t[b, :, :n].flatten() for b, n in enumerate(pages)]))
         else:
