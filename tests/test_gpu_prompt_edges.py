@@ -323,10 +323,10 @@ def test_append_on_a_stream_given_by_argument():
 
 # ------------------------------------------------------------------ waits that run out
 
-def long_items(D, tokens):
+def long_items(D, tokens, Hkv=2):
     """One row per sequence over a table that names the same few pages again and again: the KV
     heads are items of tokens / 128 key tiles each, one after the other with num_shares = 1."""
-    c = Case((1,), (200,), "bf16", D, 4, PS=64)
+    c = Case((1,), (200,), "bf16", D, 4, Hkv=Hkv, PS=64)
     table = c.table[0, torch.arange(tokens // 64, device="cuda") % 3].view(1, -1).contiguous()
     lens = torch.tensor([tokens], dtype=torch.int32, device="cuda")
     c.kv = skv.PagedKV(c.k_pool, c.v_pool, table, lens)
@@ -348,6 +348,24 @@ def test_waits_that_run_out_are_flagged_and_end_the_call(wait_limit, D):
         out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, num_shares=1)
         assert_no_device_error()
         assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+def test_waits_of_few_rows_that_run_out_are_flagged_too(wait_limit, D):
+    """The same where P has two parts: two shares of eight KV heads, several items to a block."""
+    c = long_items(D, 1 << 22, Hkv=8)
+    ref, ref_lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, num_shares=2)
+    assert_no_device_error()
+    for limit, want in ((0, (-6, 16)), (50_000, (0, 0)), (0, (-6, 16))):
+        wait_limit(limit)
+        out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, num_shares=2)
+        wait_limit(2_000_000_000)
+        assert skv.kv_check_device_errors() == want
+        if want == (0, 0):
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    out, lse = skv.kv_prefill_attn(c.kv, c.q, c.scale, num_shares=2)
+    assert_no_device_error()
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
 
 
 @pytest.mark.parametrize("D", [128, 64])
