@@ -353,7 +353,7 @@ split_attn_kernel(kv_cache_desc d, const T* __restrict__ q, float qk_scale_log2,
       flag(ctx, KV_DEVERR_TIMEOUT);
       // let every copy this CTA issued land before the CTA (and its smem) goes away
       for (int u = t; u < n_tiles && u < t + C::NSTAGE; ++u)
-        mbar_wait_bounded(&bars[u % C::NSTAGE], (uint32_t)((u / C::NSTAGE) & 1), ctx.wait_ns);
+        mbar_wait_bounded(&bars[u % C::NSTAGE], (uint32_t)((u / C::NSTAGE) & 1), kDrainNs);
     }
     for (int i = tid; i < G * D; i += C::THREADS) {
       const int hl = i / D, dd = i % D;

@@ -317,7 +317,7 @@ __device__ bool attend_run(const CUtensorMap* tmK, const CUtensorMap* tmV, char*
     // let every copy this CTA issued land before its shared memory is reused or freed
     for (int v = t; v < n_tiles && v < t + NST; ++v) {
       const uint32_t u = ring_base + (uint32_t)v;
-      mbar_wait_bounded(&bars[u % NST], (u / NST) & 1u, wait_ns);
+      mbar_wait_bounded(&bars[u % NST], (u / NST) & 1u, kDrainNs);
     }
   }
   return !aborted;

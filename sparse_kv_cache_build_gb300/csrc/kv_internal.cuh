@@ -119,6 +119,10 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   return true;
 }
 
+// Copies (and products) in flight end by themselves, within microseconds; a block that gave up
+// must outlive them whatever limit the caller set for its waits.
+constexpr unsigned long long kDrainNs = 4000000000ull;
+
 // One bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) from global
 // memory into this CTA's shared memory; completion is counted on `bar`.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,

@@ -165,9 +165,6 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity,
   }
   return __all_sync(0xffffffffu, ok);
 }
-// Products and copies in flight end by themselves, within microseconds; the block must outlive
-// them whatever limit the caller set for its waits.
-constexpr unsigned long long kDrainNs = 4000000000ull;
 // 64 columns of a tile's rows: G heads of 128 / G tokens of the query tensor [T][Hq][D].
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head,
                                          int token, uint64_t* bar) {
