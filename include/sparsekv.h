@@ -15,6 +15,8 @@
  *
  *   kv_append_rope         packed new tokens: rotary position, cache write, page statistics
  *   kv_prefill_attn        causal attention of packed query rows over the cache
+ *   kv_window_attn         the same within a sliding window and the first tokens
+ *   kv_tree_attn           the same for drafted tokens that form a tree
  *
  * Sources, by page title and section:
  *   [ENTMAX]  "EntmaxKV: Support-Aware Decoding for Entmax Attention", abstract: pages are
@@ -271,6 +273,43 @@ kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_s
                           int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
                           float sm_scale, int32_t num_shares, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * kv_window_attn -- kv_prefill_attn with a sliding window and sinks: prompts, chunks and single
+ * tokens of a model, or a stream, that looks back over `window` tokens. The row at position pos
+ * sees the tokens u <= pos of its sequence with
+ *   u > pos - window (itself and the window - 1 before it), or u < sinks (the first ones).
+ * window >= 1, sinks >= 0 (KV_ERR_INVALID_ARG). Arguments, workspace
+ * (kv_prefill_attn_workspace_size), rounding, flags and limits are otherwise kv_prefill_attn's;
+ * a window that reaches the first token gives its results up to the rounding of its sums.
+ * Pages that none of a sequence's rows see are not read and may be unmapped: those with
+ * (p + 1) * page_size <= pos_first - window + 1 and p * page_size >= sinks, pos_first the position
+ * of the sequence's first row (kv_update_pages gives them back). Tokens of other pages must be
+ * finite, seen or not.
+ */
+kv_status kv_window_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                         int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
+                         float sm_scale, int32_t window, int32_t sinks, int32_t num_shares,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
+/*
+ * kv_tree_attn -- kv_prefill_attn for drafted tokens that form a tree (several continuations
+ * verified in one step). Sequence b's n_b rows are the tree's nodes, cached behind its
+ * seq_lens[b] - n_b earlier tokens; kv_append_rope puts them there, with positions[row] = the
+ * earlier tokens plus the node's depth. parents: device int32[total_tokens], for each row the
+ * index among its sequence's rows (0 for the first) of the node it continues, which comes before
+ * it, or -1 where it continues the cached tokens. A row sees every earlier token, its ancestors and
+ * itself. A parent that is neither is flagged (KV_DEVERR_BAD_SEL) and taken as -1. Sequences of
+ * more than KV_TREE_MAX_NODES rows are flagged (KV_DEVERR_BAD_LEN) and left out. Arguments,
+ * workspace (kv_prefill_attn_workspace_size), rounding, flags and limits are otherwise
+ * kv_prefill_attn's, whose results a tree that is one line has, bit for bit.
+ */
+#define KV_TREE_MAX_NODES 1024
+kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                       int32_t num_q_heads, const int32_t* parents, const int32_t* cu_tokens,
+                       int32_t total_tokens, float sm_scale, int32_t num_shares, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * kv_score_pages -- [ENTMAX] query-aware page score, [SPARDA] summed over a GQA group.
@@ -664,7 +703,7 @@ kv_status kv_entmax_decode_step(const kv_cache_desc* cache, const void* q, int32
  * kv_entmax_attn_workspace_size(cache, num_q_heads, k_max as sel_stride, 0 = every page);
  * KV_OP_ENTMAX_DECODE_STEP: kv_entmax_decode_step_workspace_size(cache, num_q_heads,
  * k_max); KV_OP_PREFILL_ATTN: kv_prefill_attn_workspace_size(cache, num_q_heads, k_max as
- * total_tokens, num_splits as num_shares)). Arguments a given op does not use are ignored.
+ * total_tokens, num_splits as num_shares), also for kv_window_attn and kv_tree_attn). Arguments a given op does not use are ignored.
  * Every other call of this library takes no workspace. Returns 0 for an unknown op or a bad
  * argument.
  */

@@ -45,8 +45,35 @@ def cached_rows(pool, page_table, b, length, page_size):
     return np.asarray(pool)[phys, :, t % page_size].astype(np.float64)
 
 
-def prefill(q, k_pool, v_pool, page_table, seq_lens, cu, page_size, sm_scale):
-    """Causal attention of packed rows: ``out`` [T][Hq][D], ``lse`` [T][Hq], and what the error
+def window_hidden(n, length, window, sinks):
+    """[n][length]: the tokens that the last n rows of a sequence do not see within a sliding
+    window of ``window`` tokens, themselves included, and the first ``sinks`` ones."""
+    hidden = np.ones((n, length), dtype=bool)
+    for i in range(n):
+        pos = length - n + i
+        for u in range(pos + 1):
+            if pos - u < window or u < sinks:
+                hidden[i, u] = False
+    return hidden
+
+
+def tree_hidden(parents, length):
+    """[n][length]: the tokens that n drafted rows, the last ones of a sequence, do not see: those
+    drafted ones that are neither the row nor reached from it by following ``parents``."""
+    n = len(parents)
+    hidden = np.zeros((n, length), dtype=bool)
+    hidden[:, length - n:] = True
+    for i in range(n):
+        node = i
+        while node >= 0:
+            hidden[i, length - n + node] = False
+            node = int(parents[node])
+    return hidden
+
+
+def prefill(q, k_pool, v_pool, page_table, seq_lens, cu, page_size, sm_scale, hidden_of=None):
+    """Causal attention of packed rows (or, with ``hidden_of(b, n, length)``, with the [n][length]
+    mask that it gives for sequence b's n rows): ``out`` [T][Hq][D], ``lse`` [T][Hq], and what the error
     bounds need, ``mass`` = sum_t p_t |v_t| like out and ``logit`` = sm_scale * the largest
     sum_d |q_d k_d| like lse. Rows that belong to no sequence stay NaN."""
     T, Hq, D = q.shape
@@ -62,6 +89,8 @@ def prefill(q, k_pool, v_pool, page_table, seq_lens, cu, page_size, sm_scale):
         V = cached_rows(v_pool, page_table, b, L, page_size)
         rows = slice(int(cu[b]), int(cu[b + 1]))
         hidden = np.arange(L)[None, :] > np.arange(L - n, L)[:, None]
+        if hidden_of is not None:
+            hidden = hidden_of(b, n, L)
         for h in range(Hq):
             x = np.asarray(q[rows, h], dtype=np.float64)
             k, v = K[:, h // G], V[:, h // G]

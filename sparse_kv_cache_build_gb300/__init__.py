@@ -42,7 +42,9 @@ from .binding import (  # noqa: F401
     kv_selftest_wait_timeout,
     kv_set_wait_limit_ns,
     kv_sparse_decode_attn,
+    kv_tree_attn,
     kv_version,
+    kv_window_attn,
     kv_workspace_size,
     max_keep_pages,
 )

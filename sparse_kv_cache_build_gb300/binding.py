@@ -46,6 +46,7 @@ EXPORTS = (
     "kv_entmax_decode_step_workspace_size", "kv_entmax_decode_step", "kv_workspace_size",
     "kv_decode_step_graph_create", "kv_decode_step_graph_launch", "kv_decode_step_graph_destroy",
     "kv_rope_turns", "kv_append_rope", "kv_prefill_attn_workspace_size", "kv_prefill_attn",
+    "kv_window_attn", "kv_tree_attn",
 )
 
 
@@ -124,6 +125,8 @@ def _declare(lib):
                                  P, P]),
         "kv_prefill_attn_workspace_size": (SZ, [D, I32, I32, I32]),
         "kv_prefill_attn": (I32, [D, P, I64, I32, P, I32, F32, I32, P, P, P, SZ, P]),
+        "kv_window_attn": (I32, [D, P, I64, I32, P, I32, F32, I32, I32, I32, P, P, P, SZ, P]),
+        "kv_tree_attn": (I32, [D, P, I64, I32, P, P, I32, F32, I32, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -423,10 +426,9 @@ def kv_prefill_attn_workspace_size(kv: PagedKV, num_q_heads: int, total_tokens: 
                                                     int(total_tokens), int(num_shares)))
 
 
-def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares: int = 0,
-                    out=None, lse=None, workspace=None, stream=None):
-    """Causal attention of packed query rows [T][Hq][D] over the cache, which holds the rows'
-    own keys and values already: (out of the cache's dtype, lse float32)."""
+def _attend(kv: PagedKV, q, cu_tokens, num_shares, out, lse, workspace, stream, call):
+    """What the calls that attend with packed rows share: checks, buffers, and
+    call(q, stride, heads, offsets, rows, last arguments), which returns its name and status."""
     T, Hq, qs, cu = _packed(kv, q, cu_tokens)
     D = kv.cols
     if out is None:
@@ -444,13 +446,46 @@ def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares:
         workspace = _new((nbytes,), torch.uint8, q.device, stream)
     elif workspace.get_device() != kv.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {kv.k_pool.device}")
-    status = lib().kv_prefill_attn(
-        kv.ref(), q.data_ptr(), qs, Hq, cu, T, float(sm_scale), int(num_shares), out.data_ptr(),
-        lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _raw_stream(kv, stream))
+    fn, status = call(q.data_ptr(), qs, Hq, cu, T, (
+        int(num_shares), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(kv, stream)))
     if status != KV_OK:
-        raise KVError("kv_prefill_attn", status)
+        raise KVError(fn, status)
     return out, lse
+
+
+def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares: int = 0,
+                    out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of packed query rows [T][Hq][D] over the cache, which holds the rows'
+    own keys and values already: (out of the cache's dtype, lse float32)."""
+    def call(ptr, stride, Hq, cu, T, last):
+        return "kv_prefill_attn", lib().kv_prefill_attn(
+            kv.ref(), ptr, stride, Hq, cu, T, float(sm_scale), *last)
+    return _attend(kv, q, cu_tokens, num_shares, out, lse, workspace, stream, call)
+
+
+def kv_window_attn(kv: PagedKV, q, sm_scale: float, window: int, sinks: int = 0, cu_tokens=None,
+                   num_shares: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """kv_prefill_attn where a row sees the last `window` tokens up to itself and the sequence's
+    first `sinks` ones: (out, lse). Pages that no row sees may be unmapped."""
+    def call(ptr, stride, Hq, cu, T, last):
+        return "kv_window_attn", lib().kv_window_attn(
+            kv.ref(), ptr, stride, Hq, cu, T, float(sm_scale), int(window), int(sinks), *last)
+    return _attend(kv, q, cu_tokens, num_shares, out, lse, workspace, stream, call)
+
+
+def kv_tree_attn(kv: PagedKV, q, sm_scale: float, parents, cu_tokens=None, num_shares: int = 0,
+                 out=None, lse=None, workspace=None, stream=None):
+    """kv_prefill_attn for drafted tokens that form a tree: a row sees the tokens cached before
+    its sequence's rows, its ancestors and itself: (out, lse). parents: int32 [T], a row's parent
+    among its sequence's rows (0 for the first), or -1."""
+    if q.dim() == 3:
+        _on_device(kv, parents, "parents", torch.int32, (q.shape[0],))
+
+    def call(ptr, stride, Hq, cu, T, last):
+        return "kv_tree_attn", lib().kv_tree_attn(
+            kv.ref(), ptr, stride, Hq, parents.data_ptr(), cu, T, float(sm_scale), *last)
+    return _attend(kv, q, cu_tokens, num_shares, out, lse, workspace, stream, call)
 
 
 def kv_score_pages(kv: PagedKV, q, stats, scores=None, stream=None):

@@ -239,6 +239,49 @@ PrefillLayout prefill_layout(const kv_cache_desc* d, int G, int total, int share
   return L;
 }
 
+// What the calls that attend with packed rows share; `a` holds the mask.
+kv_status packed_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                      int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
+                      float sm_scale, int32_t num_shares, void* out, float* lse, void* workspace,
+                      size_t workspace_bytes, PrefillArgs a, cudaStream_t stream) {
+  kv_status r = check_desc(cache);
+  if (r != KV_OK) return r;
+  if ((r = check_heads(cache, q, num_q_heads)) != KV_OK) return r;
+  if ((r = check_packed(cache, cu_tokens, total_tokens)) != KV_OK) return r;
+  if (out == nullptr || !(sm_scale > 0.f) || !isfinite(sm_scale) || num_shares < 0 ||
+      num_shares > kPrefillMaxShares)
+    return KV_ERR_INVALID_ARG;
+  if ((r = check_rows(cache, q, q_stride, num_q_heads)) != KV_OK) return r;
+  if (!aligned16(out)) return KV_ERR_MISALIGNED;
+  if (cache->dtype == KV_BF16 &&
+      (int64_t)cache->num_phys_pages * cache->num_kv_heads * cache->page_size > INT32_MAX)
+    return KV_ERR_UNSUPPORTED;                    // TMA row coordinates are 32-bit
+  if (total_tokens == 0) return KV_OK;
+  DevCtx ctx;
+  DeviceState* st = nullptr;
+  if ((r = ctx_for_call(&ctx, &st)) != KV_OK) return r;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.out = out;
+  a.lse = lse;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.Hq = num_q_heads;
+  a.G = num_q_heads / cache->num_kv_heads;
+  while (1 << a.log_g < a.G) ++a.log_g;
+  a.NC = prefill_shares(num_shares, st);
+  const PrefillLayout L = prefill_layout(cache, a.G, total_tokens, a.NC);
+  if (L.total > 0) {
+    if (workspace == nullptr || workspace_bytes < L.total ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+      return KV_ERR_WORKSPACE;
+    a.part_acc = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.ml);
+    a.notes = reinterpret_cast<BorderNote*>(static_cast<char*>(workspace) + L.notes);
+    a.part_rows = L.rows;
+  }
+  return from_cuda(launch_prefill(*cache, cu_tokens, total_tokens, a, ctx, stream));
+}
+
 __global__ void wait_selftest_kernel(unsigned long long limit_ns, DevCtx ctx) {
   __shared__ __align__(8) uint64_t bar;
   if (threadIdx.x == 0) {
@@ -398,43 +441,40 @@ kv_status kv_prefill_attn(const kv_cache_desc* cache, const void* q, int64_t q_s
                           int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
                           float sm_scale, int32_t num_shares, void* out, float* lse,
                           void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  PrefillArgs a{};
+  a.mask = Mask::kCausal;
+  return packed_attn(cache, q, q_stride, num_q_heads, cu_tokens, total_tokens, sm_scale,
+                     num_shares, out, lse, workspace, workspace_bytes, a, stream);
+}
+
+kv_status kv_window_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                         int32_t num_q_heads, const int32_t* cu_tokens, int32_t total_tokens,
+                         float sm_scale, int32_t window, int32_t sinks, int32_t num_shares,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream) {
   kv_status r = check_desc(cache);
   if (r != KV_OK) return r;
-  if ((r = check_heads(cache, q, num_q_heads)) != KV_OK) return r;
-  if ((r = check_packed(cache, cu_tokens, total_tokens)) != KV_OK) return r;
-  if (out == nullptr || !(sm_scale > 0.f) || !isfinite(sm_scale) || num_shares < 0 ||
-      num_shares > kPrefillMaxShares)
-    return KV_ERR_INVALID_ARG;
-  if ((r = check_rows(cache, q, q_stride, num_q_heads)) != KV_OK) return r;
-  if (!aligned16(out)) return KV_ERR_MISALIGNED;
-  if (cache->dtype == KV_BF16 &&
-      (int64_t)cache->num_phys_pages * cache->num_kv_heads * cache->page_size > INT32_MAX)
-    return KV_ERR_UNSUPPORTED;                    // TMA row coordinates are 32-bit
-  if (total_tokens == 0) return KV_OK;
-  DevCtx ctx;
-  DeviceState* st = nullptr;
-  if ((r = ctx_for_call(&ctx, &st)) != KV_OK) return r;
+  if (window < 1 || sinks < 0) return KV_ERR_INVALID_ARG;
   PrefillArgs a{};
-  a.q = q;
-  a.q_stride = q_stride;
-  a.out = out;
-  a.lse = lse;
-  a.scale_log2 = sm_scale * kLog2e;
-  a.Hq = num_q_heads;
-  a.G = num_q_heads / cache->num_kv_heads;
-  while (1 << a.log_g < a.G) ++a.log_g;
-  a.NC = prefill_shares(num_shares, st);
-  const PrefillLayout L = prefill_layout(cache, a.G, total_tokens, a.NC);
-  if (L.total > 0) {
-    if (workspace == nullptr || workspace_bytes < L.total ||
-        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-      return KV_ERR_WORKSPACE;
-    a.part_acc = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.ml);
-    a.notes = reinterpret_cast<BorderNote*>(static_cast<char*>(workspace) + L.notes);
-    a.part_rows = L.rows;
-  }
-  return from_cuda(launch_prefill(*cache, cu_tokens, total_tokens, a, ctx, stream));
+  a.mask = Mask::kWindow;
+  // no more than a table row can hold: the kernels' sums of positions stay in 32 bits
+  const int32_t most = cache->page_table_stride * cache->page_size;
+  a.window = window < most ? window : most;
+  a.sinks = sinks < most ? sinks : most;
+  return packed_attn(cache, q, q_stride, num_q_heads, cu_tokens, total_tokens, sm_scale,
+                     num_shares, out, lse, workspace, workspace_bytes, a, stream);
+}
+
+kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,
+                       int32_t num_q_heads, const int32_t* parents, const int32_t* cu_tokens,
+                       int32_t total_tokens, float sm_scale, int32_t num_shares, void* out,
+                       float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (parents == nullptr) return KV_ERR_INVALID_ARG;
+  PrefillArgs a{};
+  a.mask = Mask::kTree;
+  a.parents = parents;
+  return packed_attn(cache, q, q_stride, num_q_heads, cu_tokens, total_tokens, sm_scale,
+                     num_shares, out, lse, workspace, workspace_bytes, a, stream);
 }
 
 kv_status kv_score_pages(const kv_cache_desc* cache, const void* q, int32_t num_q_heads,

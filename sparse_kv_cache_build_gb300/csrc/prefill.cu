@@ -1,4 +1,4 @@
-// Causal prompt attention: the choice of kernel, and the join of the items its blocks shared.
+// Attention of packed rows: the choice of kernel, and the join of the items its blocks shared.
 #include <type_traits>
 
 #include "prefill.cuh"
@@ -139,7 +139,16 @@ cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
   const PackedRows pr{cu, total};
   const bool bf = d.dtype == KV_BF16;
-  cudaError_t e = bf ? launch_prefill_mma(d, pr, a, ctx, s) : launch_prefill_simt(d, pr, a, ctx, s);
+  cudaError_t e;
+  if (a.mask == Mask::kCausal)
+    e = bf ? launch_prefill_mma<Mask::kCausal>(d, pr, a, ctx, s)
+           : launch_prefill_simt<Mask::kCausal>(d, pr, a, ctx, s);
+  else if (a.mask == Mask::kWindow)
+    e = bf ? launch_prefill_mma<Mask::kWindow>(d, pr, a, ctx, s)
+           : launch_prefill_simt<Mask::kWindow>(d, pr, a, ctx, s);
+  else
+    e = bf ? launch_prefill_mma<Mask::kTree>(d, pr, a, ctx, s)
+           : launch_prefill_simt<Mask::kTree>(d, pr, a, ctx, s);
   if (e != cudaSuccess || a.NC == 1) return e;
   if (bf) return d.head_dim == 128 ? merge_t<bf16_t, 128>(a, s) : merge_t<bf16_t, 64>(a, s);
   return d.head_dim == 128 ? merge_t<float, 128>(a, s) : merge_t<float, 64>(a, s);

@@ -1,6 +1,7 @@
 // Causal attention of packed query rows over the paged cache: what its kernels share.
 //
-// Row (t, h) of sequence b, at position pos = len_b - n_b + t, attends to tokens 0..pos:
+// Row (t, h) of sequence b, at position pos = len_b - n_b + t, attends to tokens 0..pos, or to those
+// of them that its mask lets it see (Mask below):
 //   x_u = sm_scale q . k_u,  lse = log sum_u exp(x_u),  out = sum_u exp(x_u - lse) v_u.
 // The group's G query heads read the same keys, so a tile's rows are (token, head) pairs of
 // one KV head, token-major: a tile of R rows is R / G consecutive tokens.
@@ -20,6 +21,12 @@
 #include "packed_rows.cuh"
 
 namespace skv {
+
+// Which of its sequence's tokens the row at position pos sees, beside u <= pos: all of them, those
+// of a window and the first ones (kv_window_attn), or the tokens before the drafted rows and the
+// row's own ancestors among these (kv_tree_attn).
+enum class Mask { kCausal, kWindow, kTree };
+constexpr int kTreeNodes = KV_TREE_MAX_NODES;        // 32 words of ancestors a row
 
 // Where block c's piece of the line begins: the item there (by its first packed row and KV head)
 // and the block's key tiles of it. 0 < kt0 < nk: the border cuts the item, whose part before
@@ -41,17 +48,42 @@ struct PrefillArgs {
   int Hq, G, log_g;
   int NC;                 // blocks the work is divided among
   int part_rows;          // rows of a part: a tile's, or all there are
+  Mask mask;
+  int window, sinks;      // kWindow: u > pos - window, or u < sinks
+  const int32_t* parents; // kTree: [total], a row's parent among its sequence's rows, or -1
 };
 
 // Tile sizes of a kernel: R rows by KT keys, and what an item costs: two units per key tile, one
 // where the item has at most WIDE rows, and a fixed part of kItemCost units (bf16: an item's start
 // and end are 5000 to 9000 cycles, a unit 1300; 3, 4, 5 and 8 give 240, 242, 247 and 257 us for
 // sixteen ragged prompts, and 351, 345, 345 and 350 for one of 8192 tokens in pages of 64).
-template <int R, int KT, int WIDE> struct TileShape {
+template <int R, int KT, int WIDE, Mask M = Mask::kCausal> struct TileShape {
   static constexpr int rows = R, keys = KT, narrow = WIDE;
+  static constexpr Mask mask = M;
+  template <Mask N> using With = TileShape<R, KT, WIDE, N>;
 };
 constexpr int kItemCost = 4;
 constexpr int kMinPart = 2;      // a border leaves an item at least this many key tiles
+
+// A window leaves an item whose first row is at `pos0` the tiles of the first tokens and those
+// from the window's first token on. Its key tiles are counted without the ones between: tile kt is
+// tile real_tile(kt) of the sequence.
+template <typename S> __device__ __forceinline__ int sink_tiles(const PrefillArgs& a) {
+  return a.sinks / S::keys + (a.sinks % S::keys != 0);
+}
+template <typename S> __device__ __forceinline__ int skipped(int pos0, const PrefillArgs& a) {
+  if (S::mask != Mask::kWindow) return 0;
+  return max(0, max(0, pos0 - a.window + 1) / S::keys - sink_tiles<S>(a));
+}
+template <typename S>
+__device__ __forceinline__ int real_tile(int kt, int skip, const PrefillArgs& a) {
+  if (S::mask != Mask::kWindow) return kt;
+  return kt < sink_tiles<S>(a) ? kt : kt + skip;
+}
+// Whether page p holds no token that the item's rows see: such pages may have been given back.
+__device__ __forceinline__ bool dead_page(int p, int page_size, int pos0, const PrefillArgs& a) {
+  return p * page_size >= a.sinks && (p + 1) * page_size <= pos0 - a.window + 1;
+}
 
 // One sequence's rows as items, the same for each of its KV heads.
 template <typename S> struct SeqItems {
@@ -66,34 +98,47 @@ template <typename S> struct SeqItems {
   __device__ __forceinline__ int tokens(int tile) const {
     return min(1 << tq_log, n - (tile << tq_log));
   }
-  __device__ __forceinline__ int key_tiles(int tile) const {
+  __device__ __forceinline__ int key_tiles(int tile, const PrefillArgs& a) const {
     const int64_t keys = (int64_t)(len - n) + (tile << tq_log) + tokens(tile);
-    return (int)((keys + S::keys - 1) / S::keys);
+    return (int)((keys + S::keys - 1) / S::keys) - skipped<S>(len - n + (tile << tq_log), a);
   }
   __device__ __forceinline__ int unit(int tile, int log_g) const {
     return (tokens(tile) << log_g) > S::narrow ? 2 : 1;
   }
-  // Cost of the first x tiles. All but the sequence's last tile are full: FULL units for each
-  // of ceil((past + (j + 1) TQ) / KT) key tiles.
-  __device__ __forceinline__ int64_t cost(int x, int log_g) const {
-    constexpr int FULL = S::rows > S::narrow ? 2 : 1;
-    const int nt = tiles();
-    int64_t c = (int64_t)kItemCost * x;
-    if (x == nt && x > 0) {
-      --x;
-      c += (int64_t)unit(x, log_g) * key_tiles(x);
-    }
-    const int a = len - n + S::keys - 1;            // sum of floor((a + j TQ) / KT), j = 1..x
+  // sum of floor((a + j TQ) / KT) over j = 1..x, for a >= 0
+  __device__ __forceinline__ int64_t floors(int a, int x) const {
     if ((1 << tq_log) >= S::keys) {
       const int64_t r = (1 << tq_log) / S::keys;
-      return c + FULL * (x * (int64_t)(a / S::keys) + r * ((int64_t)x * (x + 1) / 2));
+      return x * (int64_t)(a / S::keys) + r * ((int64_t)x * (x + 1) / 2);
     }
     const int r_log = (__ffs(S::keys) - 1) - tq_log, r = 1 << r_log;
     const int rest = (a & (S::keys - 1)) >> tq_log;
     // floor((rest + j) / r) summed over j = 1..x; below r the terms are zero
     const int64_t y = (int64_t)rest + x + 1, q = y >> r_log;
     const int64_t steps = r * (q * (q - 1) / 2) + q * (y & (r - 1));
-    return c + FULL * (x * (int64_t)(a / S::keys) + steps);
+    return x * (int64_t)(a / S::keys) + steps;
+  }
+  // Cost of the first x tiles. All but the sequence's last tile are full: FULL units for each
+  // of ceil((past + (j + 1) TQ) / KT) key tiles, less those that the window skips.
+  __device__ __forceinline__ int64_t cost(int x, const PrefillArgs& a) const {
+    constexpr int FULL = S::rows > S::narrow ? 2 : 1;
+    const int nt = tiles();
+    int64_t c = (int64_t)kItemCost * x;
+    if (x == nt && x > 0) {
+      --x;
+      c += (int64_t)unit(x, a.log_g) * key_tiles(x, a);
+    }
+    c += FULL * floors(len - n + S::keys - 1, x);
+    if (S::mask == Mask::kWindow) {
+      // tile j skips max(0, floor((c0 + j TQ) / KT)): nothing before tile j0
+      const int64_t c0 = (int64_t)(len - n) - a.window + 1 - (int64_t)sink_tiles<S>(a) * S::keys;
+      const int64_t j0 = c0 >= 0 ? 0 : (-c0 + (1 << tq_log) - 1) >> tq_log;
+      if (j0 < x) {
+        const int first = (int)(c0 + (j0 << tq_log));
+        c -= FULL * (first / S::keys + floors(first, (int)(x - j0 - 1)));
+      }
+    }
+    return c;
   }
 };
 
@@ -121,6 +166,19 @@ __device__ __forceinline__ int tiles_before(int64_t y, int64_t x, int nk, int un
   return k < kMinPart ? 0 : nk - k < kMinPart ? nk : (int)k;
 }
 
+// One sequence's items; a tree of too many nodes is left out.
+template <typename S>
+__device__ __forceinline__ SeqItems<S> seq_items(const DevCtx& ctx, const kv_cache_desc& d,
+                                                 const PackedRows& pr, const PrefillArgs& a,
+                                                 int b) {
+  SeqRows s = seq_rows(ctx, d, pr, b);
+  if (S::mask == Mask::kTree && s.n > kTreeNodes) {
+    flag(ctx, KV_DEVERR_BAD_LEN);
+    s.n = 0;
+  }
+  return SeqItems<S>(s, a.log_g);
+}
+
 // Walks the items of the piece [lo, hi) of the line. Every warp that works on the items walks
 // them by itself; the lengths of the next sequence are fetched ahead.
 template <typename S> class ItemWalk {
@@ -129,19 +187,19 @@ template <typename S> class ItemWalk {
                                       const PrefillArgs& a, const DevCtx& ctx, int64_t lo,
                                       int64_t hi, int b, int64_t before, int block)
       : d_(d), pr_(pr), a_(a), ctx_(ctx), lo_(lo), hi_(hi), x_(before), b_(b), g_(0), tile_(-1),
-        block_(block), seq_(seq_rows(ctx, d, pr, b), a.log_g), next_(fetch(b + 1)) {
+        block_(block), seq_(seq_items<S>(ctx, d, pr, a, b)), next_(fetch(b + 1)) {
     // the last item that starts at or before lo
-    const int64_t head = seq_.cost(seq_.tiles(), a.log_g);
+    const int64_t head = seq_.cost(seq_.tiles(), a);
     if (head > 0) {
       g_ = (int)divide(lo - x_, head);
       x_ += g_ * head;
       int t = 0, end = seq_.tiles();
       while (end - t > 1) {
         const int mid = (t + end) >> 1;
-        if (x_ + seq_.cost(mid, a.log_g) <= lo) t = mid;
+        if (x_ + seq_.cost(mid, a) <= lo) t = mid;
         else end = mid;
       }
-      x_ += seq_.cost(t, a.log_g);
+      x_ += seq_.cost(t, a);
       tile_ = t - 1;
     }
   }
@@ -159,7 +217,7 @@ template <typename S> class ItemWalk {
         next_ = fetch(b_ + 1);
       }
       if (x_ >= hi_) return false;
-      const int nk = seq_.key_tiles(tile_), unit = seq_.unit(tile_, a_.log_g);
+      const int nk = seq_.key_tiles(tile_, a_), unit = seq_.unit(tile_, a_.log_g);
       const int64_t x = x_;
       x_ += kItemCost + (int64_t)unit * nk;
       it->kt0 = tiles_before(lo_, x, nk, unit);
@@ -184,7 +242,7 @@ template <typename S> class ItemWalk {
     n.row0 = seq_.row0 + (t << seq_.tq_log);
     n.n_tok = seq_.tokens(t);
     n.g = g_;
-    n.nk = seq_.key_tiles(t);
+    n.nk = seq_.key_tiles(t, a_);
     n.kt0 = tiles_before(lo_, x_, n.nk, seq_.unit(t, a_.log_g));
     n.kt1 = tiles_before(hi_, x_, n.nk, seq_.unit(t, a_.log_g));
     return n;
@@ -192,7 +250,7 @@ template <typename S> class ItemWalk {
 
  private:
   __device__ __forceinline__ SeqItems<S> fetch(int b) const {
-    if (b < d_.batch) return SeqItems<S>(seq_rows(ctx_, d_, pr_, b), a_.log_g);
+    if (b < d_.batch) return seq_items<S>(ctx_, d_, pr_, a_, b);
     return SeqItems<S>(SeqRows{0, 0, 0}, a_.log_g);
   }
   const kv_cache_desc& d_;
@@ -225,8 +283,8 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
   const int per = (d.batch + blockDim.x - 1) / blockDim.x;
   const int b0 = tid * per, b1 = min(d.batch, b0 + per);
   auto cost_of = [&](int b) -> int64_t {
-    const SeqItems<S> s(seq_rows(ctx, d, pr, b), a.log_g);
-    return s.cost(s.tiles(), a.log_g) * d.num_kv_heads;
+    const SeqItems<S> s = seq_items<S>(ctx, d, pr, a, b);
+    return s.cost(s.tiles(), a) * d.num_kv_heads;
   };
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += cost_of(b);
@@ -270,8 +328,10 @@ using SimtShape = TileShape<128, 64, 0>;         // fp32, CUDA cores
 int prefill_tile_rows(int dtype);
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
+template <Mask M>
 cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
                                 const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
+template <Mask M>
 cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
 
