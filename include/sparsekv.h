@@ -17,6 +17,9 @@
  *   kv_prefill_attn        causal attention of packed query rows over the cache
  *   kv_window_attn         the same within a sliding window and the first tokens
  *   kv_tree_attn           the same for drafted tokens that form a tree
+ *   kv_compact             kept tokens (accepted drafts, an eviction) moved together in place
+ *   kv_update_pages        the batch's next page table: forks, drops, frees and new pages
+ *   kv_copy_pages          copies of physical pages (what a fork has to write to)
  *
  * Sources, by page title and section:
  *   [ENTMAX]  "EntmaxKV: Support-Aware Decoding for Entmax Attention", abstract: pages are
@@ -103,9 +106,11 @@ enum {
   KV_DEVERR_BAD_PAGE = 1,    /* page-table entry outside [0, num_phys_pages) */
   KV_DEVERR_BAD_LEN = 2,     /* seq_len < 0 or above page_table_stride * page_size; packed
                                 offsets out of order or longer than their sequence */
-  KV_DEVERR_BAD_SEL = 4,     /* selected index outside [0, n_pages) or sel_cnt > stride */
+  KV_DEVERR_BAD_SEL = 4,     /* selected index outside [0, n_pages) or sel_cnt > stride; a parent
+                                or kept index that is none */
   KV_DEVERR_KEEP = 8,        /* keep count above k_max (clamped to k_max) */
-  KV_DEVERR_TIMEOUT = 16     /* bounded wait on an asynchronous copy ran out */
+  KV_DEVERR_TIMEOUT = 16,    /* bounded wait on an asynchronous copy ran out */
+  KV_DEVERR_NO_PAGES = 32    /* kv_update_pages: fewer free pages than the rows need */
 };
 
 /* The paged cache. All pointers are device pointers owned by the caller. */
@@ -310,6 +315,79 @@ kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stri
                        int32_t num_q_heads, const int32_t* parents, const int32_t* cu_tokens,
                        int32_t total_tokens, float sm_scale, int32_t num_shares, void* out,
                        float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * kv_compact -- some of a sequence's last tokens stay and move together, in place: the accepted
+ * drafts of a verified tree, or the tokens that an eviction keeps. Sequence b's candidates are its
+ * n_b = cu_tokens[b+1] - cu_tokens[b] last tokens (cu_tokens: device int32[batch+1] as in
+ * kv_append_rope; NULL: all its seq_lens[b] tokens), from position s_b = seq_lens[b] - n_b on. The
+ * token at s_b + keep[b][i] moves to s_b + i, for i < keep_cnt[b]:
+ *   keep: device int32 [batch][keep_stride], indices among the candidates, rising;
+ *   keep_cnt: device int32[batch], 0 .. min(n_b, keep_stride).
+ * Keys move as they are (a rotated key keeps its position's rotation). Statistics of the pages that
+ * hold candidates or what is kept, s_b / page_size up to the last kept token's, become those of
+ * kv_build_page_stats at the new length (stats may be NULL: they are left alone; so are those of a
+ * sequence without candidates). Tokens before s_b and slots behind the last kept token stay as they
+ * are. new_lens: device int32[batch], becomes
+ * s_b + keep_cnt[b]; it is not seq_lens, which the call leaves as it is (the caches of all layers
+ * take the same lists), and which the caller replaces when all are done.
+ * Pages from s_b on must not be shared with another sequence. Indices that do not rise or are
+ * outside the candidates are flagged (KV_DEVERR_BAD_SEL) and not moved; the sequence's tokens from
+ * there on are unspecified. A count that does not fit is flagged and the sequence left as it is,
+ * with new_lens = seq_lens; so are bad lengths and offsets (KV_DEVERR_BAD_LEN), where new_lens is 0
+ * for a bad length. An unmapped page is flagged (KV_DEVERR_BAD_PAGE) and its tokens left out.
+ * KV_ERR_UNSUPPORTED for page-table rows of 2^31 - 4096 tokens or more.
+ */
+kv_status kv_compact(const kv_cache_desc* cache, const int32_t* cu_tokens, const int32_t* keep,
+                     int32_t keep_stride, const int32_t* keep_cnt, void* stats, int32_t* new_lens,
+                     cudaStream_t stream);
+
+/*
+ * kv_copy_pages -- for each i < n, physical page pairs[i][0]'s keys and values (and its rows of
+ * stats, if not NULL) are copied to page pairs[i][1]. pairs: device int32 [n][2], 8-byte aligned;
+ * a pair with a negative number copies nothing, one beyond the pool is flagged
+ * (KV_DEVERR_BAD_PAGE) and copies nothing. A page that is written must not occur a second time in
+ * the list. stats: device, of the cache dtype as in kv_build_page_stats.
+ */
+kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_t n, void* stats,
+                        cudaStream_t stream);
+
+/*
+ * kv_update_pages -- the page table of the next step, with pages counted by their holders:
+ * refs: device int32[num_phys_pages], 16-byte aligned; refs[P] is the number of page-table entries
+ * (and other holders, a prefix cache say) that hold page P, 0 for a free one. Entries that map no
+ * page are -1 throughout a row, also behind its sequence's end.
+ * New row b (of `rows`) continues old row parents[b] of the descriptor's page_table (device
+ * int32[rows]; -1: a new sequence, no old row; NULL: row b continues row b, rows = batch), keeps its
+ * first keep_lens[b] tokens (NULL: all seq_lens[parents[b]] of them) and gets pages for
+ * new_lens[b] >= keep_lens[b] tokens (both device int32[rows]). In this order:
+ *  - table (device int32 [rows][page_table_stride]; page_table itself is allowed without parents,
+ *    any other overlap is not) becomes the old rows' entries of the pages that hold kept tokens,
+ *    and -1 elsewhere. With window > 0, pages that kv_window_attn with this window and these sinks
+ *    never reads again are -1 too: those with p * page_size >= sinks and
+ *    (p + 1) * page_size <= keep - window + 1. refs follows: every old row's entries are given
+ *    back, every new row's are held; an old row that nobody continues is thereby freed.
+ *  - a row that grows (new > keep) out of a partial page that others hold too gets a fresh page in
+ *    its place, to which copies[b] = (old page, fresh page) asks kv_copy_pages (of every layer) to
+ *    copy; of rows that alone hold a page together, the last keeps it. copies: device int32
+ *    [rows][2], (-1, -1) where there is nothing to copy.
+ *  - rows get their fresh pages, the one in the partial page's place first, then those behind, in
+ *    the order of the rows: always the free page of the lowest number.
+ * Where the free pages do not suffice for all rows, none is handed out: rows keep what they hold,
+ * copies are (-1, -1), and KV_DEVERR_NO_PAGES is flagged. free_left: device int32[1], the free
+ * pages after the call, or minus those that were missing.
+ * Lengths that do not fit (keep outside the old row's tokens, new below keep or above the table
+ * row) are flagged (KV_DEVERR_BAD_LEN) and the row keeps its old row's tokens; a parent that is no
+ * old row is flagged (KV_DEVERR_BAD_SEL) and taken as -1; an entry that is neither -1 nor a page is
+ * flagged (KV_DEVERR_BAD_PAGE) and taken as -1. KV_ERR_UNSUPPORTED for more than KV_PAGES_MAX_ROWS
+ * rows, old or new, and for page-table rows of 2^31 - 256 tokens or more. seq_lens is not written: the caller makes new_lens the lengths when the step's
+ * tokens are appended.
+ */
+#define KV_PAGES_MAX_ROWS 16384
+kv_status kv_update_pages(const kv_cache_desc* cache, int32_t* refs, const int32_t* parents,
+                          int32_t rows, const int32_t* keep_lens, const int32_t* new_lens,
+                          int32_t window, int32_t sinks, int32_t* table, int32_t* copies,
+                          int32_t* free_left, cudaStream_t stream);
 
 /*
  * kv_score_pages -- [ENTMAX] query-aware page score, [SPARDA] summed over a GQA group.

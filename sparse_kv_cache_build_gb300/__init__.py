@@ -17,6 +17,8 @@ from .binding import (  # noqa: F401
     kv_build_page_stats,
     kv_build_page_stats_fp8,
     kv_check_device_errors,
+    kv_compact,
+    kv_copy_pages,
     kv_decode_attn_merge,
     kv_decode_step,
     kv_decode_step_fp8,
@@ -43,6 +45,7 @@ from .binding import (  # noqa: F401
     kv_set_wait_limit_ns,
     kv_sparse_decode_attn,
     kv_tree_attn,
+    kv_update_pages,
     kv_version,
     kv_window_attn,
     kv_workspace_size,

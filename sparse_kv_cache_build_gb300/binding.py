@@ -30,7 +30,8 @@ PLANS = {0: "four kernels", 1: "score, then select + attention + merge",
 STATUS = {0: "KV_OK", -1: "KV_ERR_INVALID_ARG", -2: "KV_ERR_UNSUPPORTED", -3: "KV_ERR_CUDA",
           -4: "KV_ERR_WORKSPACE", -5: "KV_ERR_BAD_INDEX", -6: "KV_ERR_TIMEOUT",
           -7: "KV_ERR_MISALIGNED"}
-DEVERR = {"BAD_PAGE": 1, "BAD_LEN": 2, "BAD_SEL": 4, "KEEP": 8, "TIMEOUT": 16}
+DEVERR = {"BAD_PAGE": 1, "BAD_LEN": 2, "BAD_SEL": 4, "KEEP": 8, "TIMEOUT": 16,
+          "NO_PAGES": 32}
 
 # Every symbol include/sparsekv.h declares.
 EXPORTS = (
@@ -46,7 +47,7 @@ EXPORTS = (
     "kv_entmax_decode_step_workspace_size", "kv_entmax_decode_step", "kv_workspace_size",
     "kv_decode_step_graph_create", "kv_decode_step_graph_launch", "kv_decode_step_graph_destroy",
     "kv_rope_turns", "kv_append_rope", "kv_prefill_attn_workspace_size", "kv_prefill_attn",
-    "kv_window_attn", "kv_tree_attn",
+    "kv_window_attn", "kv_tree_attn", "kv_compact", "kv_copy_pages", "kv_update_pages",
 )
 
 
@@ -126,6 +127,9 @@ def _declare(lib):
         "kv_prefill_attn_workspace_size": (SZ, [D, I32, I32, I32]),
         "kv_prefill_attn": (I32, [D, P, I64, I32, P, I32, F32, I32, P, P, P, SZ, P]),
         "kv_window_attn": (I32, [D, P, I64, I32, P, I32, F32, I32, I32, I32, P, P, P, SZ, P]),
+        "kv_compact": (I32, [D, P, P, I32, P, P, P, P]),
+        "kv_copy_pages": (I32, [D, P, I32, P, P]),
+        "kv_update_pages": (I32, [D, P, P, I32, P, P, I32, I32, P, P, P, P]),
         "kv_tree_attn": (I32, [D, P, I64, I32, P, P, I32, F32, I32, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
@@ -486,6 +490,94 @@ def kv_tree_attn(kv: PagedKV, q, sm_scale: float, parents, cu_tokens=None, num_s
         return "kv_tree_attn", lib().kv_tree_attn(
             kv.ref(), ptr, stride, Hq, parents.data_ptr(), cu, T, float(sm_scale), *last)
     return _attend(kv, q, cu_tokens, num_shares, out, lse, workspace, stream, call)
+
+
+def _current(kv: PagedKV):
+    if kv.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {kv.k_pool.device}, which is not the current device")
+
+
+def kv_compact(kv: PagedKV, keep, keep_cnt, stats=None, cu_tokens=None, new_lens=None,
+               stream=None):
+    """Kept tokens move together in place: of each sequence's last cu_tokens[b+1] - cu_tokens[b]
+    tokens (None: of all) those numbered keep[b][:keep_cnt[b]] (int32 [B][n], rising; int32 [B])
+    stay, and the statistics of their pages follow. Returns the new lengths (int32 [B], not
+    kv.seq_lens, which is left as it is)."""
+    _current(kv)
+    B = kv.sequences
+    if keep.dim() != 2 or keep.shape[1] < 1:
+        raise ValueError("keep must have shape [batch][at least 1]")
+    _on_device(kv, keep, "keep", torch.int32, (B, keep.shape[1]))
+    _on_device(kv, keep_cnt, "keep_cnt", torch.int32, (B,))
+    if stats is not None:
+        _on_device(kv, stats, "stats", kv.elem, (kv.pages, kv.groups, 2, kv.cols))
+    if cu_tokens is not None:
+        _on_device(kv, cu_tokens, "cu_tokens", torch.int32, (B + 1,))
+    if new_lens is None:
+        new_lens = _new((B,), torch.int32, kv.k_pool.device, stream)
+    else:
+        _on_device(kv, new_lens, "new_lens", torch.int32, (B,))
+    status = lib().kv_compact(
+        kv.ref(), None if cu_tokens is None else cu_tokens.data_ptr(), keep.data_ptr(),
+        keep.shape[1], keep_cnt.data_ptr(), None if stats is None else stats.data_ptr(),
+        new_lens.data_ptr(), _raw_stream(kv, stream))
+    if status != KV_OK:
+        raise KVError("kv_compact", status)
+    return new_lens
+
+
+def kv_copy_pages(kv: PagedKV, pairs, stats=None, stream=None):
+    """Copies physical pages (and their rows of stats): pairs int32 [n][2] of source and
+    destination; a pair with a negative number copies nothing."""
+    _current(kv)
+    if pairs.dim() != 2:
+        raise ValueError("pairs must have shape [n][2]")
+    _on_device(kv, pairs, "pairs", torch.int32, (pairs.shape[0], 2))
+    if stats is not None:
+        _on_device(kv, stats, "stats", kv.elem, (kv.pages, kv.groups, 2, kv.cols))
+    if pairs.shape[0] == 0:
+        return
+    status = lib().kv_copy_pages(kv.ref(), pairs.data_ptr(), pairs.shape[0],
+                                 None if stats is None else stats.data_ptr(),
+                                 _raw_stream(kv, stream))
+    if status != KV_OK:
+        raise KVError("kv_copy_pages", status)
+
+
+def kv_update_pages(kv: PagedKV, refs, new_lens, keep_lens=None, parents=None, window: int = 0,
+                    sinks: int = 0, table=None, copies=None, free_left=None, stream=None):
+    """The next step's page table: row b continues row parents[b] (None: row b, -1: none), keeps
+    keep_lens[b] of its tokens (None: all) and gets pages for new_lens[b]; refs (int32 [pages],
+    holders of each page) is updated in place. Returns (table, copies, free_left): the table
+    (kv.page_table itself by default without parents, else a new one), the (old, fresh) pages per
+    row that kv_copy_pages has to copy, and the free pages left (negative: those missing, and
+    nothing was handed out)."""
+    _current(kv)
+    rows = new_lens.shape[0] if new_lens.dim() == 1 else 0
+    _on_device(kv, new_lens, "new_lens", torch.int32, (rows,))
+    _on_device(kv, refs, "refs", torch.int32, (kv.pages,))
+    for t, name in ((keep_lens, "keep_lens"), (parents, "parents")):
+        if t is not None:
+            _on_device(kv, t, name, torch.int32, (rows,))
+    dev = kv.k_pool.device
+    if table is None:
+        table = kv.page_table if parents is None else _new((rows, kv.stride), torch.int32, dev,
+                                                           stream)
+    if copies is None:
+        copies = _new((rows, 2), torch.int32, dev, stream)
+    if free_left is None:
+        free_left = _new((1,), torch.int32, dev, stream)
+    for t, name, shape in ((table, "table", (rows, kv.stride)), (copies, "copies", (rows, 2)),
+                           (free_left, "free_left", (1,))):
+        _on_device(kv, t, name, torch.int32, shape)
+    status = lib().kv_update_pages(
+        kv.ref(), refs.data_ptr(), None if parents is None else parents.data_ptr(), rows,
+        None if keep_lens is None else keep_lens.data_ptr(), new_lens.data_ptr(), int(window),
+        int(sinks), table.data_ptr(), copies.data_ptr(), free_left.data_ptr(),
+        _raw_stream(kv, stream))
+    if status != KV_OK:
+        raise KVError("kv_update_pages", status)
+    return table, copies, free_left
 
 
 def kv_score_pages(kv: PagedKV, q, stats, scores=None, stream=None):

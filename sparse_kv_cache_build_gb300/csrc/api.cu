@@ -477,6 +477,66 @@ kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stri
                      num_shares, out, lse, workspace, workspace_bytes, a, stream);
 }
 
+kv_status kv_compact(const kv_cache_desc* cache, const int32_t* cu_tokens, const int32_t* keep,
+                     int32_t keep_stride, const int32_t* keep_cnt, void* stats, int32_t* new_lens,
+                     cudaStream_t stream) {
+  kv_status r = check_desc(cache);
+  if (r != KV_OK) return r;
+  if (keep == nullptr || keep_stride < 1 || keep_cnt == nullptr || new_lens == nullptr ||
+      new_lens == cache->seq_lens)
+    return KV_ERR_INVALID_ARG;
+  if (!aligned16(stats)) return KV_ERR_MISALIGNED;
+  // tokens are counted in 32 bits, up to a batch of a block past the last
+  if ((int64_t)cache->page_table_stride * cache->page_size > INT32_MAX - 4096)
+    return KV_ERR_UNSUPPORTED;
+  DevCtx ctx;
+  DeviceState* st = nullptr;
+  if ((r = ctx_for_call(&ctx, &st)) != KV_OK) return r;
+  return from_cuda(launch_compact(*cache, cu_tokens, keep, keep_stride, keep_cnt, stats, new_lens,
+                                  st->sms, ctx, stream));
+}
+
+kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_t n, void* stats,
+                        cudaStream_t stream) {
+  kv_status r = check_desc(cache);
+  if (r != KV_OK) return r;
+  if (n < 0 || (n > 0 && pairs == nullptr)) return KV_ERR_INVALID_ARG;
+  if (!aligned16(stats) || (reinterpret_cast<uintptr_t>(pairs) & 7u) != 0)
+    return KV_ERR_MISALIGNED;
+  if (copy_pages_blocks(*cache, n) > INT32_MAX) return KV_ERR_UNSUPPORTED;
+  if (n == 0) return KV_OK;
+  DevCtx ctx;
+  if ((r = ctx_for_call(&ctx)) != KV_OK) return r;
+  return from_cuda(launch_copy_pages(*cache, pairs, n, stats, ctx, stream));
+}
+
+kv_status kv_update_pages(const kv_cache_desc* cache, int32_t* refs, const int32_t* parents,
+                          int32_t rows, const int32_t* keep_lens, const int32_t* new_lens,
+                          int32_t window, int32_t sinks, int32_t* table, int32_t* copies,
+                          int32_t* free_left, cudaStream_t stream) {
+  kv_status r = check_desc(cache);
+  if (r != KV_OK) return r;
+  if (refs == nullptr || new_lens == nullptr || table == nullptr || copies == nullptr ||
+      free_left == nullptr || rows < 1 || window < 0 || sinks < 0 ||
+      (parents == nullptr && rows != cache->batch))
+    return KV_ERR_INVALID_ARG;
+  if (rows > kMaxPageRows || cache->batch > kMaxPageRows) return KV_ERR_UNSUPPORTED;
+  if ((int64_t)cache->page_table_stride * cache->page_size > INT32_MAX - 256)
+    return KV_ERR_UNSUPPORTED;                     // tokens are counted in 32 bits
+  if (!aligned16(refs)) return KV_ERR_MISALIGNED;
+  // in place only where a row continues itself
+  const int64_t stride = cache->page_table_stride;
+  const uintptr_t in0 = reinterpret_cast<uintptr_t>(cache->page_table);
+  const uintptr_t out0 = reinterpret_cast<uintptr_t>(table);
+  const bool apart = out0 + (uintptr_t)rows * stride * sizeof(int32_t) <= in0 ||
+                     in0 + (uintptr_t)cache->batch * stride * sizeof(int32_t) <= out0;
+  if (!apart && (parents != nullptr || in0 != out0)) return KV_ERR_INVALID_ARG;
+  DevCtx ctx;
+  if ((r = ctx_for_call(&ctx)) != KV_OK) return r;
+  return from_cuda(launch_update_pages(*cache, refs, parents, rows, keep_lens, new_lens, window,
+                                       sinks, table, copies, free_left, ctx, stream));
+}
+
 kv_status kv_score_pages(const kv_cache_desc* cache, const void* q, int32_t num_q_heads,
                          const void* stats, float* scores, int32_t scores_stride,
                          cudaStream_t stream) {

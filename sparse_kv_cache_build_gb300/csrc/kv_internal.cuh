@@ -288,6 +288,20 @@ cudaError_t launch_append_rope(const kv_cache_desc& d, const int32_t* cu, int to
                                bool interleaved, void* q_out, int64_t q_out_stride, void* stats,
                                DevCtx ctx, cudaStream_t s);
 
+// Kept tokens moved together in place (compact.cu), copies of pages and the next page table
+// (pages.cu). cu NULL: every token of a sequence is a candidate.
+cudaError_t launch_compact(const kv_cache_desc& d, const int32_t* cu, const int32_t* keep,
+                           int keep_stride, const int32_t* keep_cnt, void* stats,
+                           int32_t* new_lens, int sms, DevCtx ctx, cudaStream_t s);
+long copy_pages_blocks(const kv_cache_desc& d, long n);       // blocks of a copy of n pages
+cudaError_t launch_copy_pages(const kv_cache_desc& d, const int32_t* pairs, int n, void* stats,
+                              DevCtx ctx, cudaStream_t s);
+constexpr int kMaxPageRows = KV_PAGES_MAX_ROWS;    // two numbers per row in the allocating block's memory
+cudaError_t launch_update_pages(const kv_cache_desc& d, int32_t* refs, const int32_t* parents,
+                                int rows, const int32_t* keep_lens, const int32_t* new_lens,
+                                int window, int sinks, int32_t* table, int32_t* copies,
+                                int32_t* free_left, DevCtx ctx, cudaStream_t s);
+
 // The single-launch decode step (bf16): cluster size for this shape on this device
 // (0 = use the four-kernel path), and its launcher.
 int fused_cluster_size(const kv_cache_desc& d, int G, int num_sms);
