@@ -268,6 +268,8 @@ kv_status packed_attn(const kv_cache_desc* cache, const void* q, int64_t q_strid
   a.Hq = num_q_heads;
   a.G = num_q_heads / cache->num_kv_heads;
   while (1 << a.log_g < a.G) ++a.log_g;
+  while (1 << a.page_log < cache->page_size) ++a.page_log;
+  a.sink_pages = a.sinks / cache->page_size + (a.sinks % cache->page_size != 0);
   a.NC = prefill_shares(num_shares, st);
   const PrefillLayout L = prefill_layout(cache, a.G, total_tokens, a.NC);
   if (L.total > 0) {

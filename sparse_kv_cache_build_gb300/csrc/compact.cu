@@ -8,8 +8,8 @@
 // In place without a copy: the slot of token i may hold the source of a token j <= i only (keep[j]
 // = i means j <= i), so a slot may be written once every source up to it has been read, and what
 // later tokens read is never overwritten early. A block owns some 16-byte columns of one KV head's
-// keys or values, so blocks need nothing of each other; it walks the tokens in batches, loads the
-// next batch, and writes the present one behind a barrier that all its loads are ordered before.
+// keys or values, so blocks need nothing of each other; it walks the tokens in batches: where they
+// come from and go to, worked out once for all columns, then all loads, a barrier, all stores.
 //
 // Bound: every moved token is read and written once. A batch costs a block one round of loads, so
 // a long list is the columns split further, down to 32 bytes a row (a sector), until there are
@@ -20,10 +20,9 @@
 namespace skv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSteps = 4;              // tokens of a thread in a batch
+constexpr int kFew = 256, kMany = 512; // threads of a block
+constexpr int kSteps = 8;              // tokens of a thread in a batch
 constexpr int kMinLanes = 2;           // 16-byte columns of a block: at least a sector
-constexpr int kBlocksPerSM = 2;
 
 struct CompactArgs {
   const int32_t* cu;                   // [batch + 1], or NULL: every token is a candidate
@@ -68,12 +67,18 @@ template <typename T> __device__ __forceinline__ void fold(Chunk<T>* mn, Chunk<T
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(NT)
 compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ CompactArgs a,
                const __grid_constant__ DevCtx ctx) {
   constexpr int ROW = D * sizeof(T) / 16;            // 16-byte columns of a token
-  __shared__ Chunk<T> sh_mn[kThreads], sh_mx[kThreads];
+  constexpr int BATCH = NT * kSteps / kMinLanes;     // tokens of a batch at most
+  // two batches of moves, later the extremes of the pages' parts
+  constexpr size_t MOVES = 2 * BATCH * sizeof(uint2), PARTS = 2 * NT * sizeof(Chunk<T>);
+  __shared__ __align__(16) uint8_t sh[MOVES > PARTS ? MOVES : PARTS];
+  uint2* moves = reinterpret_cast<uint2*>(sh);
+  Chunk<T>* sh_mn = reinterpret_cast<Chunk<T>*>(sh);
+  Chunk<T>* sh_mx = sh_mn + NT;
   pdl_trigger();
   pdl_wait();
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
@@ -81,7 +86,7 @@ compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ 
   const bool values = (int)blockIdx.x >= parts;
   const int col = (((int)blockIdx.x - (values ? parts : 0)) << a.log_lanes) +
                   (tid & ((1 << a.log_lanes) - 1));
-  const int row = tid >> a.log_lanes, rows = kThreads >> a.log_lanes;
+  const int row = tid >> a.log_lanes, rows = NT >> a.log_lanes;
   const int PS = d.page_size, Hkv = d.num_kv_heads;
   const bool first_block = blockIdx.x == 0 && g == 0;
 
@@ -104,47 +109,72 @@ compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ 
   const int32_t* table = d.page_table + (int64_t)b * d.page_table_stride;
   const int32_t* keep = a.keep + (int64_t)b * a.keep_stride;
   uint4* pool = static_cast<uint4*>(const_cast<void*>(values ? d.v_pool : d.k_pool)) + col;
-  // 16-byte index of a token's column, or -1 where its page is unmapped
-  auto place = [&](int t) -> int64_t {
-    const int P = __ldg(table + t / PS);
-    if (P >= 0 && P < d.num_phys_pages) return (((int64_t)P * Hkv + g) * PS + t % PS) * ROW;
+  // A token's slot in the pool, counted over pages (below 2^32: a slot is 256 bytes of memory and
+  // more), or kNone where its page is unmapped.
+  constexpr uint32_t kNone = ~0u;
+  const int page_log = __ffs(PS) - 1;
+  auto slot_at = [&](int P, int t) -> uint32_t {
+    if (P >= 0 && P < d.num_phys_pages) return ((uint32_t)P << page_log) + (t & (PS - 1));
     flag(ctx, KV_DEVERR_BAD_PAGE);
-    return -1;
+    return kNone;
   };
-  struct Batch {
-    int64_t to[kSteps];                              // -1: nothing to move
-    uint4 v[kSteps];
+  // where the block's column of a slot lies, in 16 bytes
+  auto place = [&](uint32_t slot) {
+    return ((((int64_t)(slot >> page_log) * Hkv + g) << page_log) + (slot & (PS - 1))) * ROW;
   };
-  auto load = [&](int i0, Batch* x) {
-    int64_t from[kSteps];
+  const int batch = kSteps * rows;
+  // Sources and places of a batch, each level of reads for all of a thread's tokens at once.
+  auto find_moves = [&](int i0, uint2* m) {
+    constexpr int MINE = kSteps / kMinLanes;
+    int k[MINE], before[MINE], from[MINE], to[MINE];
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-      const int i = i0 + u * rows + row;
-      from[u] = x->to[u] = -1;
-      if (i >= cnt) continue;
-      const int k = __ldg(keep + i);
-      // rising from k >= i on, and inside the candidates
-      if (k < i || k >= n || (i > 0 && __ldg(keep + i - 1) >= k)) {
-        flag(ctx, KV_DEVERR_BAD_SEL);
-        continue;
-      }
-      if (k == i) continue;
-      from[u] = place(start + k);
-      x->to[u] = from[u] < 0 ? -1 : place(start + i);
+    for (int u = 0; u < MINE; ++u) {
+      const int x = tid + u * NT, i = i0 + x;
+      k[u] = x < batch && i < cnt ? __ldg(keep + i) : i;         // staying where it is: no move
+      before[u] = x < batch && i < cnt && i > 0 ? __ldg(keep + i - 1) : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u)
-      if (x->to[u] >= 0) x->v[u] = __ldcg(pool + from[u]);
+    for (int u = 0; u < MINE; ++u) {
+      const int i = i0 + tid + u * NT;
+      // rising from k >= i on, and inside the candidates
+      const bool good = k[u] >= i && k[u] < n && before[u] < k[u];
+      if (!good && i < cnt && tid + u * NT < batch) flag(ctx, KV_DEVERR_BAD_SEL);
+      if (!good) k[u] = i;
+      from[u] = to[u] = -1;
+      if (k[u] != i) {
+        from[u] = __ldg(table + ((start + k[u]) >> page_log));
+        to[u] = __ldg(table + ((start + i) >> page_log));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < MINE; ++u) {
+      const int x = tid + u * NT, i = i0 + x;
+      if (x >= batch) continue;
+      uint2 move = make_uint2(kNone, kNone);
+      if (k[u] != i) {
+        move.x = slot_at(from[u], start + k[u]);
+        move.y = slot_at(to[u], start + i);
+        if (move.y == kNone) move.x = kNone;
+      }
+      m[x] = move;
+    }
   };
-  Batch now, next;
-  load(0, &now);
-  for (int i0 = 0; i0 < cnt; i0 += kSteps * rows) {
-    load(i0 + kSteps * rows, &next);
+  find_moves(0, moves);
+  for (int i0 = 0, buf = 0; i0 < cnt; i0 += batch, buf ^= 1) {
+    __syncthreads();
+    const uint2* mine = moves + buf * batch;
+    uint2 m[kSteps];
+    uint4 v[kSteps];
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      m[u] = mine[u * rows + row];
+      if (m[u].x != kNone) v[u] = __ldcg(pool + place(m[u].x));
+    }
+    if (i0 + batch < cnt) find_moves(i0 + batch, moves + (buf ^ 1) * batch);
     __syncthreads();                                 // every source up to here has been read
 #pragma unroll
     for (int u = 0; u < kSteps; ++u)
-      if (now.to[u] >= 0) pool[now.to[u]] = now.v[u];
-    now = next;
+      if (m[u].x != kNone) pool[place(m[u].y)] = v[u];
   }
   if (values || a.stats == nullptr) return;
   __syncthreads();
@@ -158,8 +188,9 @@ compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ 
   for (int q = 0; q < pages; q += at_once) {
     const int p = p0 + q + mine;
     const bool have = q + mine < pages;
-    const int64_t base = have ? place(p * PS) : -1;
-    const int valid = base < 0 ? 0 : min(PS, fresh - p * PS);
+    const uint32_t page = have ? slot_at(__ldg(table + p), 0) : kNone;
+    const int64_t base = place(page);
+    const int valid = page == kNone ? 0 : min(PS, fresh - p * PS);
     Chunk<T> mn, mx;
 #pragma unroll
     for (int e = 0; e < Chunk<T>::N; ++e) {
@@ -168,13 +199,13 @@ compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ 
     }
     // the first key starts the extremes (where it is NaN they stay so), later NaN do not count
     if (sub == 0 && valid > 0) mn = mx = unpack<T>(__ldcg(pool + base));
-    for (int t = sub == 0 ? share : sub; t < valid; t += 4 * share) {
-      uint4 v[4];
+    for (int t = sub == 0 ? share : sub; t < valid; t += 8 * share) {
+      uint4 v[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
         if (t + u * share < valid) v[u] = __ldcg(pool + base + (int64_t)(t + u * share) * ROW);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < 8; ++u)
         if (t + u * share < valid) {
           const Chunk<T> c = unpack<T>(v[u]);
           fold(&mn, &mx, c, c);
@@ -190,8 +221,8 @@ compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ 
       __syncthreads();
     }
     if (sub == 0 && valid > 0) {
-      const int P = __ldg(table + p);
-      uint4* dst = static_cast<uint4*>(a.stats) + ((int64_t)P * Hkv + g) * 2 * ROW + col;
+      uint4* dst = static_cast<uint4*>(a.stats) +
+                   ((int64_t)(page >> page_log) * Hkv + g) * 2 * ROW + col;
       dst[0] = pack<T>(mn);
       dst[ROW] = pack<T>(mx);
     }
@@ -201,14 +232,17 @@ compact_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant__ 
 template <typename T, int D>
 cudaError_t launch_t(const kv_cache_desc& d, CompactArgs a, int sms, DevCtx ctx, cudaStream_t s) {
   constexpr int ROW = D * sizeof(T) / 16;
+  // Lists of more than a batch: larger blocks, one to an SM, and their columns split as long as
+  // the blocks find an SM each.
   int lanes = ROW;
-  // split the columns while a list is more than a batch and blocks are fewer than the GPU takes
-  while (lanes > kMinLanes && (long)a.keep_stride * lanes > (long)kSteps * kThreads &&
-         2l * d.batch * d.num_kv_heads * (ROW / lanes) < (long)kBlocksPerSM * sms)
+  const bool many = (long)a.keep_stride * ROW > (long)kSteps * kFew;
+  while (many && lanes > kMinLanes && (long)a.keep_stride * lanes > (long)kSteps * kMany &&
+         4l * d.batch * d.num_kv_heads * (ROW / lanes) <= sms)
     lanes /= 2;
   while (1 << a.log_lanes < lanes) ++a.log_lanes;
   const dim3 grid(2 * ROW / lanes, d.num_kv_heads, d.batch);
-  return launch_pdl(compact_kernel<T, D>, grid, dim3(kThreads), 0, s, d, a, ctx);
+  return many ? launch_pdl(compact_kernel<T, D, kMany>, grid, dim3(kMany), 0, s, d, a, ctx)
+              : launch_pdl(compact_kernel<T, D, kFew>, grid, dim3(kFew), 0, s, d, a, ctx);
 }
 
 }  // namespace

@@ -18,6 +18,8 @@
 // closed forms inside the sequence.
 #pragma once
 
+#include <type_traits>
+
 #include "packed_rows.cuh"
 
 namespace skv {
@@ -50,6 +52,8 @@ struct PrefillArgs {
   int part_rows;          // rows of a part: a tile's, or all there are
   Mask mask;
   int window, sinks;      // kWindow: u > pos - window, or u < sinks
+  int page_log;           // log2 of the page size
+  int sink_pages;         // pages with a sink
   const int32_t* parents; // kTree: [total], a row's parent among its sequence's rows, or -1
 };
 
@@ -65,24 +69,16 @@ template <int R, int KT, int WIDE, Mask M = Mask::kCausal> struct TileShape {
 constexpr int kItemCost = 4;
 constexpr int kMinPart = 2;      // a border leaves an item at least this many key tiles
 
-// A window leaves an item whose first row is at `pos0` the tiles of the first tokens and those
-// from the window's first token on. Its key tiles are counted without the ones between: tile kt is
-// tile real_tile(kt) of the sequence.
-template <typename S> __device__ __forceinline__ int sink_tiles(const PrefillArgs& a) {
-  return a.sinks / S::keys + (a.sinks % S::keys != 0);
-}
-template <typename S> __device__ __forceinline__ int skipped(int pos0, const PrefillArgs& a) {
+// A window leaves an item whose first row is at `pos0` the pages of the first tokens and those
+// from the window's first token on. The item's keys are counted without the pages between, so that
+// its tiles are full of keys that some row sees: key x is token x among the first pages' tokens,
+// and token x + skipped pages * page_size from there on. A row at position pos is then at key
+// pos - skipped pages * page_size, and sees key x when x is not after it and less than a window
+// before it, or x < sinks: a key among the first pages' tokens that is no sink is always further
+// back, as pages are skipped only where the window begins behind them.
+template <typename S> __device__ __forceinline__ int skipped_pages(int pos0, const PrefillArgs& a) {
   if (S::mask != Mask::kWindow) return 0;
-  return max(0, max(0, pos0 - a.window + 1) / S::keys - sink_tiles<S>(a));
-}
-template <typename S>
-__device__ __forceinline__ int real_tile(int kt, int skip, const PrefillArgs& a) {
-  if (S::mask != Mask::kWindow) return kt;
-  return kt < sink_tiles<S>(a) ? kt : kt + skip;
-}
-// Whether page p holds no token that the item's rows see: such pages may have been given back.
-__device__ __forceinline__ bool dead_page(int p, int page_size, int pos0, const PrefillArgs& a) {
-  return p * page_size >= a.sinks && (p + 1) * page_size <= pos0 - a.window + 1;
+  return max(0, (max(0, pos0 - a.window + 1) >> a.page_log) - a.sink_pages);
 }
 
 // One sequence's rows as items, the same for each of its KV heads.
@@ -99,8 +95,9 @@ template <typename S> struct SeqItems {
     return min(1 << tq_log, n - (tile << tq_log));
   }
   __device__ __forceinline__ int key_tiles(int tile, const PrefillArgs& a) const {
-    const int64_t keys = (int64_t)(len - n) + (tile << tq_log) + tokens(tile);
-    return (int)((keys + S::keys - 1) / S::keys) - skipped<S>(len - n + (tile << tq_log), a);
+    const int pos0 = len - n + (tile << tq_log);
+    const int64_t keys = (int64_t)pos0 + tokens(tile) - (skipped_pages<S>(pos0, a) << a.page_log);
+    return (int)((keys + S::keys - 1) / S::keys);
   }
   __device__ __forceinline__ int unit(int tile, int log_g) const {
     return (tokens(tile) << log_g) > S::narrow ? 2 : 1;
@@ -119,7 +116,7 @@ template <typename S> struct SeqItems {
     return x * (int64_t)(a / S::keys) + steps;
   }
   // Cost of the first x tiles. All but the sequence's last tile are full: FULL units for each
-  // of ceil((past + (j + 1) TQ) / KT) key tiles, less those that the window skips.
+  // of ceil((past + (j + 1) TQ) / KT) key tiles, up to where the window skips pages.
   __device__ __forceinline__ int64_t cost(int x, const PrefillArgs& a) const {
     constexpr int FULL = S::rows > S::narrow ? 2 : 1;
     const int nt = tiles();
@@ -128,17 +125,26 @@ template <typename S> struct SeqItems {
       --x;
       c += (int64_t)unit(x, a.log_g) * key_tiles(x, a);
     }
-    c += FULL * floors(len - n + S::keys - 1, x);
-    if (S::mask == Mask::kWindow) {
-      // tile j skips max(0, floor((c0 + j TQ) / KT)): nothing before tile j0
-      const int64_t c0 = (int64_t)(len - n) - a.window + 1 - (int64_t)sink_tiles<S>(a) * S::keys;
-      const int64_t j0 = c0 >= 0 ? 0 : (-c0 + (1 << tq_log) - 1) >> tq_log;
+    if constexpr (S::mask == Mask::kWindow) {
+      // From tile j0 on pages are skipped, and a tile has its tokens, the window before them, the
+      // first pages and what lies before the window in its first page: the same for every tile, or
+      // for every second or fourth where a page is several tiles long.
+      const int TQ = 1 << tq_log, PS = 1 << a.page_log;
+      const int64_t skip_from = ((int64_t)a.sink_pages + 1) << a.page_log;    // of the window's start
+      const int64_t start0 = (int64_t)(len - n) - a.window + 1;
+      int64_t j0 = start0 >= skip_from ? 0 : (skip_from - start0 + TQ - 1) >> tq_log;
       if (j0 < x) {
-        const int first = (int)(c0 + (j0 << tq_log));
-        c -= FULL * (first / S::keys + floors(first, (int)(x - j0 - 1)));
+        const int turn_log = max(0, a.page_log - tq_log), turn = 1 << turn_log;
+        for (int r = 0; r < turn; ++r) {
+          const int64_t times = x - j0 > r ? (x - j0 - r + turn - 1) >> turn_log : 0;
+          const int64_t keys = (int64_t)TQ + a.window - 1 + ((int64_t)a.sink_pages << a.page_log) +
+                               ((start0 + ((j0 + r) << tq_log)) & (PS - 1));
+          c += FULL * times * ((keys + S::keys - 1) / S::keys);
+        }
+        x = (int)j0;
       }
     }
-    return c;
+    return c + FULL * floors(len - n + S::keys - 1, x);
   }
 };
 
@@ -150,6 +156,16 @@ struct PrefillItem {
   int kt0, kt1;
   int part;             // workspace part, or -1: the block has the whole item
 };
+// What other masks than the causal one add. Positions and keys are counted without the pages that
+// the window skips.
+struct MaskedItem : PrefillItem {
+  int skip;             // pages skipped
+  int end;              // tokens of the sequence: keys from here on are nobody's
+  int past;             // tokens before the sequence's rows
+};
+template <typename S>
+using ItemOf =
+    typename std::conditional<S::mask == Mask::kCausal, PrefillItem, MaskedItem>::type;
 
 // a / b for a >= 0, b > 0, in 32 bits where they fit: a 64-bit division is a quarter of a
 // microsecond of dependent instructions, and a block's start has several.
@@ -205,7 +221,7 @@ template <typename S> class ItemWalk {
   }
 
   // The next item with key tiles for this block; false when the piece is done.
-  __device__ __forceinline__ bool next(PrefillItem* it) {
+  __device__ __forceinline__ bool next(ItemOf<S>* it) {
     for (;;) {
       ++tile_;
       while (tile_ >= seq_.tiles()) {
@@ -230,6 +246,12 @@ template <typename S> class ItemWalk {
       it->n_tok = seq_.tokens(tile_);
       it->pos0 = seq_.len - seq_.n + t0;
       it->part = it->kt0 > 0 ? 2 * block_ : it->kt1 < nk ? 2 * block_ + 1 : -1;
+      if constexpr (S::mask != Mask::kCausal) {
+        it->skip = skipped_pages<S>(it->pos0, a_);
+        it->pos0 -= it->skip << a_.page_log;
+        it->end = seq_.len - (it->skip << a_.page_log);
+        it->past = seq_.len - seq_.n;
+      }
       return true;
     }
   }

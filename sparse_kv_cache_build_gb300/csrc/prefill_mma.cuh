@@ -102,7 +102,8 @@ template <int D> struct Cfg {
   static constexpr int BARS = 2 * STAGES + 17 + 2 * kItems;
   static constexpr size_t OFF_MISC = OFF_BAR + 8 * BARS;        // TMEM base, items, [2][128] (m, l)
   static constexpr size_t OFF_ITEMS = OFF_MISC + 8;
-  static constexpr size_t OFF_ML = OFF_ITEMS + kItems * sizeof(PrefillItem);
+  static constexpr size_t OFF_ML = OFF_ITEMS + kItems * 48;
+  static_assert(sizeof(MaskedItem) <= 48, "items");
   static constexpr size_t SMEM = OFF_ML + 1024 + 1024;          // + alignment slack
   static_assert(SMEM <= 227 * 1024 - sizeof(LineScratch), "shared memory");
   static constexpr int COL_O = 0, COL_S = 2 * D;                // TMEM: two O, two S with P over it
@@ -115,12 +116,12 @@ struct Plan {
   int n;          // key tiles of the item (or of the block's part of it)
   int n0, n1;     // key tiles of each warpgroup
 
-  __device__ __forceinline__ Plan(const PrefillItem& it, int log_g, bool few, int skip) {
+  __device__ __forceinline__ Plan(const PrefillItem& it, int log_g, bool few) {
     wide = !few && (it.n_tok << log_g) > 128;
     n = it.kt1 - it.kt0;
     if (wide) {
       // the first tile's rows end earlier: its last keys may lie a tile before the item's
-      n0 = max(0, min(n, (it.pos0 + (127 >> log_g)) / kKeys + 1 - skip - it.kt0));
+      n0 = max(0, min(n, (it.pos0 + (127 >> log_g)) / kKeys + 1 - it.kt0));
       n1 = n;
     } else {
       n0 = (n + 1) / 2;
@@ -248,6 +249,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ DevCtx ctx) {
   using C = Cfg<D>;
   using Shape = typename std::conditional<FEW, FewShape, MmaShape>::type::template With<M>;
+  using Item = ItemOf<Shape>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ LineScratch scratch;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -268,7 +270,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   uint64_t* drained = v_land + 1;                // no product in flight
   uint64_t* item_full = drained + 1;             // [kItems] an item is in shared memory
   uint64_t* item_free = item_full + kItems;      // [kItems] every warp is done with it
-  PrefillItem* items = reinterpret_cast<PrefillItem*>(sm + C::OFF_ITEMS);
+  Item* items = reinterpret_cast<Item*>(sm + C::OFF_ITEMS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_MISC);
   float* box = reinterpret_cast<float*>(sm + C::OFF_ML);          // [2][128]: m, l
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -338,14 +340,13 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       // What the tiles need of the item; it is read again for the output (its registers are
       // short while a row's 128 scores are held).
       int n, row, seen, warp_seen, step;
-      int tile = 0, stride = 0, skip = 0, past = 0;               // other masks than the causal one
+      int left = 0;          // kWindow: sinks from the tile's first key on; kTree: earlier tokens
       Ancestors line;
       bool idle;
       {
-        const PrefillItem it = items[j % kItems];
+        const Item it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
-        skip = skipped<Shape>(it.pos0, a);
-        const Plan plan(it, log_g, FEW, skip);
+        const Plan plan(it, log_g, FEW);
         n = plan.tiles(w);
         row = plan.wide ? w * 128 + r : r;
         idle = row - lane >= it.n_tok << log_g;                   // no row in this warp
@@ -354,24 +355,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         seen = it.pos0 + (row >> log_g) - u0;
         warp_seen = it.pos0 + ((row - lane) >> log_g) - u0;
         step = plan.wide ? kKeys : 2 * kKeys;
-        if (M != Mask::kCausal) {
-          tile = it.kt0 + plan.tile(w, 0);
-          stride = plan.wide ? 1 : 2;
-        }
-        if (M == Mask::kWindow) {                                 // from the sequence's first token
-          seen = it.pos0 + (row >> log_g);
-          warp_seen = it.pos0 + ((row - lane) >> log_g);
-        }
-        if (M == Mask::kTree) {
+        if (M == Mask::kWindow) left = a.sinks - u0;
+        if constexpr (M == Mask::kTree) {
+          left = it.past - u0;
           // the copy that left from the warp's buffer has read it
           if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           __syncwarp();
-          const int first = pr.cu != nullptr ? pr.cu[it.b] : it.b, t0 = it.row0 - first;
-          past = it.pos0 - t0;
+          const int t0 = it.pos0 - it.past;                       // the item's first row
           line.words = reinterpret_cast<uint32_t*>(sm + C::OFF_OUT + warp * 4096) + lane * 32;
           line.last = -1;
           if (!idle && n > 0)
-            line.walk(ctx, a.parents + first, t0 + min(row >> log_g, it.n_tok - 1));
+            line.walk(ctx, a.parents + it.row0 - t0, t0 + min(row >> log_g, it.n_tok - 1));
         }
       }
       float m = -INFINITY, l = 0.f;
@@ -388,40 +382,34 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           tc::wait_ld();
 #pragma unroll
           for (int c = 0; c < 4; ++c) tc::after_wait(s + 32 * c);
-          if constexpr (M == Mask::kCausal) {
-            if (warp_seen < kKeys - 1) {                          // on the border
+          // every row of the warp sees the whole tile
+          const bool all =
+              M == Mask::kTree ? left >= kKeys
+                               : warp_seen >= kKeys - 1 &&
+                                     (M == Mask::kCausal || left >= kKeys ||
+                                      warp_seen + (31 >> log_g) < a.window);
+          if (!all) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (warp_seen < 32 * q + 31) {
-                  const int last = seen - 32 * q;
-                  const uint32_t keep = last >= 31 ? ~0u : last < 0 ? 0u : (2u << last) - 1u;
-#pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    if ((keep >> c & 1u) == 0u) s[32 * q + c] = 0xff800000u;
-                }
-            }
-            seen -= step;
-            warp_seen -= step;
-          } else {
-            const int u0 = real_tile<Shape>(tile, skip, a) * kKeys;
-            // every row of the warp sees the whole tile
-            const bool all = M == Mask::kTree ? u0 + kKeys <= past
-                : u0 + kKeys - 1 <= warp_seen &&
-                      (u0 > warp_seen + (31 >> log_g) - a.window || u0 + kKeys <= a.sinks);
-            if (!all) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int v0 = u0 + 32 * q;
-                const uint32_t keep = M == Mask::kTree ? line.seen(v0 - past)
-                    : low_bits(seen + 1 - v0) &
-                          (~low_bits(seen + 1 - a.window - v0) | low_bits(a.sinks - v0));
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if ((keep >> c & 1u) == 0u) s[32 * q + c] = 0xff800000u;
+            for (int q = 0; q < 4; ++q) {
+              uint32_t keep;
+              if constexpr (M == Mask::kCausal) {
+                if (warp_seen >= 32 * q + 31) continue;
+                const int last = seen - 32 * q;
+                keep = last >= 31 ? ~0u : last < 0 ? 0u : (2u << last) - 1u;
+              } else if constexpr (M == Mask::kWindow) {
+                const int upto = seen + 1 - 32 * q;
+                keep = low_bits(upto) & (~low_bits(upto - a.window) | low_bits(left - 32 * q));
+              } else {
+                keep = line.seen(32 * q - left);
               }
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if ((keep >> c & 1u) == 0u) s[32 * q + c] = 0xff800000u;
             }
-            tile += stride;
           }
+          seen -= step;
+          warp_seen -= step;
+          if (M != Mask::kCausal) left -= step;
           float top[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -496,7 +484,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok) break;
       // ---- output
       const PrefillItem it = items[j % kItems];
-      const Plan plan(it, log_g, FEW, skipped<Shape>(it.pos0, a));
+      const Plan plan(it, log_g, FEW);
       const int rows = it.n_tok << log_g, warp_row = row - lane;
       const bool join = !plan.wide && plan.n1 > 0;
       if (n > 0) ok = wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
@@ -630,8 +618,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   } else {
     tc::fewer_regs<kRegsOther>();
     auto uniform_plan = [&](int j) {
-      const PrefillItem& it = items[j % kItems];
-      Plan plan(it, log_g, FEW, skipped<Shape>(it.pos0, a));
+      Plan plan(items[j % kItems], log_g, FEW);
       if (!FEW) plan.wide = uniform(plan.wide);
       plan.n = uniform(plan.n);
       plan.n0 = uniform(plan.n0);
@@ -780,6 +767,11 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       for (int j = 0; ok && plan.n > 0; ++j) {
         const int most = max(plan.n0, plan.n1);
         bool early = false;
+        int it_end = 0;                                // keys there are from the item's first tile on
+        if constexpr (M != Mask::kCausal) {
+          const Item& it = items[j % kItems];
+          it_end = it.end - it.kt0 * kKeys;
+        }
 #pragma unroll 1
         for (int i = 0; ok && i < most; ++i) {
           if (i == most - 1) {
@@ -796,7 +788,20 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             // The tile's scores are there: so is every tile before, whose barriers' phases (of
             // two kinds) could otherwise be taken for those waited for here.
             wait(s_full + w, tiles & 1);
-            wait_slot(base + plan.v_slot(plan.tile(w, i)));
+            const int v_slot = base + plan.v_slot(plan.tile(w, i));
+            wait_slot(v_slot);
+            if constexpr (M != Mask::kCausal) {
+              // the V rows behind the sequence's end become zeros, before the first product reads them
+              const int valid = it_end - plan.tile(w, i) * kKeys;
+              if (ok && valid < kKeys && (!plan.wide || w == 0 || i >= plan.n0)) {
+                uint8_t* tile = ring + v_slot % C::STAGES * C::TILE_BYTES;
+                for (int x = valid * 8 + lane; x < kKeys * 8; x += 32)
+#pragma unroll
+                  for (int h = 0; h < C::HALVES; ++h)
+                    *reinterpret_cast<uint4*>(tile + h * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
+                tc::fence_async_smem();
+              }
+            }
             if (i == 0 && before > 0) wait(o_free + w, (before - 1) & 1);     // it has been read
             if (!ok) continue;
             say(p_half + w);
@@ -828,20 +833,23 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       for (int j = 0;; ++j) {
         ok = ok && item_ready(j);
         if (!ok) break;
-        const PrefillItem it = items[j % kItems];
+        const Item it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
         item_done(j);
-        const int skip = skipped<Shape>(it.pos0, a);
-        const Plan plan(it, log_g, FEW, skip);
+        const Plan plan(it, log_g, FEW);
         const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
-        const int keys = it.pos0 + it.n_tok;         // keys from here on are nobody's
+        // Keys from here on are nobody's. (With another mask: the sequence's end, as all its tokens
+        // are cached and finite; only the tile that ends the sequence then needs zeros.)
+        int keys = it.pos0 + it.n_tok;
+        if constexpr (M != Mask::kCausal) keys = it.end;
         const int pages = (int)(((int64_t)keys + PS - 1) / PS);
         // The table's entries 32 at a time, one to a lane: those of the tile being loaded, the
         // ones before (V tiles come up to two tiles after their K tile) and the ones ahead.
         auto entries = [&](int chunk) {
-          const int p = chunk * 32 + lane;
+          int p = chunk * 32 + lane;
           int P = -1;
-          if (p < pages && !(M == Mask::kWindow && dead_page(p, PS, it.pos0, a))) {
+          if (p < pages) {
+            if constexpr (M == Mask::kWindow) p += p < a.sink_pages ? 0 : it.skip;
             P = __ldg(table + p);
             if (P < 0 || P >= d.num_phys_pages) {
               flag(ctx, KV_DEVERR_BAD_PAGE);
@@ -850,37 +858,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
           }
           return P;
         };
-        int chunk = real_tile<Shape>(it.kt0, skip, a) * per_tile / 32;
+        int chunk = it.kt0 * per_tile / 32;
         int e0 = -1, e1 = entries(chunk), e2 = entries(chunk + 1);
-        int last_page = -1, page_before = -1;        // window: those of the last two K tiles
         auto load = [&](bool values, int t) {
           if (!ok) return;
-          const int kt = real_tile<Shape>(it.kt0 + t, skip, a), first = kt * per_tile;
-          int P;
-          if constexpr (M == Mask::kWindow) {
-            // The tiles jump over what the window skips, so a V tile takes its pages from its K
-            // tile, the last one loaded or the one before.
-            if (!values) {
-              if (first / 32 == chunk + 1) {
-                e1 = e2;
-                e2 = entries(++chunk + 1);
-              } else if (first / 32 != chunk) {
-                chunk = first / 32;
-                e1 = entries(chunk);
-                e2 = entries(chunk + 1);
-              }
-              page_before = last_page;
-              last_page = __shfl_sync(0xffffffffu, e1, (first + page) & 31);
-            }
-            P = !values || plan.wide || t == plan.n - 1 ? last_page : page_before;
-          } else {
-            if (first / 32 > chunk) {
-              e0 = e1;
-              e1 = e2;
-              e2 = entries(++chunk + 1);
-            }
-            P = __shfl_sync(0xffffffffu, first / 32 == chunk ? e1 : e0, (first + page) & 31);
+          const int first = (it.kt0 + t) * per_tile;
+          if (first / 32 > chunk) {
+            e0 = e1;
+            e1 = e2;
+            e2 = entries(++chunk + 1);
           }
+          int P = __shfl_sync(0xffffffffu, first / 32 == chunk ? e1 : e0, (first + page) & 31);
           if (lane >= copies) P = -1;
           const int slot = used;
           const int stage = slot % C::STAGES;
@@ -888,24 +876,10 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             ok = wait_bounded(empty + stage, (slot / C::STAGES - 1) & 1, ctx.wait_ns);
           if (!ok) return;
           // the item's last key lies inside this tile: the V rows after it become zeros
-          const int valid = min(kKeys, keys - kt * kKeys);
-          const bool tail = values && valid < kKeys;
+          // (with another mask: by the ready warp)
+          const int valid = min(kKeys, keys - (it.kt0 + t) * kKeys);
+          const bool tail = M == Mask::kCausal && values && valid < kKeys;
           uint64_t* land = tail ? v_land : full + stage;
-          if (M == Mask::kWindow && values) {
-            // pages that nobody sees are not read: their rows become zeros too
-            const uint32_t dead =
-                __ballot_sync(0xffffffffu, lane < per_tile && dead_page(first + page, PS, it.pos0, a));
-            if (dead != 0) {
-              uint8_t* rows = ring + stage * C::TILE_BYTES;
-              for (int i = lane; i < kKeys * 8; i += 32)
-                if (dead >> (i / 8 / PS) & 1u)
-#pragma unroll
-                  for (int h = 0; h < C::HALVES; ++h)
-                    *reinterpret_cast<uint4*>(rows + h * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-              tc::fence_async_smem();
-              __syncwarp();
-            }
-          }
           const int boxes = __popc(__ballot_sync(0xffffffffu, P >= 0));
           if (lane == 0) mbar_arrive_expect_tx(land, boxes * box_bytes);
           __syncwarp();
@@ -954,7 +928,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (lane == 0 && a.notes != nullptr) a.notes[blockIdx.x] = walk.border();
       bool ok = true;
       int loaded[2] = {0, 0};
-      PrefillItem it, next{};
+      Item it, next{};
       int open[kItems] = {};                         // key tiles of the last items published
       auto patience = [&]() {
         unsigned long long tiles = 1;
@@ -979,7 +953,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         it = next;
         publish(j + 1);
         if (!ok) break;
-        const Plan plan(it, log_g, FEW, skipped<Shape>(it.pos0, a));
+        const Plan plan(it, log_g, FEW);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || plan.tiles(w) == 0) continue;

@@ -94,15 +94,14 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
   const float* vp = static_cast<const float*>(d.v_pool);
   const int turn = 16 * (ty & 1);            // the two rows of a warp's read in different banks
 
-  PrefillItem it;
+  ItemOf<Shape> it;
   while (walk.next(&it)) {
     const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
     const int rows = it.n_tok << a.log_g, keys = it.pos0 + it.n_tok;
-    const int skip = skipped<Shape>(it.pos0, a);
     int past = 0;                            // kTree: tokens before the drafted rows
-    if (M == Mask::kTree) {
-      const int first = pr.cu != nullptr ? pr.cu[it.b] : it.b, t0 = it.row0 - first;
-      past = it.pos0 - t0;
+    if constexpr (M == Mask::kTree) {
+      past = it.past;
+      const int t0 = it.pos0 - past, first = it.row0 - t0;
       // row r's line of ancestors (read only after the tiles' barriers)
       for (int r = tid; r < rows; r += kThreads) {
         const int32_t* up = a.parents + first;
@@ -128,16 +127,16 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
     };
     // keys past the item's last are zeros: whatever their slots hold stays out of the sums
     auto stage_tile = [&](int kt, int buf) {
-      const int u0 = real_tile<Shape>(kt, skip, a) * KT;
+      const int u0 = kt * KT;
       float* dst = ring + 2 * buf * KT * LD;
       for (int which = 0; which < 2; ++which) {
         const float* pool = which == 0 ? kp : vp;
         stage_rows<D>(dst + which * KT * LD, KT, pool, [&](int i) -> const float* {
           if (i >= keys - u0) return nullptr;
           const int u = u0 + i;
-          // pages that nobody sees may have been given back
-          if (M == Mask::kWindow && dead_page(u / PS, PS, it.pos0, a)) return nullptr;
-          const int P = table[u / PS];
+          int p = u / PS;
+          if constexpr (M == Mask::kWindow) p += p < a.sink_pages ? 0 : it.skip;
+          const int P = table[p];
           if (P < 0 || P >= d.num_phys_pages) {
             flag(ctx, KV_DEVERR_BAD_PAGE);
             return nullptr;
@@ -164,7 +163,7 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
     }
 
     for (int kt = it.kt0; kt < it.kt1; ++kt) {
-      const int buf = (kt - it.kt0) & 1, u0 = real_tile<Shape>(kt, skip, a) * KT;
+      const int buf = (kt - it.kt0) & 1, u0 = kt * KT;
       if (kt + 1 < it.kt1) {
         stage_tile(kt + 1, buf ^ 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
