@@ -308,7 +308,7 @@ kv_status kv_window_attn(const kv_cache_desc* cache, const void* q, int64_t q_st
  * itself. A parent that is neither is flagged (KV_DEVERR_BAD_SEL) and taken as -1. Sequences of
  * more than KV_TREE_MAX_NODES rows are flagged (KV_DEVERR_BAD_LEN) and left out. Arguments,
  * workspace (kv_prefill_attn_workspace_size), rounding, flags and limits are otherwise
- * kv_prefill_attn's, whose results a tree that is one line has, bit for bit.
+ * kv_prefill_attn's; a tree that is one line gives its results up to the rounding of its sums.
  */
 #define KV_TREE_MAX_NODES 1024
 kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stride,

@@ -58,15 +58,15 @@ struct PrefillArgs {
 };
 
 // Tile sizes of a kernel: R rows by KT keys, and what an item costs: two units per key tile, one
-// where the item has at most WIDE rows, and a fixed part of kItemCost units (bf16: an item's start
+// where the item has at most WIDE rows, and a fixed part of item_cost units (bf16: an item's start
 // and end are 5000 to 9000 cycles, a unit 1300; 3, 4, 5 and 8 give 240, 242, 247 and 257 us for
 // sixteen ragged prompts, and 351, 345, 345 and 350 for one of 8192 tokens in pages of 64).
-template <int R, int KT, int WIDE, Mask M = Mask::kCausal> struct TileShape {
-  static constexpr int rows = R, keys = KT, narrow = WIDE;
+template <int R, int KT, int WIDE, Mask M = Mask::kCausal, int COST = 4> struct TileShape {
+  static constexpr int rows = R, keys = KT, narrow = WIDE, item_cost = COST;
   static constexpr Mask mask = M;
-  template <Mask N> using With = TileShape<R, KT, WIDE, N>;
+  static constexpr bool called = R == 32;
+  template <Mask N> using With = TileShape<R, KT, WIDE, N, COST>;
 };
-constexpr int kItemCost = 4;
 constexpr int kMinPart = 2;      // a border leaves an item at least this many key tiles
 
 // A window leaves an item whose first row is at `pos0` the pages of the first tokens and those
@@ -118,12 +118,23 @@ template <typename S> struct SeqItems {
   // Cost of the first x tiles. All but the sequence's last tile are full: FULL units for each
   // of ceil((past + (j + 1) TQ) / KT) key tiles, up to where the window skips pages.
   __device__ __forceinline__ int64_t cost(int x, const PrefillArgs& a) const {
+    if constexpr (S::called) return called_cost(*this, x, &a);
+    else return sum_of_tiles(x, a);
+  }
+  // One copy of the code for all its callers: the start of a block that runs it once or twice is
+  // bound by fetching instructions. (A kernel that moves registers between its warps can have no
+  // calls.)
+  static __device__ __noinline__ int64_t called_cost(SeqItems s, int x, const PrefillArgs* a) {
+    return s.sum_of_tiles(x, *a);
+  }
+  __device__ __forceinline__ int64_t sum_of_tiles(int x, const PrefillArgs& a) const {
     constexpr int FULL = S::rows > S::narrow ? 2 : 1;
     const int nt = tiles();
-    int64_t c = (int64_t)kItemCost * x;
+    int64_t c = (int64_t)S::item_cost * x;
     if (x == nt && x > 0) {
       --x;
       c += (int64_t)unit(x, a.log_g) * key_tiles(x, a);
+      if (S::mask != Mask::kCausal && x == 0) return c;
     }
     if constexpr (S::mask == Mask::kWindow) {
       // From tile j0 on pages are skipped, and a tile has its tokens, the window before them, the
@@ -176,8 +187,9 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
 
 // Key tiles of an item before border `y` of the line; the item starts at x and costs `unit`
 // per key tile. Borders that would leave a few tiles on one side move to the item's end.
+template <typename S>
 __device__ __forceinline__ int tiles_before(int64_t y, int64_t x, int nk, int unit) {
-  const int64_t k = (y - x - kItemCost + unit - 1) >> (unit - 1);       // unit is 1 or 2
+  const int64_t k = (y - x - S::item_cost + unit - 1) >> (unit - 1);       // unit is 1 or 2
   if (k >= nk) return nk;
   return k < kMinPart ? 0 : nk - k < kMinPart ? nk : (int)k;
 }
@@ -235,9 +247,9 @@ template <typename S> class ItemWalk {
       if (x_ >= hi_) return false;
       const int nk = seq_.key_tiles(tile_, a_), unit = seq_.unit(tile_, a_.log_g);
       const int64_t x = x_;
-      x_ += kItemCost + (int64_t)unit * nk;
-      it->kt0 = tiles_before(lo_, x, nk, unit);
-      it->kt1 = tiles_before(hi_, x, nk, unit);
+      x_ += S::item_cost + (int64_t)unit * nk;
+      it->kt0 = tiles_before<S>(lo_, x, nk, unit);
+      it->kt1 = tiles_before<S>(hi_, x, nk, unit);
       if (it->kt0 >= it->kt1) continue;
       it->b = b_;
       it->g = g_;
@@ -265,8 +277,8 @@ template <typename S> class ItemWalk {
     n.n_tok = seq_.tokens(t);
     n.g = g_;
     n.nk = seq_.key_tiles(t, a_);
-    n.kt0 = tiles_before(lo_, x_, n.nk, seq_.unit(t, a_.log_g));
-    n.kt1 = tiles_before(hi_, x_, n.nk, seq_.unit(t, a_.log_g));
+    n.kt0 = tiles_before<S>(lo_, x_, n.nk, seq_.unit(t, a_.log_g));
+    n.kt1 = tiles_before<S>(hi_, x_, n.nk, seq_.unit(t, a_.log_g));
     return n;
   }
 
@@ -346,6 +358,7 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
 // Launchers.
 using MmaShape = TileShape<256, 128, 128>;       // bf16, tensor cores
 using FewShape = TileShape<128, 128, 128>;       // the same for batches of few rows
+using SwapShape = TileShape<32, 128, 32, Mask::kCausal, 3>;        // and where keys take the rows' place
 using SimtShape = TileShape<128, 64, 0>;         // fp32, CUDA cores
 int prefill_tile_rows(int dtype);
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
@@ -353,6 +366,9 @@ cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
 template <Mask M>
 cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
                                 const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
+template <Mask M>       // batches of few rows, with another mask than the causal one
+cudaError_t launch_prefill_few(const kv_cache_desc& d, const PackedRows& pr,
+                               const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
 template <Mask M>
 cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s);

@@ -117,9 +117,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
 }
 
 // Instruction descriptor: float32 accumulators, bf16 operands, M = 128 rows, N columns; B is
-// given as N rows of K elements, or as K rows of N elements (transposed).
-__host__ __device__ constexpr uint32_t idesc(int n, bool b_transposed) {
-  return 1u << 4 | 1u << 7 | 1u << 10 | (b_transposed ? 1u << 16 : 0u) |
+// given as N rows of K elements, or as K rows of N elements (transposed), and A likewise.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_transposed, bool a_transposed = false) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (a_transposed ? 1u << 15 : 0u) |
+         (b_transposed ? 1u << 16 : 0u) |
          (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 

@@ -105,6 +105,55 @@ def test_window(new, past, dtype, D, G, PS, shares, window, sinks):
     c.check_attn(c.q, out, lse)
 
 
+# batches of few rows (32 to a sequence on average, heads counted), whose items have 32 rows: some
+# of the batch may have more, cut into several items
+FEW = [
+    # new, past, dtype, D, G, PS, shares
+    ((1,), (0,), "bf16", 128, 1, 16, 0),
+    ((1,), (5,), "bf16", 64, 8, 64, 0),
+    ((4,), (3000,), "bf16", 128, 8, 16, 0),
+    ((8,), (3001,), "bf16", 64, 4, 32, 0),
+    ((32,), (700,), "bf16", 128, 1, 64, 5),
+    ((32,), (700,), "bf16", 64, 1, 16, 0),
+    ((16, 0, 3, 16, 9), (0, 40, 127, 128, 1000), "bf16", 128, 2, 16, 3),
+    ((1, 1, 1, 1, 1, 1, 40), (0, 15, 16, 127, 128, 1400, 900), "bf16", 128, 4, 32, 0),
+    ((1, 1, 1, 1, 1, 1, 40), (0, 15, 16, 127, 128, 1400, 900), "bf16", 64, 4, 16, 2),
+    ((2, 2, 2, 2), (62, 190, 254, 4094), "bf16", 64, 8, 16, 40),
+    (tuple(1 + i % 3 for i in range(40)), tuple((131 * i) % 1500 for i in range(40)), "bf16", 128,
+     8, 16, 0),
+    (tuple(1 + i % 3 for i in range(40)), tuple((131 * i) % 1500 for i in range(40)), "bf16", 64,
+     2, 64, 0),
+]
+
+
+@pytest.mark.parametrize("new,past,dtype,D,G,PS,shares", FEW)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 4), (1000, 300), (10 ** 6, 0)])
+def test_window_of_few_rows(new, past, dtype, D, G, PS, shares, window, sinks):
+    test_window(new, past, dtype, D, G, PS, shares, window, sinks)
+
+
+@pytest.mark.parametrize("new,past,dtype,D,G,PS,shares", FEW)
+def test_tree_of_few_rows(new, past, dtype, D, G, PS, shares):
+    test_tree(new, past, dtype, D, G, PS, shares)
+
+
+def test_few_rows_whose_maximum_keeps_growing():
+    """Keys that grow along the sequence: the reference moves, and what was summed is rescaled."""
+    for D, G in ((128, 4), (64, 8)):
+        for kind in ("window", "tree"):
+            c = Masked((1, 4), (1500, 2000), "bf16", D, G, window=1200 if kind == "window" else None,
+                       sinks=3, parents=[[-1], bush(4, 2)] if kind == "tree" else None)
+            grow = torch.linspace(0.1, 6.0, c.PS, device="cuda")
+            for b, n in enumerate(c.lens):
+                for p in range(-(-n // c.PS)):
+                    c.k_pool[c.table[b, p].long()] *= (grow * (1 + p / 8))[None, :, None].to(
+                        c.k_pool.dtype)
+            c.clean = (f64(c.k_pool), f64(c.v_pool), c.clean[2])
+            out, lse = c.attend()
+            assert_no_device_error()
+            c.check_attn(c.q, out, lse)
+
+
 def test_window_of_single_tokens_without_offsets():
     """One row per sequence; the row of an empty sequence is zeros."""
     c = Masked((1, 1, 1, 1), (5000, 130, 77, 4096), G=8, window=300, sinks=4)
