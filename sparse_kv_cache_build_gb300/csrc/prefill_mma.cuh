@@ -110,25 +110,44 @@ template <int D> struct Cfg {
 
 // An item's plan: which key tiles each warpgroup takes and where they lie in the ring, counted
 // from the item's first slot.
-struct Plan {
+// AHEAD (a window at D = 64, whose ring holds four tiles of keys and values): where the second row
+// tile's window begins behind the first key tile, the second warpgroup begins with the second one
+// and stays a tile ahead. Both then have as many tiles, where the first's rows end a tile earlier,
+// and the next item's scores can follow at once.
+template <bool AHEAD> struct Plan {
   bool wide;      // two row tiles; else one, with the key tiles dealt out in turn
   int n;          // key tiles of the item (or of the block's part of it)
   int n0, n1;     // key tiles of each warpgroup
+  int ahead;      // key tiles that the second warpgroup leaves out at the start: 0 or 1
 
-  __device__ __forceinline__ Plan(const PrefillItem& it, int log_g, bool few) {
+  __device__ __forceinline__ Plan(const PrefillItem& it, const PrefillArgs& a, bool few) {
+    const int log_g = a.log_g;
     wide = !few && (it.n_tok << log_g) > 128;
     n = it.kt1 - it.kt0;
+    ahead = 0;
     if (wide) {
       // the first tile's rows end earlier: its last keys may lie a tile before the item's
       n0 = max(0, min(n, (it.pos0 + (127 >> log_g)) / kKeys + 1 - it.kt0));
       n1 = n;
+      if (AHEAD) {
+        ahead = a.sinks <= it.kt0 * kKeys &&
+                it.pos0 + (128 >> log_g) - a.window + 1 >= (it.kt0 + 1) * kKeys;
+        n1 -= ahead;
+      }
     } else {
       n0 = (n + 1) / 2;
       n1 = n / 2;
     }
   }
   __device__ __forceinline__ int tiles(int w) const { return w == 0 ? n0 : n1; }
-  __device__ __forceinline__ int tile(int w, int i) const { return wide ? i : 2 * i + w; }
+  __device__ __forceinline__ int tile(int w, int i) const {
+    return wide ? i + (AHEAD && w == 1 ? ahead : 0) : 2 * i + w;
+  }
+  // Whether warpgroup w is the last to read tile t's keys, or values.
+  __device__ __forceinline__ bool last_reader(int w, int t) const {
+    if (AHEAD && wide && ahead) return w == 0 || t >= n0;
+    return !wide || w == 1;
+  }
   // Ring slots in the order of first use: K0 V0 K1 V1 ..., or (dealt out) K0 K1 V0 K2 V1 K3 ...
   __device__ __forceinline__ int k_slot(int t) const {
     return wide ? 2 * t : t < 2 ? t : 2 * t - 1;
@@ -201,6 +220,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   using C = Cfg<D>;
   using Shape = typename std::conditional<FEW, FewShape, MmaShape>::type::template With<M>;
   using Item = ItemOf<Shape>;
+  using Plan = skv::Plan<M == Mask::kWindow && C::STAGES >= 8>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ LineScratch scratch;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -297,7 +317,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       {
         const Item it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
-        const Plan plan(it, log_g, FEW);
+        const Plan plan(it, a, FEW);
         n = plan.tiles(w);
         row = plan.wide ? w * 128 + r : r;
         idle = row - lane >= it.n_tok << log_g;                   // no row in this warp
@@ -435,7 +455,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
       if (!ok) break;
       // ---- output
       const PrefillItem it = items[j % kItems];
-      const Plan plan(it, log_g, FEW);
+      const Plan plan(it, a, FEW);
       const int rows = it.n_tok << log_g, warp_row = row - lane;
       const bool join = !plan.wide && plan.n1 > 0;
       if (n > 0) ok = wait_bounded(o_done + w, items_seen & 1, ctx.wait_ns);
@@ -569,16 +589,17 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
   } else {
     tc::fewer_regs<kRegsOther>();
     auto uniform_plan = [&](int j) {
-      Plan plan(items[j % kItems], log_g, FEW);
+      Plan plan(items[j % kItems], a, FEW);
       if (!FEW) plan.wide = uniform(plan.wide);
       plan.n = uniform(plan.n);
       plan.n0 = uniform(plan.n0);
       plan.n1 = uniform(plan.n1);
+      plan.ahead = uniform(plan.ahead);
       return plan;
     };
     // The next item's first scores can be issued with the last of this one's products.
     auto runs_on = [](const Plan& plan, const Plan& next) {
-      return plan.wide && plan.n0 == plan.n1 && next.wide && next.n0 > 0;
+      return plan.wide && plan.n0 == plan.n1 && next.wide && next.n0 > 0 && next.n1 > 0;
     };
     if (warp == kMmaWarp) {
       // ---- products. The time between two batches of them is lost to the tensor core, so this
@@ -622,12 +643,12 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll 1
           for (int w = 0; w < 2; ++w) {
             if (!ok || plan.tiles(w) == 0) continue;
-            const int slot = base + plan.k_slot(plan.tile(w, 0));
+            const int t = plan.tile(w, 0), slot = base + plan.k_slot(t);
             wait(q_full + w, (w == 0 ? items0 : items1) & 1);
             wait(full + slot % C::STAGES, (slot / C::STAGES) & 1);
             if (!ok) continue;
             tc::fence_after();
-            if (tc::elect()) scores(w, slot, !plan.wide || w == 1, plan.tiles(w) == 1);
+            if (tc::elect()) scores(w, slot, plan.last_reader(w, t), plan.tiles(w) == 1);
             __syncwarp();
           }
         }
@@ -644,11 +665,12 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll kUnroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || i >= plan.tiles(w)) continue;
-            const int slot = base + plan.v_slot(plan.tile(w, i));
+            const int t = plan.tile(w, i), slot = base + plan.v_slot(t);
             const int tiles = w == 0 ? tiles0++ : tiles1++;
             const bool more = i + 1 < plan.tiles(w), go_on = more || early;
-            const int k_slot = more ? base + plan.k_slot(plan.tile(w, i + 1)) : base + 2 * plan.n;
-            const bool done = !plan.wide || w == 1;
+            const int k_slot = more ? base + plan.k_slot(plan.tile(w, i + 1))
+                                    : base + 2 * plan.n + next.k_slot(next.tile(w, 0));
+            const bool done = plan.last_reader(w, t);
             const bool last = more ? i + 2 == plan.tiles(w) : next.tiles(w) == 1;
             constexpr uint32_t id = tc::idesc(D, true);
             const uint64_t vd = v_desc + (uint64_t)(slot % C::STAGES * (C::TILE_BYTES >> 4));
@@ -676,7 +698,10 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
               values(1);
               if (!more) tc::commit(o_done + w);
               if (done) tc::commit(empty + slot % C::STAGES);
-              if (go_on) scores(w, k_slot, more ? done : w == 1, last);
+              if (go_on)
+                scores(w, k_slot,
+                       more ? plan.last_reader(w, plan.tile(w, i + 1))
+                            : next.last_reader(w, next.tile(w, 0)), last);
             }
             __syncwarp();
           }
@@ -744,7 +769,9 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             if constexpr (M != Mask::kCausal) {
               // the V rows behind the sequence's end become zeros, before the first product reads them
               const int valid = it_end - plan.tile(w, i) * kKeys;
-              if (ok && valid < kKeys && (!plan.wide || w == 0 || i >= plan.n0)) {
+              // (by whoever comes to them first)
+              if (ok && valid < kKeys &&
+                  (!plan.wide || (plan.ahead ? w == 1 : w == 0 || i >= plan.n0))) {
                 uint8_t* tile = ring + v_slot % C::STAGES * C::TILE_BYTES;
                 for (int x = valid * 8 + lane; x < kKeys * 8; x += 32)
 #pragma unroll
@@ -758,7 +785,8 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
             say(p_half + w);
             if (more || early) {
               if (!more) wait(q_full + w, (before + 1) & 1);
-              wait_slot(more ? base + plan.k_slot(plan.tile(w, i + 1)) : base + 2 * plan.n);
+              wait_slot(more ? base + plan.k_slot(plan.tile(w, i + 1))
+                             : base + 2 * plan.n + next.k_slot(next.tile(w, 0)));
               if (!ok) continue;
             }
             say(p_full + w);
@@ -787,7 +815,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         const Item it = items[j % kItems];
         if (it.kt0 >= it.kt1) break;
         item_done(j);
-        const Plan plan(it, log_g, FEW);
+        const Plan plan(it, a, FEW);
         const int32_t* table = d.page_table + (int64_t)it.b * d.page_table_stride;
         // Keys from here on are nobody's. (With another mask: the sequence's end, as all its tokens
         // are cached and finite; only the tile that ends the sequence then needs zeros.)
@@ -904,7 +932,7 @@ prefill_mma_kernel(const __grid_constant__ CUtensorMap map_k,
         it = next;
         publish(j + 1);
         if (!ok) break;
-        const Plan plan(it, log_g, FEW);
+        const Plan plan(it, a, FEW);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || plan.tiles(w) == 0) continue;

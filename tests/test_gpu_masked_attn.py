@@ -105,6 +105,16 @@ def test_window(new, past, dtype, D, G, PS, shares, window, sinks):
     c.check_attn(c.q, out, lse)
 
 
+@pytest.mark.parametrize("G", [1, 2])
+@pytest.mark.parametrize("window", [1, 63, 64, 127, 128, 129, 130, 192, 256, 257, 383, 500])
+@pytest.mark.parametrize("shares", [0, 1, 5])
+def test_window_whose_row_tiles_begin_apart(G, window, shares):
+    """At D = 64 the second tile of rows may begin a key tile later than the first."""
+    for new, past, sinks, PS in (((900, 333, 129), (0, 700, 64), 0, 16), ((1024,), (2000,), 0, 64),
+                                 ((600, 200), (300, 1000), 5, 32)):
+        test_window(new, past, "bf16", 64, G, PS, shares, window, sinks)
+
+
 # batches of few rows (32 to a sequence on average, heads counted), whose items have 32 rows: some
 # of the batch may have more, cut into several items
 FEW = [
