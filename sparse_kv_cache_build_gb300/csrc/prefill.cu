@@ -121,9 +121,10 @@ constexpr int kMergeFewRows = 64;
 
 template <typename T, int D, int V>
 cudaError_t merge_v(const PrefillArgs& a, cudaStream_t s) {
-  const int units = a.part_rows * (D / (32 * V));
+  // few rows with many parts: a unit per warp, as one after the other they are the call's end
+  const int units = a.part_rows * (D / (32 * V)), per_warp = V == 1 ? 1 : kMergeUnits;
   return launch_pdl(prefill_merge_kernel<T, D, V>,
-                    dim3(a.NC - 1, ceil_div(units, kMergeWarps * kMergeUnits)),
+                    dim3(a.NC - 1, ceil_div(units, kMergeWarps * per_warp)),
                     dim3(kMergeWarps * 32), 0, s, a);
 }
 template <typename T, int D>

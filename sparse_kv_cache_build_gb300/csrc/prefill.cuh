@@ -360,6 +360,7 @@ using MmaShape = TileShape<256, 128, 128>;       // bf16, tensor cores
 using FewShape = TileShape<128, 128, 128>;       // the same for batches of few rows
 using SwapShape = TileShape<32, 128, 32, Mask::kCausal, 3>;        // and where keys take the rows' place
 using SimtShape = TileShape<128, 64, 0>;         // fp32, CUDA cores
+using SimtFewShape = TileShape<32, 64, 32>;      // the same for batches of few rows
 int prefill_tile_rows(int dtype);
 cudaError_t launch_prefill(const kv_cache_desc& d, const int32_t* cu, int total,
                            const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
@@ -369,6 +370,9 @@ cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
 template <Mask M>       // batches of few rows, with another mask than the causal one
 cudaError_t launch_prefill_few(const kv_cache_desc& d, const PackedRows& pr,
                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
+template <Mask M>
+cudaError_t launch_prefill_simt_few(const kv_cache_desc& d, const PackedRows& pr,
+                                    const PrefillArgs& a, DevCtx ctx, cudaStream_t s);
 template <Mask M>
 cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s);

@@ -35,6 +35,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int R = SimtShape::rows, KT = SimtShape::keys;
 constexpr int RPT = R / 16, KPT = KT / 16;           // rows and keys of a thread
+constexpr int kSimtFewRows = 64;     // mean rows per sequence up to which items have 32 rows
 
 template <int D> struct SimtCfg {
   static constexpr int LD = D + 4;                   // padded row, floats
@@ -195,6 +196,10 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
           }
         }
       }
+      // with another mask: whether some row does not see some key of the tile that is before it
+      const bool border = M == Mask::kTree
+          ? u0 + KT > past
+          : it.pos0 + it.n_tok - 1 - u0 >= a.window && u0 + KT > a.sinks;
       if (D == 128) __syncthreads();         // the key tile's buffer takes the probabilities
 #pragma unroll
       for (int i = 0; i < RPT; ++i) {
@@ -204,7 +209,8 @@ prefill_simt_kernel(const __grid_constant__ kv_cache_desc d, const __grid_consta
 #pragma unroll
         for (int j = 0; j < KPT; ++j) {
           s[j] = (s2[i][j].x + s2[i][j].y) * a.scale_log2;
-          if (tx + 16 * j > last - u0 || (row < rows && hidden(u0 + tx + 16 * j, last, row)))
+          if (tx + 16 * j > last - u0 ||
+              (M != Mask::kCausal && border && row < rows && hidden(u0 + tx + 16 * j, last, row)))
             s[j] = -INFINITY;
           top = fmaxf(top, s[j]);
         }
@@ -306,6 +312,11 @@ cudaError_t launch_t(const kv_cache_desc& d, const PackedRows& pr, const Prefill
 template <Mask M>
 cudaError_t launch_prefill_simt(const kv_cache_desc& d, const PackedRows& pr,
                                 const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
+  // one share promises a row the same bits whatever the batch, so the batch chooses nothing there
+  if constexpr (M != Mask::kCausal) {
+    if (a.NC > 1 && (int64_t)pr.total * a.G <= (int64_t)kSimtFewRows * d.batch)
+      return launch_prefill_simt_few<M>(d, pr, a, ctx, s);
+  }
   return d.head_dim == 128 ? launch_t<128, M>(d, pr, a, ctx, s) : launch_t<64, M>(d, pr, a, ctx, s);
 }
 

@@ -136,6 +136,9 @@ FEW = [
 ]
 
 
+FEW += [(new, past, "fp32", D, G, PS, shares) for new, past, _, D, G, PS, shares in FEW]
+
+
 @pytest.mark.parametrize("new,past,dtype,D,G,PS,shares", FEW)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (100, 4), (1000, 300), (10 ** 6, 0)])
 def test_window_of_few_rows(new, past, dtype, D, G, PS, shares, window, sinks):
@@ -149,9 +152,9 @@ def test_tree_of_few_rows(new, past, dtype, D, G, PS, shares):
 
 def test_few_rows_whose_maximum_keeps_growing():
     """Keys that grow along the sequence: the reference moves, and what was summed is rescaled."""
-    for D, G in ((128, 4), (64, 8)):
+    for D, G, dtype in ((128, 4, "bf16"), (64, 8, "bf16"), (128, 2, "fp32")):
         for kind in ("window", "tree"):
-            c = Masked((1, 4), (1500, 2000), "bf16", D, G, window=1200 if kind == "window" else None,
+            c = Masked((1, 4), (1500, 2000), dtype, D, G, window=1200 if kind == "window" else None,
                        sinks=3, parents=[[-1], bush(4, 2)] if kind == "tree" else None)
             grow = torch.linspace(0.1, 6.0, c.PS, device="cuda")
             for b, n in enumerate(c.lens):
