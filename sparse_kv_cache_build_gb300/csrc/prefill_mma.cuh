@@ -993,12 +993,17 @@ cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
                                const PrefillArgs& a, DevCtx ctx, cudaStream_t s) {
   // one share promises a row the same bits whatever the batch, so the batch chooses nothing there
   const bool few = a.NC > 1 && (int64_t)pr.total * a.G <= (int64_t)kFewRows * d.batch;
+  // Up to 16 rows to a sequence at D = 128, 8 at D = 64, another mask's keys take the rows' place.
+  // Measured against the instance of few rows, 32 sequences of 32/8 heads of 128 in a window of
+  // 1000: 4, 8, 16 and 32 rows 34, 35, 37 and 41 us (41 to 42); 16 heads of 64: 45, 46, 55 and 73
+  // (58, 60, 60 and 61), trees over 6000 tokens 101, 105, 127 and 167 (104, 106, 111 and 114).
   if constexpr (M != Mask::kCausal) {
-    if (few) return launch_prefill_few<M>(d, pr, a, ctx, s);
-  } else if (few) {
+    if (few && (int64_t)pr.total * a.G * 8 <= (int64_t)d.head_dim * d.batch)
+      return launch_prefill_few<M>(d, pr, a, ctx, s);
+  }
+  if (few)
     return d.head_dim == 128 ? launch_t<128, true, M>(d, pr, a, ctx, s)
                              : launch_t<64, true, M>(d, pr, a, ctx, s);
-  }
   return d.head_dim == 128 ? launch_t<128, false, M>(d, pr, a, ctx, s)
                            : launch_t<64, false, M>(d, pr, a, ctx, s);
 }
