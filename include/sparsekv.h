@@ -331,6 +331,7 @@ kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stri
  * are. new_lens: device int32[batch], becomes
  * s_b + keep_cnt[b]; it is not seq_lens, which the call leaves as it is (the caches of all layers
  * take the same lists), and which the caller replaces when all are done.
+ * FP8 statistics are not kept: kv_build_page_stats_fp8 makes them anew.
  * Pages from s_b on must not be shared with another sequence. Indices that do not rise or are
  * outside the candidates are flagged (KV_DEVERR_BAD_SEL) and not moved; the sequence's tokens from
  * there on are unspecified. A count that does not fit is flagged and the sequence left as it is,
@@ -380,7 +381,9 @@ kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_
  * row) are flagged (KV_DEVERR_BAD_LEN) and the row keeps its old row's tokens; a parent that is no
  * old row is flagged (KV_DEVERR_BAD_SEL) and taken as -1; an entry that is neither -1 nor a page is
  * flagged (KV_DEVERR_BAD_PAGE) and taken as -1. KV_ERR_UNSUPPORTED for more than KV_PAGES_MAX_ROWS
- * rows, old or new, and for page-table rows of 2^31 - 256 tokens or more. seq_lens is not written: the caller makes new_lens the lengths when the step's
+ * rows, old or new, and for page-table rows of 2^31 - 256 tokens or more. After pages went out of a
+ * window only kv_window_attn reads such a sequence: calls that read every page flag the entries of
+ * -1. seq_lens is not written: the caller makes new_lens the lengths when the step's
  * tokens are appended.
  */
 #define KV_PAGES_MAX_ROWS 16384
