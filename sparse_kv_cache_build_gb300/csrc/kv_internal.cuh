@@ -296,7 +296,7 @@ cudaError_t launch_compact(const kv_cache_desc& d, const int32_t* cu, const int3
 long copy_pages_blocks(const kv_cache_desc& d, long n);       // blocks of a copy of n pages
 cudaError_t launch_copy_pages(const kv_cache_desc& d, const int32_t* pairs, int n, void* stats,
                               DevCtx ctx, cudaStream_t s);
-constexpr int kMaxPageRows = KV_PAGES_MAX_ROWS;    // two numbers per row in the allocating block's memory
+constexpr int kMaxPageRows = KV_PAGES_MAX_ROWS;    // three numbers per row in the allocating block's memory
 cudaError_t launch_update_pages(const kv_cache_desc& d, int32_t* refs, const int32_t* parents,
                                 int rows, const int32_t* keep_lens, const int32_t* new_lens,
                                 int window, int sinks, int32_t* table, int32_t* copies,

@@ -8,17 +8,18 @@
 // the old one; the page's reference count changes by the rows that kept the entry less one, so
 // a row that one row continues costs no atomic. (Counts are sums of whole numbers: the order of
 // the atomics does not show.) The second is one cluster of eight blocks. It
-//   1. finds the partial pages that rows are about to write to and that others hold too: every such
-//      row takes itself off the page's count; where none is left, the last row of the batch (an
-//      atomic minimum over the count, below zero meanwhile) keeps the page, the others get a fresh
-//      one. No order of the atomics changes which;
-//   2. adds up the rows' needs, and counts the free pages (count zero), each warp its own stretch;
-//   3. hands the lowest free pages out in the order of the rows: a free page's rank among the free
-//      ones says which row and entry it is for.
-// The pool's state is the counts alone, so the pages handed out depend on nothing else.
+//   1. counts the free pages (count zero), each warp its own stretch;
+//   2. finds, in every block for itself, the partial pages that rows are about to write to and that
+//      others hold too, and adds up the rows' needs;
+//   3. tells the blocks each other's free pages, and hands the lowest ones out in the order of the
+//      rows: a free page's rank among the free ones says which row and entry it is for.
+// A shared page's count never passes zero on the way, so counting and reading it need no order but
+// the one barrier. The pool's state is the counts alone: the pages handed out depend on nothing else.
 //
 // Bound: latency. The table is read and written once and the counts once or twice, all of it in L2;
-// what shows is the two launches and the second one's chain of cluster barriers.
+// what shows is the two launches and the second one's chain of dependent reads (parent, length,
+// entry, count). Rows that share a page look for each other among all rows, which for thousands of
+// them is the longest part.
 #include <cooperative_groups.h>
 
 #include "packed_rows.cuh"
@@ -184,16 +185,14 @@ fork_rows_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant_
     if (e[i] >= 0 && kept[i] != 1) atomicAdd(a.refs + e[i], kept[i] - 1);
 }
 
-// The needs of the rows as a running sum in shared memory: row b's pages have the ranks
-// sums[b] .. sums[b + 1] - 1. Called by a whole block; returns the total.
-__device__ __forceinline__ int64_t running_sum(const int32_t* copies, int rows, int64_t* scratch,
-                                               int32_t* sums) {
+// Exclusive running sum of `need` over the rows, in place, and their total; by a whole block.
+// Sums beyond 32 bits are more than any pool has, and then nothing is handed out.
+__device__ __forceinline__ int64_t running_sum(int32_t* need, int rows, int64_t* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t before = 0;
   for (int b0 = 0; b0 < rows; b0 += kAllocThreads) {
-    const int b = b0 + tid;
-    const int need = b < rows ? __ldcg(copies + 2 * b + 1) : 0;
-    int64_t upto = need;
+    const int b = b0 + tid, mine = b < rows ? need[b] : 0;
+    int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -201,13 +200,12 @@ __device__ __forceinline__ int64_t running_sum(const int32_t* copies, int rows, 
     }
     if (lane == 31) scratch[warp] = upto;
     __syncthreads();
-    int64_t mine = before;
+    int64_t start = before;
     for (int w = 0; w < kAllocWarps; ++w) {
-      if (w < warp) mine += scratch[w];
+      if (w < warp) start += scratch[w];
       before += scratch[w];
     }
-    // sums beyond 32 bits are more than any pool has, and then nothing is handed out
-    if (b < rows) sums[b] = (int32_t)(mine + upto - need);
+    if (b < rows) need[b] = (int32_t)(start + upto - mine);
     __syncthreads();
   }
   return before;
@@ -220,54 +218,18 @@ alloc_pages_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constan
   __shared__ int64_t scratch[kAllocWarps];
   __shared__ int warp_free[kAllocWarps], block_free[kAllocBlocks];
   cg::cluster_group cluster = cg::this_cluster();
+  // every block must have started before its shared memory is written: half a barrier here, the
+  // other half before the first write
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_trigger();
   pdl_wait();
-  int32_t* sums = sm;                                // [rows] rank of a row's first page
-  int32_t* places = sm + a.rows;                     // [rows] its entry, twice, plus 1 for a copy
+  int32_t* sums = sm;                                // [rows] needs, then a row's first rank
+  int32_t* places = sums + a.rows;                   // [rows] its entry, twice, plus 1 for a copy
+  int32_t* parts = places + a.rows;                  // [rows] the partial page it writes to, or -1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster.block_rank(), PS = d.page_size, NP = d.num_phys_pages;
   const int stride = d.page_table_stride;
-  const int me = rank * kAllocThreads + tid, step = kAllocBlocks * kAllocThreads;
 
-  // The partial page that row b is about to write to, or -1, and the entries it adds.
-  auto partial = [&](int b, int* first, int* last) {
-    const RowPlan r = row_plan(ctx, d, a, b);
-    *first = pages_of(r.keep, PS);
-    *last = pages_of(r.want, PS);
-    if (r.want <= r.keep || r.keep % PS == 0) return -1;
-    return a.table[(int64_t)b * stride + *first - 1];
-  };
-  int first, last;
-  for (int b = me; b < a.rows; b += step) {
-    const int part = partial(b, &first, &last);
-    if (part >= 0) atomicSub(a.refs + part, 1);
-  }
-  __threadfence();
-  cluster.sync();
-  for (int b = me; b < a.rows; b += step) {
-    const int part = partial(b, &first, &last);
-    if (part >= 0 && __ldcg(a.refs + part) <= 0) atomicMin(a.refs + part, -(b + 1));
-  }
-  __threadfence();
-  cluster.sync();
-  // copies[b] = {the page to copy or -1, pages needed} until every block has read it
-  for (int b = me; b < a.rows; b += step) {
-    const int part = partial(b, &first, &last);
-    const bool fork = part >= 0 && __ldcg(a.refs + part) != -(b + 1);
-    a.copies[2 * b] = fork ? part : -1;
-    a.copies[2 * b + 1] = last - first + fork;
-  }
-  __threadfence();
-  cluster.sync();
-  for (int b = me; b < a.rows; b += step) {          // its only holder keeps it
-    const int part = partial(b, &first, &last);
-    if (part >= 0 && __ldcg(a.copies + 2 * b) < 0) a.refs[part] = 1;
-  }
-  const int64_t total = running_sum(a.copies, a.rows, scratch, sums);
-  for (int b = tid; b < a.rows; b += kAllocThreads) {
-    const int fork = __ldcg(a.copies + 2 * b) >= 0;
-    places[b] = 2 * (pages_of(row_plan(ctx, d, a, b).keep, PS) - fork) + fork;
-  }
   // free pages, each warp its own stretch of the counts
   const int warps = kAllocBlocks * kAllocWarps;
   const int64_t each = ((int64_t)NP + warps * 128 - 1) / (warps * 128) * 128;
@@ -290,13 +252,44 @@ alloc_pages_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constan
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) warp_free[warp] = mine;
+
+  // Every block works out all rows' needs, so that none has to wait for another's. A row that
+  // grows out of a partial page that others hold too gets a fresh one, unless it is the last row
+  // of those that alone hold the page.
+  for (int b = tid; b < a.rows; b += kAllocThreads) {
+    const RowPlan r = row_plan(ctx, d, a, b);
+    const int first = pages_of(r.keep, PS);
+    const bool writes = r.want > r.keep && r.keep % PS != 0;
+    parts[b] = writes ? a.table[(int64_t)b * stride + first - 1] : -1;
+    sums[b] = pages_of(r.want, PS) - first;
+    places[b] = 2 * first;
+  }
   __syncthreads();
+  for (int b = tid; b < a.rows; b += kAllocThreads) {
+    const int part = parts[b];
+    if (part < 0) continue;
+    const int holders = __ldcg(a.refs + part);
+    if (holders <= 1) continue;
+    int writers = 0, last = b;
+    for (int k = 0; k < a.rows; ++k)
+      if (parts[k] == part) {
+        ++writers;
+        last = k;
+      }
+    if (holders > writers || last != b) {
+      ++sums[b];
+      places[b] -= 1;                                // 2 (first - 1) + 1
+    }
+  }
+  __syncthreads();
+  const int64_t total = running_sum(sums, a.rows, scratch);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (tid < kAllocBlocks) {
     int sum = 0;
     for (int w = 0; w < kAllocWarps; ++w) sum += warp_free[w];
     cluster.map_shared_rank(block_free, tid)[rank] = sum;
   }
-  cluster.sync();
+  cluster.sync();                                    // counts are known, and have been read
   int64_t at = 0, have = 0;                          // free pages before the warp's, and in all
   for (int r = 0; r < kAllocBlocks; ++r) {
     if (r < rank) at += block_free[r];
@@ -304,17 +297,15 @@ alloc_pages_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constan
   }
   for (int w = 0; w < warp; ++w) at += warp_free[w];
   const bool enough = total <= have;
-  if (me == 0) {
+  if (rank == 0 && tid == 0) {
     a.free_left[0] = (int32_t)max((int64_t)INT32_MIN, have - total);
     if (!enough) flag(ctx, KV_DEVERR_NO_PAGES);
   }
-  for (int b = me; b < a.rows; b += step) {
-    const int src = __ldcg(a.copies + 2 * b);
-    if (src >= 0 && !enough) {                       // the row keeps what it holds
-      atomicAdd(a.refs + src, 1);
-      a.copies[2 * b] = -1;
-    }
-    if (src < 0 || !enough) a.copies[2 * b + 1] = -1;
+  for (int b = rank * kAllocThreads + tid; b < a.rows; b += kAllocBlocks * kAllocThreads) {
+    const bool fork = enough && (places[b] & 1);
+    a.copies[2 * b] = fork ? parts[b] : -1;
+    if (!fork) a.copies[2 * b + 1] = -1;             // else by who hands the page out
+    else atomicSub(a.refs + parts[b], 1);
   }
   if (!enough) return;
   for (int64_t p0 = from; p0 < to && at < total; p0 += 128) {
@@ -380,10 +371,10 @@ cudaError_t launch_update_pages(const kv_cache_desc& d, int32_t* refs, const int
   const dim3 grid(ceil_div(d.page_table_stride, kRowEntries), d.batch + (parents != nullptr));
   cudaError_t e = launch_pdl(fork_rows_kernel, grid, dim3(kRowThreads), 0, s, d, a, ctx);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)rows * 2 * sizeof(int32_t);
+  const size_t smem = (size_t)rows * 3 * sizeof(int32_t);
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(alloc_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kMaxPageRows * 2 * sizeof(int32_t)));
+                             (int)(kMaxPageRows * 3 * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(alloc_pages_kernel, dim3(kAllocBlocks), dim3(kAllocThreads), smem, s, d, a,
