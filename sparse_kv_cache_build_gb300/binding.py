@@ -234,7 +234,7 @@ class PagedKV:
         # what the packed calls check on every step, as plain values
         self.index, self.elem = self.k_pool.get_device(), self.k_pool.dtype
         self.pages, self.groups, self.cols = NP, Hkv, D
-        self.sequences = self.page_table.shape[0]
+        self.sequences, self.entries = self.page_table.shape
         self._ref = ctypes.byref(self.desc)
 
     @classmethod
@@ -556,23 +556,28 @@ def kv_update_pages(kv: PagedKV, refs, new_lens, keep_lens=None, parents=None, w
     rows = new_lens.shape[0] if new_lens.dim() == 1 else 0
     _on_device(kv, new_lens, "new_lens", torch.int32, (rows,))
     _on_device(kv, refs, "refs", torch.int32, (kv.pages,))
-    for t, name in ((keep_lens, "keep_lens"), (parents, "parents")):
-        if t is not None:
-            _on_device(kv, t, name, torch.int32, (rows,))
-    dev = kv.k_pool.device
+    keep = parent = None
+    if keep_lens is not None:
+        _on_device(kv, keep_lens, "keep_lens", torch.int32, (rows,))
+        keep = keep_lens.data_ptr()
+    if parents is not None:
+        _on_device(kv, parents, "parents", torch.int32, (rows,))
+        parent = parents.data_ptr()
+    dev = refs.device
     if table is None:
-        table = kv.page_table if parents is None else _new((rows, kv.stride), torch.int32, dev,
+        table = kv.page_table if parents is None else _new((rows, kv.entries), torch.int32, dev,
                                                            stream)
+    _on_device(kv, table, "table", torch.int32, (rows, kv.entries))
     if copies is None:
         copies = _new((rows, 2), torch.int32, dev, stream)
+    else:
+        _on_device(kv, copies, "copies", torch.int32, (rows, 2))
     if free_left is None:
         free_left = _new((1,), torch.int32, dev, stream)
-    for t, name, shape in ((table, "table", (rows, kv.stride)), (copies, "copies", (rows, 2)),
-                           (free_left, "free_left", (1,))):
-        _on_device(kv, t, name, torch.int32, shape)
+    else:
+        _on_device(kv, free_left, "free_left", torch.int32, (1,))
     status = lib().kv_update_pages(
-        kv.ref(), refs.data_ptr(), None if parents is None else parents.data_ptr(), rows,
-        None if keep_lens is None else keep_lens.data_ptr(), new_lens.data_ptr(), int(window),
+        kv.ref(), refs.data_ptr(), parent, rows, keep, new_lens.data_ptr(), int(window),
         int(sinks), table.data_ptr(), copies.data_ptr(), free_left.data_ptr(),
         _raw_stream(kv, stream))
     if status != KV_OK:
