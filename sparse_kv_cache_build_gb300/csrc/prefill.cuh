@@ -58,11 +58,15 @@ struct PrefillArgs {
 };
 
 // Tile sizes of a kernel: R rows by KT keys, and what an item costs: two units per key tile, one
-// where the item has at most WIDE rows, and a fixed part of item_cost units (bf16: an item's start
+// where the item has at most WIDE rows, and a fixed part of COST units (bf16: an item's start
 // and end are 5000 to 9000 cycles, a unit 1300; 3, 4, 5 and 8 give 240, 242, 247 and 257 us for
-// sixteen ragged prompts, and 351, 345, 345 and 350 for one of 8192 tokens in pages of 64).
+// sixteen ragged prompts, and 351, 345, 345 and 350 for one of 8192 tokens in pages of 64). In a
+// window the items' tiles are fewer and their border masks more: 4, 6, 8 and 12 give 127, 121, 119
+// and 117 us for sixteen ragged prompts of 16 heads of 64 in a window of 512, and 327, 328, 330
+// and 335 for one prompt of 8192 tokens in a window of 4096.
 template <int R, int KT, int WIDE, Mask M = Mask::kCausal, int COST = 4> struct TileShape {
-  static constexpr int rows = R, keys = KT, narrow = WIDE, item_cost = COST;
+  static constexpr int rows = R, keys = KT, narrow = WIDE;
+  static constexpr int item_cost = M == Mask::kWindow && R == 256 ? 8 : COST;
   static constexpr Mask mask = M;
   static constexpr bool called = R == 32;
   template <Mask N> using With = TileShape<R, KT, WIDE, N, COST>;
