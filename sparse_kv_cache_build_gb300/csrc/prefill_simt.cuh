@@ -35,7 +35,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int R = SimtShape::rows, KT = SimtShape::keys;
 constexpr int RPT = R / 16, KPT = KT / 16;           // rows and keys of a thread
-constexpr int kSimtFewRows = 64;     // mean rows per sequence up to which items have 32 rows
+// Mean rows per sequence up to which another mask's items have 32 rows: at 64 rows they take two
+// thirds of the time of items of 128, at 124 from half of it (short windows, one sequence) to 1.3
+// times it (prefill_simt_few.cuh).
+constexpr int kSimtFewRows = 64;
 
 template <int D> struct SimtCfg {
   static constexpr int LD = D + 4;                   // padded row, floats
