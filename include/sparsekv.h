@@ -328,9 +328,9 @@ kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stri
  * hold candidates or what is kept, s_b / page_size up to the last kept token's, become those of
  * kv_build_page_stats at the new length (stats may be NULL: they are left alone; so are those of a
  * sequence without candidates). Tokens before s_b and slots behind the last kept token stay as they
- * are. new_lens: device int32[batch], becomes
- * s_b + keep_cnt[b]; it is not seq_lens, which the call leaves as it is (the caches of all layers
- * take the same lists), and which the caller replaces when all are done.
+ * are. new_lens: device int32[batch], becomes s_b + keep_cnt[b]; it overlaps no input and is not
+ * seq_lens, which the call leaves as it is (the caches of all layers take the same lists), and which
+ * the caller replaces when all are done.
  * FP8 statistics are not kept: kv_build_page_stats_fp8 makes them anew.
  * Pages from s_b on must not be shared with another sequence. Indices that do not rise or are
  * outside the candidates are flagged (KV_DEVERR_BAD_SEL) and not moved; the sequence's tokens from
@@ -377,6 +377,9 @@ kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_
  * Where the free pages do not suffice for all rows, none is handed out: rows keep what they hold,
  * copies are (-1, -1), and KV_DEVERR_NO_PAGES is flagged. free_left: device int32[1], the free
  * pages after the call, or minus those that were missing.
+ * Statistics are not touched: where keep_lens drops tokens of a page that stays, kv_compact
+ * with the dropped tokens as candidates and none kept, or kv_build_page_stats, makes that page's
+ * anew before the next append.
  * Lengths that do not fit (keep outside the old row's tokens, new below keep or above the table
  * row) are flagged (KV_DEVERR_BAD_LEN) and the row keeps its old row's tokens; a parent that is no
  * old row is flagged (KV_DEVERR_BAD_SEL) and taken as -1; an entry that is neither -1 nor a page is

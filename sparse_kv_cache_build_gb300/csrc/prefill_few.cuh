@@ -227,7 +227,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
       for (int i = 0; i < n; ++i, ++c) {
         const int u0 = (it.kt0 + i) * kFewKeys, key = u0 + tid;
         ok = ok && wait_bounded(s_full + (c & 1), (c >> 1) & 1, ctx.wait_ns);
-        float x[kFewTileRows];
+        float x[kFewTileRows];                       // q . k, or -inf where the row does not see it
         bool grow = false;
         if (ok) {
           tc::fence_after();
@@ -249,7 +249,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
             }
 #pragma unroll
             for (int e = 8 * q; e < 8 * q + 8; ++e) {
-              x[e] = __uint_as_float(s[e]) * a.scale_log2;
+              x[e] = __uint_as_float(s[e]);
               if (!all) {
                 const int pos = it.pos0 + (e >> log_g);
                 bool sees = key <= pos;
@@ -263,7 +263,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
                 if (!sees) x[e] = -INFINITY;
               }
               if (e >= rows) x[e] = -INFINITY;               // nobody's row
-              grow |= x[e] > ref[e] + kFewLazy;
+              grow |= fmaf(x[e], a.scale_log2, -ref[e]) > kFewLazy;   // NaN for no key so far
             }
           }
         }
@@ -278,8 +278,8 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
           red[warp * 32 + lane] = join_lanes(v, [](float p, float q) { return fmaxf(p, q); });
           group_sync();
           if (warp == 0) {
-            const float top = fmaxf(fmaxf(red[lane], red[32 + lane]),
-                                    fmaxf(red[64 + lane], red[96 + lane]));
+            const float top = a.scale_log2 * fmaxf(fmaxf(red[lane], red[32 + lane]),
+                                                   fmaxf(red[64 + lane], red[96 + lane]));
             const float old = ref_sh[lane], now = top > old + kFewLazy ? top : old;
             ref_sh[lane] = now;
             factor_sh[lane] = now == -INFINITY ? 1.f : exp2f(old - now);
@@ -322,9 +322,10 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int r = 8 * q + 2 * e;
-            const float p0 = tc::exp2_approx(x[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
-            const float p1 =
-                tc::exp2_approx(x[r + 1] - (ref[r + 1] == -INFINITY ? 0.f : ref[r + 1]));
+            const float m0 = ref[r] == -INFINITY ? 0.f : ref[r];
+            const float m1 = ref[r + 1] == -INFINITY ? 0.f : ref[r + 1];
+            const float p0 = tc::exp2_approx(fmaf(x[r], a.scale_log2, -m0));
+            const float p1 = tc::exp2_approx(fmaf(x[r + 1], a.scale_log2, -m1));
             sum[r] += p0;
             sum[r + 1] += p1;
             high[e] = tc::pack_bf16(p0, p1);

@@ -210,3 +210,22 @@ def test_drafts_forks_and_windows(seed):
     s.update([0], [0], parents=[-1])
     assert int(s.refs.sum()) == 0
     assert_no_device_error()
+
+
+def test_dropped_tokens_leave_the_statistics():
+    """A page whose last tokens are dropped: its statistics follow by a compaction that keeps none
+    of them, and the next append builds on them."""
+    s = Server(5)
+    assert s.update([45, 30], [0, 0], parents=[-1, -1]) > 0
+    s.append([45, 30], list(range(45)) + list(range(30)))
+    drop = ints([0, 9, 9 + 14])
+    for kv, stats in zip(s.caches(), s.stats):
+        lens = skv.kv_compact(kv, ints([[0], [0]]), ints([0, 0]), stats, cu_tokens=drop)
+    assert lens.tolist() == [36, 16]
+    s.held, s.lens = [h[:n] for h, n in zip(s.held, (36, 16))], [36, 16]
+    s.check_stats()
+    assert s.update([40, 17], [36, 16]) > 0
+    s.append([4, 1], [36, 37, 38, 39, 16])
+    s.check()
+    s.check_stats()
+    assert_no_device_error()
