@@ -359,6 +359,47 @@ __device__ __forceinline__ LinePlace find_place(const DevCtx& ctx, const kv_cach
   return LinePlace{total, sh->before, sh->b, lo, hi};
 }
 
+// The same by one warp, for batches of which a lane takes a few sequences. (b, before) are not
+// meant where the line is empty.
+template <typename S>
+__device__ __forceinline__ LinePlace find_place_warp(const DevCtx& ctx, const kv_cache_desc& d,
+                                                     const PackedRows& pr, const PrefillArgs& a,
+                                                     int i) {
+  const int lane = threadIdx.x & 31, per = (d.batch + 31) / 32;
+  const int b0 = lane * per, b1 = min(d.batch, b0 + per);
+  auto cost_of = [&](int b) -> int64_t {
+    const SeqItems<S> s = seq_items<S>(ctx, d, pr, a, b);
+    return s.cost(s.tiles(), a) * d.num_kv_heads;
+  };
+  int64_t mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += cost_of(b);
+  int64_t before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  const int64_t total = __shfl_sync(0xffffffffu, before, 31);
+  before -= mine;
+  const int64_t each = divide(total, a.NC);
+  const int rest = (int)(total - each * a.NC);
+  const int64_t lo = each * i + rest * i / a.NC;       // rest * i < 2^20
+  const int64_t hi = each * (i + 1) + rest * (i + 1) / a.NC;
+  const bool here = mine > 0 && lo >= before && lo < before + mine;
+  int b = b0;
+  if (here && per > 1)
+#pragma unroll 1
+    for (; b < b1 - 1; ++b) {
+      const int64_t c = cost_of(b);
+      if (lo < before + c) break;
+      before += c;
+    }
+  const int from = max(0, __ffs(__ballot_sync(0xffffffffu, here)) - 1);
+  return LinePlace{total, __shfl_sync(0xffffffffu, before, from),
+                   __shfl_sync(0xffffffffu, b, from), lo, hi};
+}
+
 // Launchers.
 using MmaShape = TileShape<256, 128, 128>;       // bf16, tensor cores
 using FewShape = TileShape<128, 128, 128>;       // the same for batches of few rows

@@ -41,6 +41,10 @@ constexpr int kFewThreads = 224;       // softmax warpgroup, products, loads, it
 constexpr int kFewMma = 4, kFewLoad = 5, kFewItem = 6;
 constexpr int kFewItems = 4;           // items known ahead
 constexpr int kFewKeys = SwapShape::keys, kFewTileRows = SwapShape::rows;
+// Sequences up to which one warp finds the block's place: against the whole block's search, which
+// has the others fetch its code and wait at its barriers, 12.5 -> 12.2 us for one sequence and 34.3
+// -> 33.9 for 32 (32/8 heads, a window of 1000).
+constexpr int kFewAlone = 256;
 constexpr float kFewLazy = 8.f;        // log2 of the growth that forces a rescale
 
 template <int D> struct FewCfg {
@@ -151,18 +155,13 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
   pdl_trigger();
   pdl_wait();
   finish_empty<bf16_t, D>(ctx, d, pr, a);
-  const LinePlace at = find_place<Shape>(ctx, d, pr, a, blockIdx.x, &scratch);
-  const int64_t lo = at.lo, hi = at.hi;
-  if (at.total == 0 || lo >= hi) {               // nothing, or less than a unit of the line
-    if (tid == 0 && a.notes != nullptr)
-      a.notes[blockIdx.x] =
-          at.total == 0 ? BorderNote{0, 0, 0, 0, 0, 0}
-                        : ItemWalk<Shape>(d, pr, a, ctx, lo, hi, at.b, at.before, 0).border();
-    __syncwarp();
-    if (warp == kFewMma) tc::dealloc(*tmem_slot, C::TMEM_COLS);
-    return;
-  }
-  tc::fence_after();                             // the search's barriers order what is above
+  // Only the warp that walks the items needs the block's place in the line; it looks for it alone
+  // where the batch is small, while the others wait for the first item.
+  const bool alone = d.batch <= kFewAlone;
+  LinePlace at{0, 0, 0, 0, 0};
+  if (!alone) at = find_place<Shape>(ctx, d, pr, a, blockIdx.x, &scratch);
+  __syncthreads();
+  tc::fence_after();
   const uint32_t tmem = uniform(*tmem_slot);
   auto item_ready = [&](int j) {
     return wait_bounded(item_full + j % kFewItems, (j / kFewItems) & 1, ctx.wait_ns);
@@ -577,7 +576,10 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
   } else {
     // ---- the block's items, one ahead of their rows, and after the last an item without key
     // tiles. Waits for an item's end are for work and count the limit once per key tile.
-    ItemWalk<Shape> walk(d, pr, a, ctx, lo, hi, at.b, at.before, blockIdx.x);
+    if (alone) at = find_place_warp<Shape>(ctx, d, pr, a, blockIdx.x);
+    const bool none = at.total == 0;                 // less than a unit of the line: no item either
+    ItemWalk<Shape> walk(d, pr, a, ctx, at.lo, none ? at.lo : at.hi, none ? 0 : at.b,
+                         none ? 0 : at.before, blockIdx.x);
     ItemWalk<Shape> start = walk;                    // for the note that a merge reads
     bool ok = true;
     int loaded = 0;
@@ -606,7 +608,7 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
         __syncwarp();
         ++loaded;
       }
-      if (!walk.next(&next)) next.kt0 = next.kt1 = 0;
+      if (none || !walk.next(&next)) next.kt0 = next.kt1 = 0;
       if (j + 1 >= kFewItems)
         ok = wait_bounded(item_free + (j + 1) % kFewItems, ((j + 1) / kFewItems - 1) & 1,
                           patience());
@@ -621,7 +623,8 @@ prefill_few_kernel(const __grid_constant__ CUtensorMap map_k,
       __syncwarp();
       if (next.kt0 >= next.kt1) break;
     }
-    if (lane == 0 && a.notes != nullptr) a.notes[blockIdx.x] = start.border();
+    if (lane == 0 && a.notes != nullptr)
+      a.notes[blockIdx.x] = none ? BorderNote{0, 0, 0, 0, 0, 0} : start.border();
     if (!ok && lane == 0) flag(ctx, KV_DEVERR_TIMEOUT);
     for (int j = max(0, loaded - 2); j < loaded; ++j)
       (void)wait_bounded(q_full + (j & 1), (j >> 1) & 1, kDrainNs);

@@ -136,6 +136,13 @@ FEW = [
 ]
 
 
+FEW += [
+    # more sequences than one warp looks through for a block's place, most without rows
+    (tuple(int(i % 7 == 3) for i in range(300)), tuple((37 * i) % 200 for i in range(300)), "bf16",
+     128, 4, 16, 0),
+    (tuple(int(i % 5 == 1) for i in range(1100)), tuple((11 * i) % 90 for i in range(1100)), "bf16",
+     64, 2, 16, 0),
+]
 FEW += [(new, past, "fp32", D, G, PS, shares) for new, past, _, D, G, PS, shares in FEW]
 
 
