@@ -121,7 +121,8 @@ constexpr int kMergeFewRows = 64;
 
 template <typename T, int D, int V>
 cudaError_t merge_v(const PrefillArgs& a, cudaStream_t s) {
-  // few rows with many parts: a unit per warp, as one after the other they are the call's end
+  // Few rows with many parts: a unit per warp, as four one after the other are the call's end (eight
+  // drafts over 8192 tokens, 8/2 heads of 64: 29 -> 17 us).
   const int units = a.part_rows * (D / (32 * V)), per_warp = V == 1 ? 1 : kMergeUnits;
   return launch_pdl(prefill_merge_kernel<T, D, V>,
                     dim3(a.NC - 1, ceil_div(units, kMergeWarps * per_warp)),

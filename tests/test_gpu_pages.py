@@ -459,3 +459,34 @@ def test_captured_update_follows_its_inputs():
     assert_no_device_error()
     assert np.array_equal(table.cpu().numpy(), ref[0]) and p.refs.tolist() == ref[1]
     assert np.array_equal(copies.cpu().numpy(), ref[2]) and left.tolist() == [ref[3]]
+
+
+def test_calls_on_a_stream_given_by_argument():
+    """A call's own buffers are the stream's: not ones that the current stream still writes to."""
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        p = Pool(300, 20)
+        p.step([50, 70], parents=[-1, -1], keep=[0, 0])
+        want, keep, parents = ints([51, 75]), ints([50, 50]), ints([0, 0])
+        ref = oracle.update_pages(p.table, p.lens, p.refs.tolist(), 2, [0, 0], [50, 50], [51, 75],
+                                  16)
+        c = Case((20, 30), (30, 7), G=1)
+        kept, k0 = [[1, 4], [0, 2, 29]], f32(c.k_pool)
+        lists_ = lists(kept)
+        old = [torch.empty(x, dtype=torch.int32, device="cuda")
+               for x in ((2, 20), (2, 2), (1,), (2,))]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(10_000_000)
+        for x in old:                          # freed with a write of this stream still to come
+            x.fill_(-9)
+        del old, x
+        table, copies, left = skv.kv_update_pages(p.kv, p.refs, want, keep_lens=keep,
+                                                  parents=parents, stream=s)
+        lens = skv.kv_compact(c.kv, *lists_, cu_tokens=c.cu, stream=s)
+        skv.kv_copy_pages(c.kv, ints([[-1, -1]]), stream=s)
+        torch.cuda.synchronize()
+        assert_no_device_error()
+        assert np.array_equal(table.cpu().numpy(), ref[0]) and p.refs.tolist() == ref[1]
+        assert np.array_equal(copies.cpu().numpy(), ref[2]) and left.tolist() == [ref[3]]
+        k, _, ref_lens, _ = oracle.compact(k0, k0, c.table.cpu().numpy(), c.lens, c.new, kept, 16)
+        assert np.array_equal(f32(c.k_pool), k) and lens.tolist() == ref_lens
