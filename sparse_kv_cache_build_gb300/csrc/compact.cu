@@ -11,13 +11,14 @@
 // keys or values, so blocks need nothing of each other; it walks the tokens in batches: where they
 // come from and go to, worked out once for all columns, then all loads, a barrier, all stores.
 //
-// Bound: every moved token is read and written once. A batch costs a block one round of reads (list,
-// table, token), of which the first two run beside the tokens of the batch before; so a long list is
-// the columns split further, down to 32 bytes a row (a sector), as long as the blocks find an SM
-// each; a short one, that is a batch at once, is a chain of dependent reads (offsets, list, table,
-// token, statistics). Measured: 32 sequences that keep up to 9 of 26 drafts, 32/8 heads: 8.7 us on the
-// device; one of 32768 tokens that keeps 4600 (39 MB): 18.4 us, where columns of 64 bytes take 4 us
-// more, and blocks of half the threads and batch, two to an SM, 2 more.
+// Bound: every moved token is read and written once. A batch costs a block one round of reads
+// (list, table, token), of which the first two run beside the tokens of the batch before; so a
+// long list is the columns split further, down to 32 bytes a row (a sector), as long as the
+// blocks find an SM each; a short one, that is a batch at once, is a chain of dependent reads
+// (offsets, list, table, token, statistics). Measured: 32 sequences that keep up to 9 of 26
+// drafts, 32/8 heads: 8.7 us on the device; one of 32768 tokens that keeps 4600 (39 MB): 18.4 us,
+// where columns of 64 bytes take 4 us more, and blocks of half the threads and batch, two to an
+// SM, 2 more.
 #include "packed_rows.cuh"
 
 namespace skv {

@@ -14,14 +14,15 @@
 //      others hold too, and adds up the rows' needs;
 //   3. tells the blocks each other's free pages, and hands the lowest ones out in the order of the
 //      rows: a free page's rank among the free ones says which row and entry it is for.
-// A shared page's count never passes zero on the way, so counting and reading it need no order but
-// the one barrier. The pool's state is the counts alone: the pages handed out depend on nothing else.
+// A shared page's count never passes zero on the way, so counting and reading it need no order
+// but the one barrier. The pool's state is the counts alone: the pages handed out depend on
+// nothing else.
 //
-// Bound: latency. The table is read and written once and the counts once or twice, all of it in L2;
-// what shows is the two launches and the second one's chain of dependent reads (parent, length,
-// entry, count): 64 rows of 4096 entries over a pool of 65536 10.3 us on the device (15.9 with the
-// rows dealt out to the blocks and four barriers among them). Rows that share a page look for each other among all rows, which for thousands of
-// them is the longest part.
+// Bound: latency. The table is read and written once and the counts once or twice, all of it in
+// L2; what shows is the two launches and the second one's chain of dependent reads (parent,
+// length, entry, count): 64 rows of 4096 entries over a pool of 65536 10.3 us on the device (15.9
+// with the rows dealt out to the blocks and four barriers among them). Rows that share a page
+// look for each other among all rows, which for thousands of them is the longest part.
 #include <cooperative_groups.h>
 
 #include "packed_rows.cuh"

@@ -1,7 +1,7 @@
 // Causal attention of packed query rows over the paged cache: what its kernels share.
 //
-// Row (t, h) of sequence b, at position pos = len_b - n_b + t, attends to tokens 0..pos, or to those
-// of them that its mask lets it see (Mask below):
+// Row (t, h) of sequence b, at position pos = len_b - n_b + t, attends to tokens 0..pos, or to
+// those of them that its mask lets it see (Mask below):
 //   x_u = sm_scale q . k_u,  lse = log sum_u exp(x_u),  out = sum_u exp(x_u - lse) v_u.
 // The group's G query heads read the same keys, so a tile's rows are (token, head) pairs of
 // one KV head, token-major: a tile of R rows is R / G consecutive tokens.

@@ -17,12 +17,12 @@
 // over the one in use, common to the four warps: one vote per tile says whether any score asks for
 // a new one. Sums are kept per thread (over its keys) and joined at an item's end.
 //
-// Measured: 32 single tokens of 32/8 heads in a window of 1024 (134 MB) 36 us, of which the keys and
-// values stream in 20 at the copy rate; 6 are a block's start (its place in the line, the first item,
-// the table's entries, the first pages: dependent reads, and code that runs once), the rest the
-// items' ends and the merge. In a window of 4096 102 us, 79 at the copy rate. A tile takes its
-// warpgroup 1700 cycles with 8 rows, 2200 with 32, against 2800 that its bytes take when all SMs
-// stream. The same by the kernel that holds rows as rows: 43 and 108 us.
+// Measured: 32 single tokens of 32/8 heads in a window of 1024 (134 MB) 36 us, of which the keys
+// and values stream in 20 at the copy rate; 6 are a block's start (its place in the line, the
+// first item, the table's entries, the first pages: dependent reads, and code that runs once),
+// the rest the items' ends and the merge. In a window of 4096 102 us, 79 at the copy rate. A tile
+// takes its warpgroup 1700 cycles with 8 rows, 2200 with 32, against 2800 that its bytes take
+// when all SMs stream. The same by the kernel that holds rows as rows: 43 and 108 us.
 //
 // One warp issues the products, a tile's scores before the product with the values of the tile
 // before; one feeds K and V tiles through a ring by TMA, in the order in which the products take

@@ -41,15 +41,16 @@
 // Other masks (M). A window's items count their keys without the skipped pages (prefill.cuh): the
 // pipeline is the causal one, the loading warp adds the skipped pages to the table's index, and a
 // tile on either border of the window gets its mask from three compares to 32 columns. A tree's
-// rows follow their parents to bits of their ancestors, kept in the warp's output buffer while the
-// tiles run. With these masks the loading warp does not wait for a sequence's last V tile: the warp
-// that is ahead of the products zeroes what is behind the end, and items inside a sequence need no
-// zeros at all, as the tokens after them are cached and finite. Measured, D = 128, 32/8 heads, pages
-// of 16, a prompt of 8192 tokens in windows of 128, 1024 and 8192 tokens: 65, 152 and 408 us (causal
-// 407); 16384 tokens of 64/8 heads in pages of 64, window 4096: 1.18 to 1.32 ms, up to 1.65 PFLOP/s.
-// Short windows: an item's start and end, 9000 cycles (the output alone 5000, half of it fetching
-// its instructions), against 1300 to 2600 a tile. Trees of 26 nodes of 8 heads to a group over 16
-// sequences of 700 to 9700 tokens: 84 us, 61% of the copy rate over the call.
+// rows follow their parents to bits of their ancestors, kept in the warp's output buffer while
+// the tiles run. With these masks the loading warp does not wait for a sequence's last V tile:
+// the warp that is ahead of the products zeroes what is behind the end, and items inside a
+// sequence need no zeros at all, as the tokens after them are cached and finite. Measured, D =
+// 128, 32/8 heads, pages of 16, a prompt of 8192 tokens in windows of 128, 1024 and 8192 tokens:
+// 65, 152 and 408 us (causal 407); 16384 tokens of 64/8 heads in pages of 64, window 4096: 1.18
+// to 1.32 ms, up to 1.65 PFLOP/s. Short windows: an item's start and end, 9000 cycles (the output
+// alone 5000, half of it fetching its instructions), against 1300 to 2600 a tile. Trees of 26
+// nodes of 8 heads to a group over 16 sequences of 700 to 9700 tokens: 84 us, 61% of the copy
+// rate over the call.
 //
 // Measured and dropped, at 16384 tokens unless said: one S for both warpgroups and P beside it,
 // scores a tile ahead (the hand-over of S bounds it); two threads per row, 640 threads (3.5 ms);

@@ -7,10 +7,10 @@
 // the scores meet in shared memory, where eight threads share a row's softmax; those of the output
 // meet once, at the item's end.
 //
-// What bounds it: reads of shared memory and four barriers a tile; an unused group of eight rows costs
-// nothing. Measured, 16 sequences in a window of 4000, 32/8 heads of 128: one row to a sequence (four
-// with its heads) 262 us, eight 288, where items of 128 rows take 798 and the bytes 79; 64 rows to
-// a sequence 543 against 801, 124 rows 1039 against 807.
+// What bounds it: reads of shared memory and four barriers a tile; an unused group of eight rows
+// costs nothing. Measured, 16 sequences in a window of 4000, 32/8 heads of 128: one row to a
+// sequence (four with its heads) 262 us, eight 288, where items of 128 rows take 798 and the
+// bytes 79; 64 rows to a sequence 543 against 801, 124 rows 1039 against 807.
 #pragma once
 
 #include "prefill_simt.cuh"
