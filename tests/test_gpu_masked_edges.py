@@ -10,7 +10,7 @@ from sparse_kv_cache_build_gb300 import binding
 
 from gpu_helpers import assert_no_device_error, f64, need_gpu
 from test_gpu_masked_attn import Masked, bush, line
-from test_gpu_prompt import Case
+from test_gpu_prompt import Case, half_step
 from test_gpu_prompt_edges import long_items
 
 pytestmark = pytest.mark.gpu
@@ -242,3 +242,36 @@ def test_calls_that_the_binding_refuses():
         with pytest.raises(ValueError):
             skv.kv_copy_pages(p.kv, pairs)
     assert_no_device_error()
+
+
+@pytest.mark.parametrize("dtype,D,G,n", [("bf16", 128, 4, 1), ("bf16", 64, 8, 300),
+                                         ("bf16", 128, 8, 3), ("fp32", 64, 2, 1),
+                                         ("fp32", 128, 2, 100)])
+@pytest.mark.parametrize("window,sinks", [(700, 5), (1, 0), (64, 130)])
+def test_windows_at_the_end_of_the_longest_tables(dtype, D, G, n, window, sinks):
+    """Rows at positions near 2^31: the same tokens in a short table give the same rows."""
+    PS, stride = 64, (2 ** 31 - 1 - 256) // 64
+    length = stride * PS - 5
+    keep = -(-sinks // PS) + (window + n) // PS + 3            # pages that rows may see
+    c = Case((n,), (PS * keep,), dtype, D, G, PS=PS, extra=0)
+    first = -(-sinks // PS)                                    # pages with sinks
+    tail = keep - first
+    # the short sequence: the sinks' pages, then the long one's last pages
+    short_len = (first + tail) * PS - 5
+    pages = c.table[0, :keep]
+    c.kv = skv.PagedKV(c.k_pool, c.v_pool, pages.view(1, -1).contiguous(),
+                       torch.tensor([short_len], dtype=torch.int32, device="cuda"))
+    ref, ref_lse = skv.kv_window_attn(c.kv, c.q, c.scale, window, sinks, cu_tokens=c.cu)
+    table = torch.full((1, stride), -1, dtype=torch.int32, device="cuda")
+    table[0, :first] = pages[:first]
+    table[0, stride - tail:] = pages[first:]
+    kv = skv.PagedKV(c.k_pool, c.v_pool, table,
+                     torch.tensor([length], dtype=torch.int32, device="cuda"))
+    out, lse = skv.kv_window_attn(kv, c.q, c.scale, window, sinks, cu_tokens=c.cu)
+    assert_no_device_error()
+    # The same scores, cut into other tiles: sums of at most 1024 terms in another order (2^-13 of
+    # them), and per side the rounding of the probabilities (bf16) and of the output.
+    most = 1.01 * c.v_pool.abs().float().max().item()
+    rel = 2.0 ** -13 + 4 * half_step(dtype)
+    assert np.abs(f64(out) - f64(ref)).max() <= rel * most
+    assert (np.abs(f64(lse) - f64(ref_lse)) <= 2.0 ** -13 + 2.0 ** -22 * np.abs(f64(ref_lse))).all()

@@ -490,3 +490,24 @@ def test_calls_on_a_stream_given_by_argument():
         assert np.array_equal(copies.cpu().numpy(), ref[2]) and left.tolist() == [ref[3]]
         k, _, ref_lens, _ = oracle.compact(k0, k0, c.table.cpu().numpy(), c.lens, c.new, kept, 16)
         assert np.array_equal(f32(c.k_pool), k) and lens.tolist() == ref_lens
+
+
+def test_copies_of_many_pages():
+    c = Case((5,), (0,), "bf16", 64, 1, 1, 16, extra=160_000)
+    stats = all_stats(c)
+    pairs = torch.randperm(c.k_pool.shape[0], device="cuda")[:140_000].to(torch.int32).view(-1, 2)
+    ref = [x.clone() for x in (c.k_pool, c.v_pool, stats)]
+    for x in ref:
+        x[pairs[:, 1].long()] = x[pairs[:, 0].long()]
+    skv.kv_copy_pages(c.kv, pairs.contiguous(), stats)
+    assert_no_device_error()
+    for x, y in zip((c.k_pool, c.v_pool, stats), ref):
+        assert torch.equal(x, y)
+
+
+def test_long_rows_of_a_table():
+    """Two sequences of a few pages in rows of a million entries, one of which moves to its end."""
+    p = Pool(100, 1 << 20)
+    p.step([40, 100], parents=[-1, -1], keep=[0, 0])
+    p.step([41, 101, 100], parents=[1, 1, 0], keep=[41, 100, 40])
+    p.check_counts()
