@@ -366,7 +366,7 @@ def _packed(kv: PagedKV, q, cu_tokens):
         raise ValueError(f"q must have shape [tokens][heads][{kv.cols}], got {tuple(q.shape)}")
     T, Hq, _ = q.shape
     stride = _rows(kv, q, "q", Hq)
-    if kv.index != torch.cuda.current_device():
+    if kv.index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {kv.k_pool.device}, which is not the current device")
     if cu_tokens is None:
         if T != kv.sequences:
@@ -434,20 +434,20 @@ def _attend(kv: PagedKV, q, cu_tokens, num_shares, out, lse, workspace, stream, 
     """What the calls that attend with packed rows share: checks, buffers, and
     call(q, stride, heads, offsets, rows, last arguments), which returns its name and status."""
     T, Hq, qs, cu = _packed(kv, q, cu_tokens)
-    D = kv.cols
+    D, dev = kv.cols, q.device
     if out is None:
-        out = _new((T, Hq, D), kv.elem, q.device, stream)
+        out = _new((T, Hq, D), kv.elem, dev, stream)
     else:
         _on_device(kv, out, "out", kv.elem, (T, Hq, D))
     if lse is None:
-        lse = _new((T, Hq), torch.float32, q.device, stream)
+        lse = _new((T, Hq), torch.float32, dev, stream)
     else:
         _on_device(kv, lse, "lse", torch.float32, (T, Hq))
     if T == 0:
         return out, lse
     if workspace is None:
         nbytes = kv_prefill_attn_workspace_size(kv, Hq, T, num_shares)
-        workspace = _new((nbytes,), torch.uint8, q.device, stream)
+        workspace = _new((nbytes,), torch.uint8, dev, stream)
     elif workspace.get_device() != kv.index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {kv.k_pool.device}")
     fn, status = call(q.data_ptr(), qs, Hq, cu, T, (
@@ -493,7 +493,7 @@ def kv_tree_attn(kv: PagedKV, q, sm_scale: float, parents, cu_tokens=None, num_s
 
 
 def _current(kv: PagedKV):
-    if kv.index != torch.cuda.current_device():
+    if kv.index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {kv.k_pool.device}, which is not the current device")
 
 
@@ -505,21 +505,24 @@ def kv_compact(kv: PagedKV, keep, keep_cnt, stats=None, cu_tokens=None, new_lens
     kv.seq_lens, which is left as it is)."""
     _current(kv)
     B = kv.sequences
-    if keep.dim() != 2 or keep.shape[1] < 1:
+    kept = keep.shape[-1] if keep.dim() == 2 else 0
+    if kept < 1:
         raise ValueError("keep must have shape [batch][at least 1]")
-    _on_device(kv, keep, "keep", torch.int32, (B, keep.shape[1]))
+    _on_device(kv, keep, "keep", torch.int32, (B, kept))
     _on_device(kv, keep_cnt, "keep_cnt", torch.int32, (B,))
     if stats is not None:
         _on_device(kv, stats, "stats", kv.elem, (kv.pages, kv.groups, 2, kv.cols))
     if cu_tokens is not None:
         _on_device(kv, cu_tokens, "cu_tokens", torch.int32, (B + 1,))
-    if new_lens is None:
-        new_lens = _new((B,), torch.int32, kv.k_pool.device, stream)
-    else:
+    if new_lens is not None:
         _on_device(kv, new_lens, "new_lens", torch.int32, (B,))
+    elif stream is None:
+        new_lens = torch.empty_like(keep_cnt)
+    else:
+        new_lens = _new((B,), torch.int32, keep_cnt.device, stream)
     status = lib().kv_compact(
         kv.ref(), None if cu_tokens is None else cu_tokens.data_ptr(), keep.data_ptr(),
-        keep.shape[1], keep_cnt.data_ptr(), None if stats is None else stats.data_ptr(),
+        kept, keep_cnt.data_ptr(), None if stats is None else stats.data_ptr(),
         new_lens.data_ptr(), _raw_stream(kv, stream))
     if status != KV_OK:
         raise KVError("kv_compact", status)
