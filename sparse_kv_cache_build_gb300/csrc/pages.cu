@@ -25,6 +25,8 @@
 // look for each other among all rows, which for thousands of them is the longest part.
 #include <cooperative_groups.h>
 
+#include <atomic>
+
 #include "packed_rows.cuh"
 
 namespace cg = cooperative_groups;
@@ -372,14 +374,22 @@ cudaError_t launch_update_pages(const kv_cache_desc& d, int32_t* refs, const int
   const PagesArgs a{refs, parents, keep_lens, new_lens, rows, window, sinks, table, copies,
                     free_left};
   const dim3 grid(ceil_div(d.page_table_stride, kRowEntries), d.batch + (parents != nullptr));
-  cudaError_t e = launch_pdl(fork_rows_kernel, grid, dim3(kRowThreads), 0, s, d, a, ctx);
+  // The rows' numbers next to the kernel's own memory may pass the 48 KB a launch has by default;
+  // raised before anything is launched, so that a call that fails has changed nothing. Set once per
+  // device; setting it twice from two threads is harmless.
+  static std::atomic<int> ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)rows * 3 * sizeof(int32_t);
-  if (smem > 48 * 1024) {
+  if (dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(alloc_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(kMaxPageRows * 3 * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev].store(1, std::memory_order_release);
   }
+  e = launch_pdl(fork_rows_kernel, grid, dim3(kRowThreads), 0, s, d, a, ctx);
+  if (e != cudaSuccess) return e;
+  const size_t smem = (size_t)rows * 3 * sizeof(int32_t);
   return launch_pdl(alloc_pages_kernel, dim3(kAllocBlocks), dim3(kAllocThreads), smem, s, d, a,
                     ctx);
 }
