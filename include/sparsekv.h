@@ -381,7 +381,9 @@ kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_
  * with the dropped tokens as candidates and none kept, or kv_build_page_stats, makes that page's
  * anew before the next append.
  * Lengths that do not fit (keep outside the old row's tokens, new below keep or above the table
- * row) are flagged (KV_DEVERR_BAD_LEN) and the row keeps its old row's tokens; a parent that is no
+ * row) are flagged (KV_DEVERR_BAD_LEN) and the row keeps its old row's tokens; so is an old row whose
+ * own length is negative or above its table row, and rows that continue it hold all its entries as
+ * they are, whatever their lengths and the window, and get no page; a parent that is no
  * old row is flagged (KV_DEVERR_BAD_SEL) and taken as -1; an entry that is neither -1 nor a page is
  * flagged (KV_DEVERR_BAD_PAGE) and taken as -1. KV_ERR_UNSUPPORTED for more than KV_PAGES_MAX_ROWS
  * rows, old or new, and for page-table rows of 2^31 - 256 tokens or more. After pages went out of a

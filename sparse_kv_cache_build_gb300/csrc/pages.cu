@@ -98,6 +98,7 @@ struct PagesArgs {
 struct RowPlan {
   int parent;      // old row, or -1
   int keep, want;  // tokens kept of it, and tokens to have room for
+  bool whole;      // the old row's entries stay as they are: its own length says nothing of them
 };
 
 // Numbers that do not fit are flagged; the row then keeps what its old row holds.
@@ -109,7 +110,17 @@ __device__ __forceinline__ RowPlan row_plan(const DevCtx& c, const kv_cache_desc
     flag(c, KV_DEVERR_BAD_SEL);
     r.parent = -1;
   }
-  const int len = r.parent >= 0 ? packed_len(c, d, r.parent) : 0;
+  r.whole = false;
+  int len = 0;
+  if (r.parent >= 0) {
+    len = d.seq_lens[r.parent];
+    r.whole = len < 0 || len > d.page_table_stride * d.page_size;
+  }
+  if (r.whole) {
+    flag(c, KV_DEVERR_BAD_LEN);
+    r.keep = r.want = 0;
+    return r;
+  }
   r.keep = a.keep_lens != nullptr ? a.keep_lens[b] : len;
   r.want = a.new_lens[b];
   if (r.keep < 0 || r.keep > len || r.want < r.keep ||
@@ -168,7 +179,7 @@ fork_rows_kernel(const __grid_constant__ kv_cache_desc d, const __grid_constant_
         const RowPlan r = row_plan(ctx, d, a, b);
         const int PS = d.page_size;
         list[atomicAdd(&found, 1)] =
-            Kept{b, pages_of(r.keep, PS), pages_of(a.sinks, PS),
+            Kept{b, r.whole ? stride : pages_of(r.keep, PS), pages_of(a.sinks, PS),
                  a.window > 0 ? max(0, r.keep - a.window + 1) / PS : 0};
       }
     }
