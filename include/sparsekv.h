@@ -328,9 +328,9 @@ kv_status kv_tree_attn(const kv_cache_desc* cache, const void* q, int64_t q_stri
  * hold candidates or what is kept, s_b / page_size up to the last kept token's, become those of
  * kv_build_page_stats at the new length (stats may be NULL: they are left alone; so are those of a
  * sequence without candidates). Tokens before s_b and slots behind the last kept token stay as they
- * are. new_lens: device int32[batch], becomes s_b + keep_cnt[b]; it overlaps no input and is not
- * seq_lens, which the call leaves as it is (the caches of all layers take the same lists), and which
- * the caller replaces when all are done.
+ * are. new_lens: device int32[batch], becomes s_b + keep_cnt[b]; it overlaps neither the lists nor the
+ * page table nor seq_lens (KV_ERR_INVALID_ARG), which the call leaves as it is (the caches of all
+ * layers take the same lists), and which the caller replaces when all are done.
  * FP8 statistics are not kept: kv_build_page_stats_fp8 makes them anew.
  * Pages from s_b on must not be shared with another sequence. Indices that do not rise or are
  * outside the candidates are flagged (KV_DEVERR_BAD_SEL) and not moved; the sequence's tokens from

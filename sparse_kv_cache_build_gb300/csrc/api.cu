@@ -80,6 +80,13 @@ kv_status ctx_for_call(DevCtx* ctx, DeviceState** st_out = nullptr) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two arrays of 4-byte words share none; a NULL array has none.
+bool words_apart(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a == nullptr || b == nullptr || a0 + 4 * (uintptr_t)na <= b0 ||
+         b0 + 4 * (uintptr_t)nb <= a0;
+}
+
 kv_status check_desc(const kv_cache_desc* d) {
   if (d == nullptr || d->k_pool == nullptr || d->v_pool == nullptr ||
       d->page_table == nullptr || d->seq_lens == nullptr)
@@ -484,13 +491,18 @@ kv_status kv_compact(const kv_cache_desc* cache, const int32_t* cu_tokens, const
                      cudaStream_t stream) {
   kv_status r = check_desc(cache);
   if (r != KV_OK) return r;
-  if (keep == nullptr || keep_stride < 1 || keep_cnt == nullptr || new_lens == nullptr ||
-      new_lens == cache->seq_lens)
+  if (keep == nullptr || keep_stride < 1 || keep_cnt == nullptr || new_lens == nullptr)
     return KV_ERR_INVALID_ARG;
   if (!aligned16(stats)) return KV_ERR_MISALIGNED;
   // tokens are counted in 32 bits, up to a batch of a block past the last
   if ((int64_t)cache->page_table_stride * cache->page_size > INT32_MAX - 4096)
     return KV_ERR_UNSUPPORTED;
+  // every block reads the lists and lengths, while the first ones write the new lengths
+  const int64_t B = cache->batch;
+  auto apart = [&](const int32_t* in, int64_t n) { return words_apart(new_lens, B, in, n); };
+  if (!apart(cache->seq_lens, B) || !apart(keep_cnt, B) || !apart(keep, B * keep_stride) ||
+      !apart(cu_tokens, B + 1) || !apart(cache->page_table, B * cache->page_table_stride))
+    return KV_ERR_INVALID_ARG;
   DevCtx ctx;
   DeviceState* st = nullptr;
   if ((r = ctx_for_call(&ctx, &st)) != KV_OK) return r;
