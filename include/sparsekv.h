@@ -380,6 +380,8 @@ kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_
  * Statistics are not touched: where keep_lens drops tokens of a page that stays, kv_compact
  * with the dropped tokens as candidates and none kept, or kv_build_page_stats, makes that page's
  * anew before the next append.
+ * refs, table, copies and free_left overlap neither each other nor an input, but for the table in
+ * place (KV_ERR_INVALID_ARG).
  * Lengths that do not fit (keep outside the old row's tokens, new below keep or above the table
  * row) are flagged (KV_DEVERR_BAD_LEN) and the row keeps its old row's tokens; so is an old row whose
  * own length is negative or above its table row, and rows that continue it hold all its entries as

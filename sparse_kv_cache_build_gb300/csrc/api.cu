@@ -539,12 +539,23 @@ kv_status kv_update_pages(const kv_cache_desc* cache, int32_t* refs, const int32
     return KV_ERR_UNSUPPORTED;                     // tokens are counted in 32 bits
   if (!aligned16(refs)) return KV_ERR_MISALIGNED;
   // in place only where a row continues itself
-  const int64_t stride = cache->page_table_stride;
-  const uintptr_t in0 = reinterpret_cast<uintptr_t>(cache->page_table);
-  const uintptr_t out0 = reinterpret_cast<uintptr_t>(table);
-  const bool apart = out0 + (uintptr_t)rows * stride * sizeof(int32_t) <= in0 ||
-                     in0 + (uintptr_t)cache->batch * stride * sizeof(int32_t) <= out0;
-  if (!apart && (parents != nullptr || in0 != out0)) return KV_ERR_INVALID_ARG;
+  const int64_t stride = cache->page_table_stride, B = cache->batch;
+  if (!words_apart(table, rows * stride, cache->page_table, B * stride) &&
+      (parents != nullptr || table != cache->page_table))
+    return KV_ERR_INVALID_ARG;
+  // Blocks of both launches read the lists while others write; outputs are the call's alone.
+  const struct { const int32_t* p; int64_t n; } out[] = {
+      {table, rows * stride}, {refs, cache->num_phys_pages}, {copies, 2 * (int64_t)rows},
+      {free_left, 1}}, in[] = {
+      {parents, rows}, {keep_lens, rows}, {new_lens, rows}, {cache->seq_lens, B}};
+  for (int i = 0; i < 4; ++i) {
+    if (i > 0 && !words_apart(out[i].p, out[i].n, cache->page_table, B * stride))
+      return KV_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (!words_apart(out[i].p, out[i].n, out[k].p, out[k].n)) return KV_ERR_INVALID_ARG;
+    for (const auto& x : in)
+      if (!words_apart(out[i].p, out[i].n, x.p, x.n)) return KV_ERR_INVALID_ARG;
+  }
   DevCtx ctx;
   if ((r = ctx_for_call(&ctx)) != KV_OK) return r;
   return from_cuda(launch_update_pages(*cache, refs, parents, rows, keep_lens, new_lens, window,
