@@ -468,13 +468,19 @@ def kv_prefill_attn(kv: PagedKV, q, sm_scale: float, cu_tokens=None, num_shares:
     return _attend(kv, q, cu_tokens, num_shares, out, lse, workspace, stream, call)
 
 
+def _span(tokens):
+    """A window or a number of sinks as an int32: beyond 32 bits (where ctypes would keep the lower
+    ones) it reaches as far as the largest, and below zero it is refused as -1 is."""
+    return max(-1, min(int(tokens), 2 ** 31 - 1))
+
+
 def kv_window_attn(kv: PagedKV, q, sm_scale: float, window: int, sinks: int = 0, cu_tokens=None,
                    num_shares: int = 0, out=None, lse=None, workspace=None, stream=None):
     """kv_prefill_attn where a row sees the last `window` tokens up to itself and the sequence's
     first `sinks` ones: (out, lse). Pages that no row sees may be unmapped."""
     def call(ptr, stride, Hq, cu, T, last):
         return "kv_window_attn", lib().kv_window_attn(
-            kv.ref(), ptr, stride, Hq, cu, T, float(sm_scale), int(window), int(sinks), *last)
+            kv.ref(), ptr, stride, Hq, cu, T, float(sm_scale), _span(window), _span(sinks), *last)
     return _attend(kv, q, cu_tokens, num_shares, out, lse, workspace, stream, call)
 
 
@@ -580,8 +586,8 @@ def kv_update_pages(kv: PagedKV, refs, new_lens, keep_lens=None, parents=None, w
     else:
         _on_device(kv, free_left, "free_left", torch.int32, (1,))
     status = lib().kv_update_pages(
-        kv.ref(), refs.data_ptr(), parent, rows, keep, new_lens.data_ptr(), int(window),
-        int(sinks), table.data_ptr(), copies.data_ptr(), free_left.data_ptr(),
+        kv.ref(), refs.data_ptr(), parent, rows, keep, new_lens.data_ptr(), _span(window),
+        _span(sinks), table.data_ptr(), copies.data_ptr(), free_left.data_ptr(),
         _raw_stream(kv, stream))
     if status != KV_OK:
         raise KVError("kv_update_pages", status)
