@@ -1,6 +1,7 @@
 """Page tables over the whole range of rows, and rows whose length is none."""
 
 import os
+import random
 import subprocess
 import sys
 
@@ -77,3 +78,37 @@ def test_rows_of_a_length_that_does_not_fit_keep_their_pages(bad, parents, given
     if window == 0:
         assert np.array_equal(got, ref[0]) and p.refs.tolist() == ref[1]
         assert np.array_equal(copies.cpu().numpy(), ref[2]) and left.tolist() == [ref[3]]
+
+
+@pytest.mark.parametrize("pages,stride,PS,seed", [(1000, 30, 16, 1), (5003, 130, 64, 2),
+                                                  (129, 9, 32, 3), (70001, 1100, 16, 4)])
+def test_random_steps_that_fork_drop_and_slide(pages, stride, PS, seed):
+    """Steps that the pool has room for, but for a few, and of every kind."""
+    rng = random.Random(seed)
+    p = Pool(pages, stride, PS)
+    p.step([min(stride * PS, 20 * PS) // 2] * 4, parents=[-1] * 4, keep=[0] * 4)
+    kinds = {"refused": 0, "copied": 0, "dropped": 0, "slid": 0, "freed": 0}
+    for n in range(30):
+        grow = n % 3 != 2                            # every third step keeps the rows as they are
+        rows = rng.choice((2, 5, 9)) if grow else len(p.lens)
+        parents = [rng.randrange(len(p.lens)) for _ in range(rows)] if grow else None
+        if grow and n % 5 == 0:
+            parents[-1] = -1
+        old = p.lens if parents is None else [p.lens[q] if q >= 0 else 0 for q in parents]
+        keep = [max(0, x - rng.choice((0, 0, 1, 3, PS))) for x in old]
+        most = min(stride * PS, max(PS, pages * PS // (2 * rows)))
+        want = [min(stride * PS, max(k, min(most, k + rng.choice((1, 2, 7, 2 * PS))))) for k in keep]
+        window, sinks = (3 * PS, 4) if n % 4 == 3 else (0, 0)
+        args = (p.lens, p.refs.tolist(), rows, parents, keep, want, PS)
+        out, _, copies, left = oracle.update_pages(p.table, *args, window, sinks)
+        bare, *_ = oracle.update_pages(p.table, *args)
+        kinds["refused"] += left < 0
+        kinds["copied"] += bool((copies >= 0).any())
+        kinds["dropped"] += any(-(-k // PS) < -(-x // PS) for k, x in zip(keep, old))
+        kinds["slid"] += left >= 0 and bool(((out < 0) & (bare >= 0)).any())
+        kinds["freed"] += parents is not None and len(set(parents)) < len(p.lens)
+        p.step(want, keep=keep, parents=parents, window=window, sinks=sinks,
+               flags=32 if left < 0 else 0)
+        p.check_counts()
+    assert kinds["refused"] <= 5, kinds
+    assert min(kinds[k] for k in ("copied", "dropped", "slid", "freed")) >= 3, kinds
