@@ -306,7 +306,8 @@ kv_status kv_window_attn(const kv_cache_desc* cache, const void* q, int64_t q_st
  * index among its sequence's rows (0 for the first) of the node it continues, which comes before
  * it, or -1 where it continues the cached tokens. A row sees every earlier token, its ancestors and
  * itself. A parent that is neither is flagged (KV_DEVERR_BAD_SEL) and taken as -1. Sequences of
- * more than KV_TREE_MAX_NODES rows are flagged (KV_DEVERR_BAD_LEN) and left out. Arguments,
+ * more than KV_TREE_MAX_NODES rows are flagged (KV_DEVERR_BAD_LEN) and left out. Every earlier page
+ * is read: a sequence whose pages went out of a window has kv_window_attn only. Arguments,
  * workspace (kv_prefill_attn_workspace_size), rounding, flags and limits are otherwise
  * kv_prefill_attn's; a tree that is one line gives its results up to the rounding of its sums.
  */
@@ -348,7 +349,8 @@ kv_status kv_compact(const kv_cache_desc* cache, const int32_t* cu_tokens, const
  * stats, if not NULL) are copied to page pairs[i][1]. pairs: device int32 [n][2], 8-byte aligned;
  * a pair with a negative number copies nothing, one beyond the pool is flagged
  * (KV_DEVERR_BAD_PAGE) and copies nothing. A page that is written must not occur a second time in
- * the list. stats: device, of the cache dtype as in kv_build_page_stats.
+ * the list. stats: device, of the cache dtype as in kv_build_page_stats. FP8 statistics are not
+ * copied: kv_build_page_stats_fp8 makes them anew.
  */
 kv_status kv_copy_pages(const kv_cache_desc* cache, const int32_t* pairs, int32_t n, void* stats,
                         cudaStream_t stream);
@@ -817,8 +819,9 @@ kv_status kv_check_device_errors(cudaStream_t stream, int32_t* flags);
  * device-side wait on an asynchronous copy (default 2e9). After it runs out the kernel
  * flags KV_DEVERR_TIMEOUT, drains its own copies (again bounded, by a time of its own where the
  * limit is short) and returns. The GPU looks at the time only once or twice in some microseconds,
- * so a wait may last longer than a short limit. Where kv_prefill_attn waits for its own products
- * over a row tile's keys, the limit counts once for every 128 keys.
+ * so a wait may last longer than a short limit. Where kv_prefill_attn, kv_window_attn and
+ * kv_tree_attn wait for their own products over a row tile's keys, the limit counts once for every
+ * 128 keys.
  */
 kv_status kv_set_wait_limit_ns(uint64_t limit_ns);
 

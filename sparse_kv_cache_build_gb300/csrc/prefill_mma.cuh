@@ -1011,6 +1011,7 @@ cudaError_t launch_prefill_mma(const kv_cache_desc& d, const PackedRows& pr,
   // Measured against the instance of few rows, 32 sequences of 32/8 heads of 128 in a window of
   // 1000: 4, 8, 16 and 32 rows 34, 35, 37 and 41 us (41 to 42); 16 heads of 64: 45, 46, 55 and 73
   // (58, 60, 60 and 61), trees over 6000 tokens 101, 105, 127 and 167 (104, 106, 111 and 114).
+  // Smaller batches were not measured, and the mean counts sequences without rows too.
   if constexpr (M != Mask::kCausal) {
     if (few && (int64_t)pr.total * a.G * 8 <= (int64_t)d.head_dim * d.batch)
       return launch_prefill_few<M>(d, pr, a, ctx, s);

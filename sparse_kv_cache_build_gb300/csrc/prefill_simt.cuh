@@ -1,4 +1,4 @@
-// Causal prompt attention for fp32 caches, on the CUDA cores.
+// Attention of packed rows for fp32 caches, on the CUDA cores.
 //
 // A block takes 128 rows of an item and walks their keys 64 at a time, with the running maximum
 // and sum of the softmax per row; it walks its share of the batch's items (prefill.cuh).
@@ -22,8 +22,9 @@
 //
 // Every item computes 128 rows, however few it has, so single tokens cost as much as rows for 128:
 // 16 single tokens over 4096 each take 131 us at 8/2 heads of 64 and 846 at 32/8 heads of 128
-// (the bytes: 10 and 79), one over 32768 422 (40). kv_decode_step reads them at 18, 99 and 46, and
-// is the call for float32 caches there; a form for few rows has not been built.
+// (the bytes: 10 and 79), one over 32768 422 (40). Windows and trees of few rows have items of 32
+// in a kernel of their own (prefill_simt_few.cuh). With the causal mask there is none: kv_decode_step
+// reads those single tokens at 18, 99 and 46, and is the call for float32 caches there.
 #pragma once
 
 #include "prefill.cuh"
