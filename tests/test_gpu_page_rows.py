@@ -26,8 +26,8 @@ def _gpu():
 
 ROWS = """
 from test_gpu_pages import Pool
-for rows in (4061, 4062, 4096, 4097):
-    p = Pool(20000, 4)
+for rows in (4061, 4062, 4096, 4097, 16384):
+    p = Pool(5 * rows, 4)
     p.step([20, 33, 48], parents=[-1] * 3, keep=[0] * 3)
     held = [(20, 33, 48)[i % 3] for i in range(rows)]
     p.step([n + i % 2 for i, n in enumerate(held)], parents=[i % 3 for i in range(rows)], keep=held)
